@@ -199,7 +199,7 @@ def prepare(case, seed):
         s["live"] = live
         if case["op"] == "int8_forward":
             moe = MoE(E, case["H"], case["F"], k, "int8")
-            moe.load_weights_int8(s["w1"], s["s1"], s["w2"], s["s2"])
+            moe.load_quantized(s["w1"], s["s1"], s["w2"], s["s2"])
             s["out"] = torch.empty((cap, case["H"]), dtype=torch.bfloat16, device=DEV)
             s["call"] = moe.bind_forward(s["x"], s["ids"], s["probs"], live, s["out"], moe.new_workspace(cap),
                                          combine="bf16")

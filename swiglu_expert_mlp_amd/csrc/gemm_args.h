@@ -58,9 +58,10 @@ __device__ __forceinline__ float fc1_row_prob(const float* row_prob, const int32
     return row_prob[perm_src[row]];
 }
 
-// bf16 operands.
+// Operands of the kernels whose K steps are 16-bit units: bf16 elements, or
+// pairs of int8 codes (K then counts pairs: half the padded code row).
 struct GemmArgs {
-    const uint16_t* A;         // FC1: x [T_cap][H]; FC2: hbuf [rows][F]
+    const uint16_t* A;         // FC1: x [T_cap][H]; FC2: hbuf [rows][F] (int8: code rows)
     const uint16_t* W;         // FC1: packed W1 [E][2F][H]; FC2: W2 [E][H][F]
     const int32_t* perm_src;   // FC1: grouped row -> route (t * k + j)
     const int2* tiles;         // (expert, first row) per 64-row M tile
@@ -90,6 +91,10 @@ struct GemmArgs {
     const float* fin_prob;     // canonical probabilities, or null (every p is 1)
     void* fin_out;             // the forward's output
     int fin_mode;              // 0: fp32 chain, 1: bf16 of it, 2: rows
+    // int8 operands: fp32 scale of each activation row (FC1: of token t; FC2: of
+    // the grouped row) and of each weight row [E][N] (FC1: in packed row order)
+    const float* a_scale;
+    const float* w_scale;
 };
 
 // MXFP8 operands: E4M3 codes with one E8M0 scale byte per 32 elements of K.

@@ -32,14 +32,14 @@ __global__ void __launch_bounds__(512, 1) gemm_bf16_small_kernel(GemmArgs g)
     const int* te0 = (const int*)(g.tiles + min(xcd_first_tile() / small_col_tiles(g), g.max_tiles - 1));
     const int e0 = ld_const(te0), row00 = ld_const(te0 + 1);
     asm volatile("" : : "s"(n_big), "s"(n_small), "s"(multi), "s"(e0), "s"(row00));   // one round trip
-    if (multi) small_tiles<FC1, PROB, 0, 0>(g, smem, n_small, n_big, e0, row00);
-    else small_tiles<FC1, PROB, 0, kNonTemporal>(g, smem, n_small, n_big, e0, row00);
+    if (multi) small_tiles<OpBf16, FC1, PROB, 0, 0>(g, smem, n_small, n_big, e0, row00);
+    else small_tiles<OpBf16, FC1, PROB, 0, kNonTemporal>(g, smem, n_small, n_big, e0, row00);
 }
 
 template <bool FC1, bool PROB>
 __global__ void __launch_bounds__(512, 1) gemm_bf16_big_kernel(GemmArgs g)
 {
-    big_tiles<FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
+    big_tiles<OpBf16, FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
 }
 
 // The single-launch FFN: FC1 then FC2 in one persistent launch of the 64-row
@@ -63,12 +63,12 @@ __global__ void __launch_bounds__(512, 1) gemm_bf16_fused_kernel(GemmArgs g1, Ge
     asm volatile("" : : "s"(n_big), "s"(n_small), "s"(multi), "s"(e0), "s"(row00));
     const int* te1 = (const int*)(g2.tiles + min(xcd_first_tile() / small_col_tiles(g2), g2.max_tiles - 1));
     if (multi) {
-        small_tiles<true, PROB, 1, 0>(g1, smem, n_small, n_big, e0, row00);
-        small_tiles<false, false, F2, 0>(g2, smem, n_small, n_big, ld_const(te1), ld_const(te1 + 1),
+        small_tiles<OpBf16, true, PROB, 1, 0>(g1, smem, n_small, n_big, e0, row00);
+        small_tiles<OpBf16, false, false, F2, 0>(g2, smem, n_small, n_big, ld_const(te1), ld_const(te1 + 1),
                                          small_col_tiles(g1), &fin_lds);
     } else {
-        small_tiles<true, PROB, 1, kNonTemporal>(g1, smem, n_small, n_big, e0, row00);
-        small_tiles<false, false, F2, kNonTemporal>(g2, smem, n_small, n_big, ld_const(te1),
+        small_tiles<OpBf16, true, PROB, 1, kNonTemporal>(g1, smem, n_small, n_big, e0, row00);
+        small_tiles<OpBf16, false, false, F2, kNonTemporal>(g2, smem, n_small, n_big, ld_const(te1),
                                                     ld_const(te1 + 1), small_col_tiles(g1), &fin_lds);
     }
 }

@@ -6,6 +6,12 @@
 // element is  acc = 0; for k0 = 0, 16, 32, ... :
 // acc = MFMA_32x32x16_bf16(A[row, k0:k0+16], B[col, k0:k0+16], acc).
 //
+// The tile loops are templates of the operand type (OpBf16 here, OpInt8 in
+// gemm_int8.hip).  The int8 MFMA 32x32x32 takes the same 16 bytes per lane and
+// the same accumulator layout as the bf16 32x32x16 one and runs in the same
+// number of cycles, so with a pair of int8 codes in place of a bf16 element
+// every load, layout and schedule below holds for both, at half the K units.
+//
 // Decomposition: one workgroup of 8 waves per CU (two per SIMD, so that one
 // wave's barrier and memory waits overlap the other's matrix work), a 256 x
 // 256 output tile per workgroup, each wave a 128 x 64 part (4 x 2 MFMA blocks
@@ -45,6 +51,7 @@
 namespace moe {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 
@@ -56,9 +63,62 @@ __device__ __forceinline__ void big_load_block(const void* gsrc, void* lds_dst)
     __builtin_amdgcn_global_load_lds(gsrc, (lds_void_t*)lds_dst, 16, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8 big_frag(const char* p)
+// Operand types: a lane's 16-byte MFMA fragment, the accumulator, the
+// instruction, and whether the results carry a scale per row and column.
+struct OpBf16 {
+    typedef bf16x8 Frag;
+    typedef f32x16 Acc;
+    typedef float AccElem;
+    static constexpr bool kScaled = false;
+    static __device__ __forceinline__ Acc mfma(Frag a, Frag b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+struct OpInt8 {
+    typedef i32x4 Frag;
+    typedef i32x16 Acc;
+    typedef int AccElem;
+    static constexpr bool kScaled = true;
+    static __device__ __forceinline__ Acc mfma(Frag a, Frag b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+    }
+};
+
+template <typename Op>
+__device__ __forceinline__ typename Op::Frag big_frag(const char* p)
 {
-    return __builtin_bit_cast(bf16x8, *(const uint4*)p);
+    return __builtin_bit_cast(typename Op::Frag, *(const uint4*)p);
+}
+
+// An accumulator as fp32: the column's scale first (a bf16 accumulator as it
+// is), then, by scale_row, the row's.  Every int8 epilogue uses this order, so
+// the tile designs agree bit for bit.
+template <typename Op>
+__device__ __forceinline__ float scale_col(typename Op::AccElem acc, float col)
+{
+    if constexpr (Op::kScaled) return (float)acc * col;
+    else return acc;
+}
+template <typename Op>
+__device__ __forceinline__ float scale_row(float v, float row)
+{
+    if constexpr (Op::kScaled) return v * row;
+    else return v;
+}
+
+// A float of another lane (4 * lane in addr)
+__device__ __forceinline__ float lane_value(int addr, float v)
+{
+    return __int_as_float(__builtin_amdgcn_ds_bpermute(addr, __float_as_int(v)));
+}
+
+// The scale of a grouped row's activations
+template <bool FC1>
+__device__ __forceinline__ float act_scale(const GemmArgs& g, int row)
+{
+    return g.a_scale[FC1 ? g.perm_src[row] / g.topk : row];
 }
 
 // chunk permutation of a 64-byte activation row in the 64-row tiles
@@ -121,8 +181,9 @@ __device__ __forceinline__ void big_issue(const BigSrc& t, char* st, int s)
                 t.woff[i] + t.wstep * (2 * s + h), 0, WPOL);
 }
 
+template <typename Op>
 struct BigFrag {
-    bf16x8 a[4], b[2];
+    typename Op::Frag a[4], b[2];
 };
 
 // Lane offsets of the fragments of sub-step q (K 16 q .. 16 q + 15 of a
@@ -136,23 +197,24 @@ struct BigLanes {
 
 // (B first: the MFMAs run row block by row block, so each A fragment is needed
 // one MFMA pair after the one before)
-template <int Q>
-__device__ __forceinline__ void big_read(const char* st, const BigLanes& ln, int wm, int wn, BigFrag& f)
+template <typename Op, int Q>
+__device__ __forceinline__ void big_read(const char* st, const BigLanes& ln, int wm, int wn, BigFrag<Op>& f)
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        f.b[j] = big_frag(st + kBigWOff + (Q >> 1) * 16384 + (4 * wn + 2 * j) * 1024 + ln.b[Q & 1]);
+        f.b[j] = big_frag<Op>(st + kBigWOff + (Q >> 1) * 16384 + (4 * wn + 2 * j) * 1024 + ln.b[Q & 1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f.a[i] = big_frag(st + (128 * wm + 32 * i) * 128 + ln.a[Q]);
+    for (int i = 0; i < 4; ++i) f.a[i] = big_frag<Op>(st + (128 * wm + 32 * i) * 128 + ln.a[Q]);
 }
 
-__device__ __forceinline__ void big_mma(f32x16 (&acc)[4][2], const BigFrag& f)
+template <typename Op>
+__device__ __forceinline__ void big_mma(typename Op::Acc (&acc)[4][2], const BigFrag<Op>& f)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = Op::mfma(f.a[i], f.b[j], acc[i][j]);
 }
 
 // One sub-step: the MFMAs of the fragments in cur, with the 6 fragment reads
@@ -160,12 +222,12 @@ __device__ __forceinline__ void big_mma(f32x16 (&acc)[4][2], const BigFrag& f)
 // between them, one read after each of the first 6 MFMAs; nothing moves across
 // the phase's ends (the compiler otherwise bunched the reads, waited for each
 // right away, and sank the stage's direct loads down to the next wait).
-template <int Q>
-__device__ __forceinline__ void big_phase(f32x16 (&acc)[4][2], const BigFrag& cur, const char* st,
-                                          const BigLanes& ln, int wm, int wn, BigFrag& nxt)
+template <typename Op, int Q>
+__device__ __forceinline__ void big_phase(typename Op::Acc (&acc)[4][2], const BigFrag<Op>& cur, const char* st,
+                                          const BigLanes& ln, int wm, int wn, BigFrag<Op>& nxt)
 {
-    big_read<Q>(st, ln, wm, wn, nxt);
-    big_mma(acc, cur);
+    big_read<Op, Q>(st, ln, wm, wn, nxt);
+    big_mma<Op>(acc, cur);
 #pragma unroll
     for (int k = 0; k < 6; ++k) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
@@ -182,25 +244,25 @@ __device__ __forceinline__ void big_phase(f32x16 (&acc)[4][2], const BigFrag& cu
 // issued on one path only made the compiler wait on all loads in flight before
 // later fragment reads): where no stage is left to load, the last stage is
 // loaded once more into s0, which no later fragment read of the tile uses.
-template <int AFTER, int WPOL>
+template <typename Op, int AFTER, int WPOL>
 __device__ __forceinline__ void big_kloop(const BigSrc& t, char* s0, char* s1, const BigLanes& ln, int wm,
-                                          int wn, f32x16 (&acc)[4][2])
+                                          int wn, typename Op::Acc (&acc)[4][2])
 {
     static_assert(AFTER + kBigLoads <= 63, "vmcnt bound");
     const int nst = t.nst;                           // >= 2
-    BigFrag x, y;
+    BigFrag<Op> x, y;
     // both stages landed (waiting for stage 0 alone made the compiler add a
     // wait for everything in flight before the first fragment reads)
     BIG_WAIT_VMCNT(AFTER);
     __builtin_amdgcn_s_barrier();
-    big_read<0>(s0, ln, wm, wn, x);
+    big_read<Op, 0>(s0, ln, wm, wn, x);
 
     // sub-steps 0 .. 2 of the stage in cur (sub-step 0's fragments in x),
     // reading sub-steps 1 .. 3 (the last into y)
     auto body = [&](const char* cur) {
-        big_phase<1>(acc, x, cur, ln, wm, wn, y);
-        big_phase<2>(acc, y, cur, ln, wm, wn, x);
-        big_phase<3>(acc, x, cur, ln, wm, wn, y);
+        big_phase<Op, 1>(acc, x, cur, ln, wm, wn, y);
+        big_phase<Op, 2>(acc, y, cur, ln, wm, wn, x);
+        big_phase<Op, 3>(acc, x, cur, ln, wm, wn, y);
     };
     // a stage boundary: this wave's loads of the next stage landed (N: the
     // vector-memory operations issued after them) and its reads of the current
@@ -217,7 +279,7 @@ __device__ __forceinline__ void big_kloop(const BigSrc& t, char* s0, char* s1, c
     // sub-step 3 of the stage before (in y) with sub-step 0 of the stage in nxt read
     auto into = [&](const char* nxt) {
         __builtin_amdgcn_sched_barrier(0);
-        big_phase<0>(acc, y, nxt, ln, wm, wn, x);
+        big_phase<Op, 0>(acc, y, nxt, ln, wm, wn, x);
     };
     using Now = std::integral_constant<int, 0>;
     // stage 0 (stage 1 has landed too)
@@ -243,13 +305,13 @@ __device__ __forceinline__ void big_kloop(const BigSrc& t, char* s0, char* s1, c
         into(s0);
         body(s0);
     }
-    big_mma(acc, y);                                 // the last sub-step
+    big_mma<Op>(acc, y);                               // the last sub-step
 }
 
 // The 256-row tile loop of one 8-wave workgroup (one workgroup per CU).
 // n_mt: the number of 256-row M tiles.  Requires K % 64 == 0 and K >= 128
 // (the launch sends other shapes to the 64-row kernel).
-template <bool FC1, bool PROB>
+template <typename Op, bool FC1, bool PROB>
 __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
 {
     __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
@@ -345,19 +407,19 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
     char* const ep = lds_x + wid * kBigEpi;         // this wave's epilogue region
     while (true) {
         const int row0 = pos.row0, rows = pos.rows, n0 = pos.n0;
-        f32x16 acc[4][2];
+        typename Op::Acc acc[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 
         // every wave runs the same K loop, also one whose 128 rows all lie past
         // the tile's rows (its results are dropped by the store descriptor): a
         // second, load-only loop for such waves made the compiler wait for all
         // loads and stores in flight at every tile's first fragment reads
-        big_kloop<kStores, kWPol>(t, lds0, lds1, ln, wm, wn, acc);
+        big_kloop<Op, kStores, kWPol>(t, lds0, lds1, ln, wm, wn, acc);
 
         // every wave finished reading the stages: the next tile's two stages go
         // out before this tile's epilogue (which has LDS of its own), so they
@@ -379,11 +441,23 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
             if (r0 < rows) pr0 = g.row_prob[g.perm_src[row0 + r0]];
             if (r1 < rows) pr1 = g.row_prob[g.perm_src[row0 + r1]];
         }
+        // int8: the wave's 128 row scales (two a lane) and the lane's two column
+        // scales, fetched while the next tile is located and landed before its
+        // loads go out (no plain load is in flight among those)
+        float rs0 = 1.0f, rs1 = 1.0f, cs0 = 1.0f, cs1 = 1.0f;
+        if constexpr (Op::kScaled) {
+            rs0 = act_scale<FC1>(g, row0 + min(128 * wm + lane, rows - 1));
+            rs1 = act_scale<FC1>(g, row0 + min(128 * wm + lane + 64, rows - 1));
+            const float* wsc = g.w_scale + (int64_t)pos.e * g.N + (lane & 31);
+            cs0 = wsc[min(n0 + 64 * wn, g.N - 32)];
+            cs1 = wsc[min(n0 + 64 * wn + 32, g.N - 32)];
+        }
         TilePos npos = pos;
         if (more) {
             npos = locate(next);
             sources(npos);
         }
+        if constexpr (Op::kScaled) asm volatile("" : : "v"(rs0), "v"(rs1), "v"(cs0), "v"(cs1));
         big_issue<kWPol>(t, lds0, 0);
         big_issue<kWPol>(t, lds1, 1);
 
@@ -419,7 +493,9 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int rr = 8 * (v >> 2) + 4 * hi + (v & 3);
-                    float h = swiglu_f32(acc[i][0][v], acc[i][1][v]);
+                    const float rs = Op::kScaled ? lane_value(4 * (32 * (i & 1) + rr), i < 2 ? rs0 : rs1) : 1.0f;
+                    float h = swiglu_f32(scale_row<Op>(scale_col<Op>(acc[i][0][v], cs0), rs),
+                                         scale_row<Op>(scale_col<Op>(acc[i][1][v], cs1), rs));
                     if constexpr (PROB) h *= pw[32 * i + rr];
                     // (the offset through an opaque copy: a 16-bit LDS store whose
                     // constant part the compiler folds into the instruction made
@@ -454,14 +530,20 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
                         for (int v = 8 * hv; v < 8 * hv + 8; ++v) {
                             const int lr = 8 * ((v >> 2) & 1) + 4 * hi + (v & 3);
                             *(float*)(ep + ((lr * 256 + 4 * (32 * j + c32)) ^ (((lr >> 2) & 1) << 7))) =
-                                acc[i][j][v];
+                                scale_col<Op>(acc[i][j][v], j ? cs1 : cs0);
                         }
                     static_assert(big_stores<false>() == 4 * 2 * 4, "4 row blocks x 2 halves x 4 stores");
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int lr = (elane >> 4) + 4 * k;
-                        const u32x4_t val =
+                        u32x4_t val =
                             *(const u32x4_t*)(ep + ((lr * 256 + 16 * c) ^ (((lr >> 2) & 1) << 7)));
+                        if constexpr (Op::kScaled) {
+                            const float rs = lane_value(4 * (32 * (i & 1) + 16 * hv + lr), i < 2 ? rs0 : rs1);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                val[q] = __float_as_uint(scale_row<Op>(__uint_as_float(val[q]), rs));
+                        }
                         const int off = col < g.N ? ((128 * wm + 32 * i + 16 * hv + lr) * g.N + col) * 4
                                                   : 0x7ffffff0;
                         __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);

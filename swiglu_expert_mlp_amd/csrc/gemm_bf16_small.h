@@ -12,7 +12,9 @@
 // acc = MFMA_32x32x16_bf16(A[row, k0:k0+16], B[col, k0:k0+16], acc), with the
 // same instruction and the same K order whatever the tile, the row's position
 // inside its tile, or the number of rows of the launch.  Nothing splits K.
-// The 256-row tiles (gemm_bf16_big.h) follow the same contract.
+// The 256-row tiles (gemm_bf16_big.h) follow the same contract.  As there, the
+// tile loop is a template of the operand type (OpBf16, or OpInt8 with pairs of
+// int8 codes as the 16-bit units).
 //
 // These tiles stream the expert weights (each weight byte serves at most 64
 // rows).  A workgroup of 8 waves takes a tile of up to 64 rows x 512 columns,
@@ -244,7 +246,7 @@ __device__ __forceinline__ void small_finalize(const GemmArgs& g, SmallFinLds* f
 // WPOL: the cache policy of the weight stream (kNonTemporal when every
 // expert's rows fit one 64-row tile, else the default; the caller reads which
 // from the header).
-template <bool FC1, bool PROB, int FUSE, int WPOL>
+template <typename Op, bool FC1, bool PROB, int FUSE, int WPOL>
 __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n_small, int n_big,
                                             int e0, int row00, int need = 0, SmallFinLds* fin_lds = nullptr)
 {
@@ -359,13 +361,13 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
         };
         auto issue = [&](int s) { issue_a(s); issue_b(s); };
 
-        f32x16 acc[2][2];
+        typename Op::Acc acc[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 
         // a step's loads stay contiguous in issue order (step 0: weights, then rows)
         issue_a(0);
@@ -380,15 +382,15 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
             if (has_cols) {
                 const char* st = smem + (s % kSmallRing) * kSmallStage;
                 // B blocks 4 wid + 2 j and + 1 hold the wave's 32-column block j
-                bf16x8 a[2][2], b[2][2];
+                typename Op::Frag a[2][2], b[2][2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        b[q][j] = big_frag(st + (4 + 4 * wid + 2 * j) * 1024 + b_off[q]);
+                        b[q][j] = big_frag<Op>(st + (4 + 4 * wid + 2 * j) * 1024 + b_off[q]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        if (i < nb) a[q][i] = big_frag(st + 2 * i * 1024 + a_off[q]);
+                        if (i < nb) a[q][i] = big_frag<Op>(st + 2 * i * 1024 + a_off[q]);
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
@@ -397,7 +399,7 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
                         if (i < nb)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
-                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q][j], acc[i][j], 0, 0, 0);
+                                acc[i][j] = Op::mfma(a[q][i], b[q][j], acc[i][j]);
             }
         }
 
@@ -408,6 +410,14 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
             if constexpr (FUSE == 3) small_finalize(g, fin_lds, ct, row0, rows);
             continue;
         }
+        // int8: lane l holds the scale of row l, and those of its two columns
+        float rs = 1.0f, cs[2] = {1.0f, 1.0f};
+        if constexpr (Op::kScaled) {
+            rs = act_scale<FC1>(g, row0 + min(lane, rows - 1));
+            const float* wsc = g.w_scale + (int64_t)e * g.N + c32;
+            cs[0] = wsc[cb * 64];
+            cs[1] = wsc[min(cb * 64 + 32, g.N - 32)];
+        }
         if constexpr (FC1) {
             // column block 0 is the gate half, 1 the up half of interleave block cb
             const int F = g.N / 2;
@@ -417,10 +427,12 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int r = 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
+                    const float rv = Op::kScaled ? lane_value(4 * r, rs) : 1.0f;
                     if (i < nb && r < rows) {
                         const float pr = PROB ? fc1_row_prob(g.row_prob, g.perm_src, row0 + r) : 1.0f;
                         hb[(int64_t)(row0 + r) * F + cb * 32 + c32] =
-                            f32_to_bf16_bits(swiglu_f32(acc[i][0][v], acc[i][1][v]) * pr);
+                            f32_to_bf16_bits(swiglu_f32(scale_row<Op>(scale_col<Op>(acc[i][0][v], cs[0]), rv),
+                                                        scale_row<Op>(scale_col<Op>(acc[i][1][v], cs[1]), rv)) * pr);
                     }
                 }
         } else {
@@ -434,7 +446,9 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
 #pragma unroll
                         for (int v = 0; v < 16; ++v) {
                             const int r = 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
-                            if (i < nb && r < rows) ob[(int64_t)(row0 + r) * g.N + col] = acc[i][j][v];
+                            const float rv = Op::kScaled ? lane_value(4 * r, rs) : 1.0f;
+                            if (i < nb && r < rows)
+                                ob[(int64_t)(row0 + r) * g.N + col] = scale_row<Op>(scale_col<Op>(acc[i][j][v], cs[j]), rv);
                         }
                 }
             }
