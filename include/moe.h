@@ -6,8 +6,9 @@
  *     out[t] = sum over j in ascending e_j order, as an fp32 fused
  *              multiply-add chain from +0:  p_j * FC2_e( swiglu( FC1_e(x[t]) ) )
  *   where FC1_e yields gate g and up u, swiglu = silu(g) * u = g/(1+exp(-g)) * u,
- *   and the FC2 input is rounded to bf16 (bf16 precision) or re-quantized to
- *   MXFP8 per 32-element block (mxfp8 precision).
+ *   and the FC2 input is rounded to bf16 (bf16 precision), re-quantized to
+ *   MXFP8 per 32-element block (mxfp8 precision), or rounded to bf16 and
+ *   quantized to int8 with one scale per row (int8 precision).
  *
  * Sources (web pages):
  *   Megatron-LM PR #7830 ("flashinfer_mega" backend), section "1. Mega backend
@@ -61,7 +62,7 @@ extern "C" {
 
 typedef struct moe_ctx* moe_handle;
 
-typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_MXFP4 = 2 } moe_precision;
+typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_MXFP4 = 2, MOE_INT8 = 4 } moe_precision;
 
 typedef enum {
     MOE_OK = 0,
@@ -86,11 +87,20 @@ typedef enum {
  * Checks (Megatron-LM PR #7830, construction-time validation; cudnn-frontend
  * PR #448, MXFP8 block of 32): 1 <= E <= 1024; 1 <= topk <= min(E, 16);
  * H and F positive multiples of 32 (the interleave block and the MX
- * block); precision MOE_BF16, MOE_MXFP8 or MOE_MXFP4, else
- * MOE_ERR_UNSUPPORTED.  MOE_MXFP4: weights in E2M1 (the OCP MX 4-bit float)
+ * block); precision MOE_BF16, MOE_MXFP8, MOE_MXFP4 or MOE_INT8, else
+ * MOE_ERR_UNSUPPORTED (int8 also for H or F of 131072 and more, where an
+ * int32 sum of products could overflow).  MOE_MXFP4: weights in E2M1 (the OCP MX 4-bit float)
  * with one E8M0 scale per 32 elements of K, activations and the SwiGLU rows
  * in MXFP8 as with MOE_MXFP8 (the CDNA4-native counterpart of a 4-bit-weight,
- * 8-bit-activation expert GEMM).  Host only: no device work; the device is
+ * 8-bit-activation expert GEMM).  MOE_INT8: weights and activations in 8-bit
+ * integers, one fp32 scale per weight row (output channel) and per activation
+ * row (token, and SwiGLU row): for a row v with largest magnitude amax,
+ *   scale = amax / 127,  code = sign(v) floor(127 |v| / amax + 1/2)
+ * (round half away from zero; a row of zeros has scale 0).  The integer sums
+ * are exact; a result is (float)sum * weight scale * row scale, in that order.
+ * The SwiGLU row is rounded to bf16 as with MOE_BF16 before it is quantized.
+ * A row with an infinity or a NaN has scale NaN, so its token's outputs are
+ * NaN and no other token's change.  Host only: no device work; the device is
  * the one current at the first launch. */
 moe_status moe_create(int E, int H, int F, int topk, int precision, moe_handle* out);
 
@@ -134,12 +144,30 @@ size_t moe_weight_bytes(moe_handle h);
  *         + (b/4)%4,
  *     the scale = power-of-two ceiling of the block's max magnitude / 6,
  *     codes rounded to the nearest E2M1 value with ties to the even code.
+ *   kbuf layout (int8): sections FC1 codes, FC2 codes, FC1 scales (fp32 [E][2F],
+ *     packed row order), FC2 scales (fp32 [E][H]), each starting at a multiple
+ *     of 256 bytes.  Rows are padded with zero codes to Kp, a multiple of 64
+ *     for K < 256, else of 128.  With KS = Kp/64, c = n/16, s = k/64, g = c/32
+ *     and w = min(32, N/16 - 32g), code (e, n, k) is at byte
+ *       (e*(N/16)*KS + g*32*KS + s*w + c%32)*1024 + ((k%64)/16)*256
+ *         + (n%16)*16 + k%16.
  * The handle remembers kbuf: every later forward reads it.  Calling again
  * (same or another buffer) is the refit; forwards enqueued before it on the
  * same stream read the old contents.  w1/w2 may be freed once the work on
  * `stream` is complete.  kbuf_bytes must be >= moe_weight_bytes(h). */
 moe_status moe_load_weights(moe_handle h, const void* w1, const void* w2, void* kbuf,
                             size_t kbuf_bytes, hipStream_t stream);
+
+/* int8 handles: pack weights that are quantized already (a checkpoint with
+ * 8-bit weights) into kbuf, as moe_load_weights does for bf16 ones.
+ *   w1: int8 [E][2F][H], rows ordered as moe_load_weights' w1; w1_scale: fp32
+ *   [E][2F]; w2: int8 [E][H][F]; w2_scale: fp32 [E][H].  A weight is its code
+ *   (any int8 value) times its row's scale.
+ * Errors: as moe_load_weights; MOE_ERR_INVALID_ARG for a handle of another
+ * precision. */
+moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_scale,
+                              const int8_t* w2, const float* w2_scale, void* kbuf,
+                              size_t kbuf_bytes, hipStream_t stream);
 
 /* Workspace bytes for a token capacity T_cap (0 for a NULL handle or a
  * negative T_cap).  The workspace is caller-owned device memory with no
@@ -293,12 +321,14 @@ moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t*
 /* Copy intermediate rows of the last forward to host arrays (synchronizes
  * the stream), in grouped-row order.  fc2_rows: fp32 [n_rows][H], the
  * unweighted FC2 output rows.  fc1_out_rows: the FC2 operand rows, bf16
- * [n_rows][F] (bf16 precision) or E4M3 codes [n_rows][F] followed by E8M0
- * scales [n_rows][F/32] (mxfp8, mxfp4).  sorted_ids / sorted_probs: int32 /
+ * [n_rows][F] (bf16 precision), E4M3 codes [n_rows][F] followed by E8M0
+ * scales [n_rows][F/32] (mxfp8, mxfp4), or int8 codes [n_rows][F] followed by
+ * fp32 scales [n_rows] (int8).  sorted_ids / sorted_probs: int32 /
  * fp32 [T][topk], each token's routes in canonical order.  x_codes /
- * x_scales (mxfp8, mxfp4; must be NULL for bf16): the quantized activations,
- * E4M3 codes uint8 [T][H] and E8M0 scale bytes uint8 [T][H/32] (T = the live
- * tokens of the last forward).  Any output may be NULL.  For tests and
+ * x_scales (mxfp8, mxfp4, int8; must be NULL for bf16): the quantized
+ * activations, E4M3 codes uint8 [T][H] and E8M0 scale bytes uint8 [T][H/32],
+ * or int8 codes [T][H] and fp32 scales [T] (T = the live tokens of the last
+ * forward).  Any output may be NULL.  For tests and
  * debugging.  Errors: MOE_ERR_INVALID_ARG for a NULL handle or workspace, or
  * x_codes / x_scales with bf16; MOE_ERR_HIP if a copy fails. */
 moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_rows,
@@ -322,8 +352,9 @@ moe_status moe_check(moe_handle h, void* ws, hipStream_t stream, uint32_t* err_b
 /* Stage timing hook (for profiling).  With events != NULL, every later
  * moe_forward on this handle records, on its stream, events[0] before its
  * first kernel and events[i] after stage i: 1 permutation (sort, histogram,
- * scan, scatter), 2 MXFP8 activation quantization (nothing in bf16), 3 FC1 +
- * SwiGLU, 4 FC2, 5 finalize.  events[2] and events[3] are the start and end
+ * scan, scatter), 2 MXFP8 / int8 activation quantization (nothing in bf16), 3
+ * FC1 + SwiGLU, 4 FC2 (int8: with the quantization of the SwiGLU rows before
+ * it), 5 finalize.  events[2] and events[3] are the start and end
  * of the FC1 + SwiGLU launch itself, recorded by its dispatch (no marker
  * packets around it), so events[3] - events[2] is that launch's duration
  * (MXFP4 above a 1024-token capacity, where the stage is two launches: the

@@ -69,6 +69,9 @@ def lib() -> ctypes.CDLL:
             "orc_e8m0_exponent_fp4": (ctypes.c_int, [ctypes.c_float]),
             "orc_mx4_quantize": (None, [P, i64, i64, P, P]),
             "orc_mx4_dequantize": (None, [P, P, i64, i64, P]),
+            "orc_int8_quantize": (None, [P, i64, i64, P, P]),
+            "orc_weights_create_quantized": (P, [ctypes.c_int] * 4 + [P] * 4),
+            "orc_pack_int8": (None, [ctypes.c_int] * 3 + [P, P, P]),
             "orc_route": (u32, [P, i64, i32, ctypes.c_int, ctypes.c_int, P, P]),
             "orc_prepare": (u32, [P, P, i64, i32, ctypes.c_int, ctypes.c_int,
                                   P, P, P, P, P, P, P]),
@@ -185,7 +188,17 @@ def mx4_dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     return out
 
 
-PRECISIONS = {"bf16": 0, "mxfp8": 1, "mxfp4": 2}
+def int8_quantize(v: np.ndarray):
+    """[rows, cols] fp32 -> (codes int8 [rows, cols], scales fp32 [rows])."""
+    v = np.ascontiguousarray(v, dtype=np.float32)
+    rows, cols = v.shape
+    codes = np.empty((rows, cols), dtype=np.int8)
+    scales = np.empty(rows, dtype=np.float32)
+    lib().orc_int8_quantize(_p(v), rows, cols, _p(codes), _p(scales))
+    return codes, scales
+
+
+PRECISIONS = {"bf16": 0, "mxfp8": 1, "mxfp4": 2, "int8": 4}
 
 
 # ---------------------------------------------------------------- router / prepare
@@ -281,7 +294,8 @@ class Model:
     """Oracle weights: bf16 W1 [E, 2F, H] (gate rows first) and W2 [E, H, F].
 
     precision: "bf16", "mxfp8" (weights quantized to E4M3 per 32-block along K) or
-    "mxfp4" (weights quantized to E2M1 per 32-block along K; activations MXFP8).
+    "mxfp4" (weights quantized to E2M1 per 32-block along K; activations MXFP8) or
+    "int8" (weights and activations quantized to int8 with a scale per row).
     """
 
     def __init__(self, E, H, F, k, w1_bits: np.ndarray, w2_bits: np.ndarray,
@@ -294,6 +308,17 @@ class Model:
         assert self._w1.size == E * 2 * F * H and self._w2.size == E * H * F
         self._h = lib().orc_weights_create(E, H, F, k, PRECISIONS[precision],
                                            _p(self._w1), _p(self._w2))
+
+    @classmethod
+    def quantized(cls, E, H, F, k, w1: np.ndarray, s1: np.ndarray, w2: np.ndarray, s2: np.ndarray):
+        """An int8 model from codes w1 [E, 2F, H], w2 [E, H, F] and row scales."""
+        m = cls.__new__(cls)
+        m.E, m.H, m.F, m.k, m.precision = E, H, F, k, "int8"
+        m._keep = [np.ascontiguousarray(w1, dtype=np.int8), np.ascontiguousarray(s1, dtype=np.float32),
+                   np.ascontiguousarray(w2, dtype=np.int8), np.ascontiguousarray(s2, dtype=np.float32)]
+        assert m._keep[0].size == E * 2 * F * H and m._keep[2].size == E * H * F
+        m._h = lib().orc_weights_create_quantized(E, H, F, k, *[_p(a) for a in m._keep])
+        return m
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -372,6 +397,6 @@ def pack(E, H, F, w1_bits, w2_bits, precision="bf16") -> np.ndarray:
     w2 = np.ascontiguousarray(w2_bits, dtype=np.uint16)
     buf = np.zeros(pack_bytes(E, H, F, precision), dtype=np.uint8)
     fn = {"bf16": lib().orc_pack_bf16, "mxfp8": lib().orc_pack_mxfp8,
-          "mxfp4": lib().orc_pack_mxfp4}[precision]
+          "mxfp4": lib().orc_pack_mxfp4, "int8": lib().orc_pack_int8}[precision]
     fn(E, H, F, _p(w1), _p(w2), _p(buf))
     return buf

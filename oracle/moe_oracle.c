@@ -262,6 +262,31 @@ void orc_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t row
                                       (int)scales[r * nb + c / 32] - 127);
 }
 
+/* int8 quantization of a [rows][cols] fp32 matrix, one scale per row:
+ * scale = amax / 127 (fp32), code = sign(v) floor(127 |v| / amax + 1/2) (round
+ * half away from zero), taken in fp64 (for bf16-valued v the quotient is never
+ * within 1e-5 of a tie it is not on, so the fp64 rounding cannot move a code).
+ * A row of zeros: scale 0, codes 0.  A row with an infinity or a NaN: scale
+ * NaN, codes 0. */
+void orc_int8_quantize(const float* v, int64_t rows, int64_t cols, int8_t* codes, float* scales)
+{
+#pragma omp parallel for schedule(static)
+    for (int64_t r = 0; r < rows; ++r) {
+        const float* row = v + r * cols;
+        float amax = 0.0f;
+        int bad = 0;
+        for (int64_t c = 0; c < cols; ++c) {
+            if (!isfinite(row[c])) bad = 1;
+            if (fabsf(row[c]) > amax) amax = fabsf(row[c]);
+        }
+        scales[r] = bad ? NAN : amax / 127.0f;
+        for (int64_t c = 0; c < cols; ++c) {
+            double q = bad || amax == 0.0f ? 0.0 : floor(127.0 * fabs((double)row[c]) / (double)amax + 0.5);
+            codes[r * cols + c] = (int8_t)(row[c] < 0.0f ? -q : q);
+        }
+    }
+}
+
 /* ------------------------------------------------------------------------ */
 /* Router ([API] `_route`; softmax, top-k, renormalize)                      */
 /* ------------------------------------------------------------------------ */
@@ -419,20 +444,39 @@ static float swiglu_f32(float g, float u)
  * copied) or fp32 operand values (MXFP8 path: the dequantized quantization). */
 typedef struct {
     int E, H, F, k;
-    int mx;                 /* 0: bf16 path, 1: MXFP8 path, 2: MXFP4 weights + MXFP8 activations */
+    int mx;                 /* 0: bf16 path, 1: MXFP8 path, 2: MXFP4 weights + MXFP8 activations,
+                               4: int8 codes with a scale per row */
+    const int8_t* w1q;      /* int8: codes and row scales, shapes as w1b / w2b */
+    const int8_t* w2q;
+    const float* s1;
+    const float* s2;
     const uint16_t* w1b;    /* bf16 [E][2F][H] (gate rows 0..F-1, up rows F..2F-1) */
     const uint16_t* w2b;    /* bf16 [E][H][F] */
     const float* w1f;       /* MXFP8 / MXFP4 weight operand values, same shapes */
     const float* w2f;
 } orc_model;
 
+/* An operand row of the int8 path: the codes, then the row's scale. */
+static int64_t operand_len(const orc_model* m, int64_t K) { return m->mx == 4 ? K + 1 : K; }
+
+/* The codes' dot product (exact in fp64), converted to fp32 and multiplied by
+ * the weight row's scale, then by the operand row's. */
+static float dot_q(const double* a, const int8_t* b, float scale, int64_t n)
+{
+    double s = 0.0;
+    for (int64_t i = 0; i < n; ++i) s += a[i] * (double)b[i];
+    return (float)s * scale * (float)a[n];
+}
+
 static float dot_w1(const orc_model* m, const double* xr, int64_t row)
 {
+    if (m->mx == 4) return dot_q(xr, m->w1q + row * m->H, m->s1[row], m->H);
     return m->mx ? dot_f32w(xr, m->w1f + row * m->H, m->H) : dot_bf16(xr, m->w1b + row * m->H, m->H);
 }
 
 static float dot_w2(const orc_model* m, const double* hr, int64_t row)
 {
+    if (m->mx == 4) return dot_q(hr, m->w2q + row * m->F, m->s2[row], m->F);
     return m->mx ? dot_f32w(hr, m->w2f + row * m->F, m->F) : dot_bf16(hr, m->w2b + row * m->F, m->F);
 }
 
@@ -455,6 +499,15 @@ static void expert_row_p(const orc_model* m, int e, const double* xr, float* o,
     }
     if (!m->mx) {
         for (int64_t n = 0; n < F; ++n) hrow[n] = orc_bf16_round(a32[n]);
+    } else if (m->mx == 4) {
+        /* the bf16 row of the bf16 path, quantized with one scale */
+        int8_t* q = (int8_t*)malloc((size_t)F);
+        float sc;
+        for (int64_t n = 0; n < F; ++n) a32[n] = orc_bf16_round(a32[n]);
+        orc_int8_quantize(a32, 1, F, q, &sc);
+        for (int64_t n = 0; n < F; ++n) hrow[n] = q[n];
+        hrow[F] = sc;
+        free(q);
     } else {
         for (int64_t b = 0; b < F / 32; ++b) {
             float amax = 0.0f;
@@ -569,8 +622,19 @@ void orc_finalize_rows(const float* O, const int32_t* dst, int32_t T, int k, int
  * quantization of those bf16 values (per token, per 32-block of H). */
 static double* x_operands(const uint16_t* x, int64_t T, int H, int mx)
 {
-    double* xo = (double*)malloc(sizeof(double) * T * H);
-    if (!mx) {
+    double* xo = (double*)malloc(sizeof(double) * T * (H + 1));
+    if (mx == 4) {
+        float* xf = (float*)malloc(sizeof(float) * H);
+        int8_t* q = (int8_t*)malloc((size_t)H);
+        for (int64_t t = 0; t < T; ++t) {
+            float sc;
+            for (int64_t i = 0; i < H; ++i) xf[i] = orc_bf16_value(x[t * H + i]);
+            orc_int8_quantize(xf, 1, H, q, &sc);
+            for (int64_t i = 0; i < H; ++i) xo[t * (H + 1) + i] = q[i];
+            xo[t * (H + 1) + H] = sc;
+        }
+        free(xf); free(q);
+    } else if (!mx) {
         for (int64_t i = 0; i < T * H; ++i) xo[i] = orc_bf16_value(x[i]);
     } else {
         float* xf = (float*)malloc(sizeof(float) * T * H);
@@ -624,6 +688,17 @@ static float* w_mx4_operands(const uint16_t* w, int64_t rows, int64_t cols)
     return wf;
 }
 
+/* int8 weights: codes and row scales of the bf16 values. */
+static void w_int8_operands(const uint16_t* w, int64_t rows, int64_t cols, int8_t** q, float** sc)
+{
+    float* wf = (float*)malloc(sizeof(float) * rows * cols);
+    *q = (int8_t*)malloc(rows * cols);
+    *sc = (float*)malloc(sizeof(float) * rows);
+    for (int64_t i = 0; i < rows * cols; ++i) wf[i] = orc_bf16_value(w[i]);
+    orc_int8_quantize(wf, rows, cols, *q, *sc);
+    free(wf);
+}
+
 /* Opaque prepared weights, so that repeated oracle calls on the same model
  * (sampled tokens, timing) do not rebuild the operand values.  In the bf16
  * path the caller's arrays are read in place and must outlive the handle. */
@@ -631,6 +706,10 @@ typedef struct {
     orc_model m;
     float* w1f;
     float* w2f;
+    int8_t* w1q;
+    int8_t* w2q;
+    float* s1;
+    float* s2;
 } orc_weights;
 
 void* orc_weights_create(int E, int H, int F, int k, int mx, const uint16_t* w1,
@@ -645,8 +724,24 @@ void* orc_weights_create(int E, int H, int F, int k, int mx, const uint16_t* w1,
         w->w1f = w_mx4_operands(w1, (int64_t)E * 2 * F, H);
         w->w2f = w_mx4_operands(w2, (int64_t)E * H, F);
     }
+    if (mx == 4) {
+        w_int8_operands(w1, (int64_t)E * 2 * F, H, &w->w1q, &w->s1);
+        w_int8_operands(w2, (int64_t)E * H, F, &w->w2q, &w->s2);
+    }
     w->m.w1b = w1; w->m.w2b = w2;
     w->m.w1f = w->w1f; w->m.w2f = w->w2f;
+    w->m.w1q = w->w1q; w->m.w2q = w->w2q; w->m.s1 = w->s1; w->m.s2 = w->s2;
+    return w;
+}
+
+/* int8 weights given as codes and row scales (read in place: the caller's
+ * arrays must outlive the handle). */
+void* orc_weights_create_quantized(int E, int H, int F, int k, const int8_t* w1, const float* s1,
+                                   const int8_t* w2, const float* s2)
+{
+    orc_weights* w = (orc_weights*)calloc(1, sizeof(orc_weights));
+    w->m.E = E; w->m.H = H; w->m.F = F; w->m.k = k; w->m.mx = 4;
+    w->m.w1q = w1; w->m.s1 = s1; w->m.w2q = w2; w->m.s2 = s2;
     return w;
 }
 
@@ -654,7 +749,7 @@ void orc_weights_destroy(void* p)
 {
     orc_weights* w = (orc_weights*)p;
     if (!w) return;
-    free(w->w1f); free(w->w2f); free(w);
+    free(w->w1f); free(w->w2f); free(w->w1q); free(w->w2q); free(w->s1); free(w->s2); free(w);
 }
 
 /* The whole forward, step by step: canonical sort and permutation
@@ -689,16 +784,17 @@ uint32_t orc_forward_ex(void* wp, const uint16_t* x, const int32_t* ids, const f
 #pragma omp parallel
     {
         float* a32 = (float*)malloc(sizeof(float) * F);
-        double* hrow = (double*)malloc(sizeof(double) * F);
+        double* hrow = (double*)malloc(sizeof(double) * (F + 1));
 #pragma omp for schedule(dynamic, 1)
         for (int64_t i = 0; i < nrows; ++i) {
             int32_t r = perm_src[i];
             int32_t t = r / k;
             int32_t e = sorted_ids[r];
-            expert_row_p(m, e, xo + (int64_t)t * H, O + i * H, a32, hrow,
+            expert_row_p(m, e, xo + t * operand_len(m, H), O + i * H, a32, hrow,
                          fc1_topk ? sorted_probs[r] : 1.0f);
             if (H_out)
-                for (int64_t n = 0; n < F; ++n) H_out[i * F + n] = (float)hrow[n];
+                for (int64_t n = 0; n < F; ++n)
+                    H_out[i * F + n] = m->mx == 4 ? (float)(hrow[n] * hrow[F]) : (float)hrow[n];
         }
         free(a32); free(hrow);
     }
@@ -748,14 +844,14 @@ void orc_forward_tokens_ex(void* wp, const uint16_t* x, const int32_t* ids, cons
 #pragma omp parallel
     {
         float* a32 = (float*)malloc(sizeof(float) * F);
-        double* hrow = (double*)malloc(sizeof(double) * F);
+        double* hrow = (double*)malloc(sizeof(double) * (F + 1));
         float* o = (float*)malloc(sizeof(float) * (int64_t)k * H);
-        double* xr = (double*)malloc(sizeof(double) * H);
+        double* xr = (double*)malloc(sizeof(double) * (H + 1));
 #pragma omp for schedule(dynamic, 1)
         for (int64_t q = 0; q < n_tok; ++q) {
             int64_t t = tokens[q];
             double* xo = x_operands(x + t * H, 1, H, m->mx);
-            memcpy(xr, xo, sizeof(double) * H);
+            memcpy(xr, xo, sizeof(double) * operand_len(m, H));
             free(xo);
             int32_t id[64];
             float p[64];
@@ -936,10 +1032,48 @@ void orc_pack_mxfp4(int E, int H, int F, const uint16_t* w1, const uint16_t* w2,
     pack_mx4_section(E, H, F, F, 0, w2, kbuf + c1, kbuf + c1 + c2 + s1);
 }
 
+/* int8 buffer: codes of FC1 and FC2, then their fp32 row scales (FC1's in
+ * packed row order), each section starting at a multiple of 256 bytes.  Rows of
+ * K codes are padded with zero codes to Kp: a multiple of 64 for K < 256, else
+ * of 128.  1 KB blocks of 16 rows x 64 K; with c = n/16, s = k/64, KS = Kp/64,
+ * g = c/32 and w = min(32, N/16 - 32g), code (e, n, k) is at byte
+ *   (e*(N/16)*KS + g*32*KS + s*w + c%32)*1024 + ((k%64)/16)*256 + (n%16)*16 + k%16 . */
+static int64_t int8_pitch(int64_t K) { return K < 256 ? (K + 63) / 64 * 64 : (K + 127) / 128 * 128; }
+
+static void pack_int8_section(int E, int64_t N, int64_t K, int64_t F, int fc1, const uint16_t* w,
+                              uint8_t* codes, float* scales)
+{
+    const int64_t KS = int8_pitch(K) / 64;
+    float* row = (float*)malloc(sizeof(float) * K);
+    int8_t* q = (int8_t*)malloc(K);
+    memset(codes, 0, (size_t)E * N * int8_pitch(K));
+    for (int64_t e = 0; e < E; ++e)
+        for (int64_t n = 0; n < N; ++n) {
+            int64_t src = fc1 ? fc1_logical_row(n, F) : n;
+            for (int64_t k = 0; k < K; ++k) row[k] = orc_bf16_value(w[(e * N + src) * K + k]);
+            orc_int8_quantize(row, 1, K, q, scales + e * N + n);
+            for (int64_t k = 0; k < K; ++k)
+                codes[mx4_block(e, n / 16, k / 64, N / 16, KS) * 1024 + (k % 64) / 16 * 256 +
+                      (n % 16) * 16 + k % 16] = (uint8_t)q[k];
+        }
+    free(row); free(q);
+}
+
+void orc_pack_int8(int E, int H, int F, const uint16_t* w1, const uint16_t* w2, uint8_t* kbuf)
+{
+    int64_t c1 = up256((int64_t)E * 2 * F * int8_pitch(H)), c2 = up256((int64_t)E * H * int8_pitch(F));
+    int64_t s1 = up256((int64_t)E * 2 * F * 4);
+    pack_int8_section(E, 2 * (int64_t)F, H, F, 1, w1, kbuf, (float*)(kbuf + c1 + c2));
+    pack_int8_section(E, H, F, F, 0, w2, kbuf + c1, (float*)(kbuf + c1 + c2 + s1));
+}
+
 int64_t orc_pack_bytes(int E, int H, int F, int mx)
 {
     int64_t n1 = (int64_t)E * 2 * F * H, n2 = (int64_t)E * H * F;
     if (!mx) return 2 * (n1 + n2);
+    if (mx == 4)
+        return up256((int64_t)E * 2 * F * int8_pitch(H)) + up256((int64_t)E * H * int8_pitch(F)) +
+               up256((int64_t)E * 2 * F * 4) + up256((int64_t)E * H * 4);
     if (mx == 2)
         return up256(code4_bytes(E, 2 * (int64_t)F, H)) + up256(code4_bytes(E, H, F)) +
                up256(scale_bytes(E, 2 * (int64_t)F, H)) + up256(scale_bytes(E, H, F));

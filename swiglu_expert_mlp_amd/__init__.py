@@ -6,7 +6,7 @@ of ``libmoe.so`` (C ABI in ``include/moe.h``); torch supplies device memory
 and the current stream.  There is no CPU fallback: if the library is missing
 or no GPU is present, the calls raise.
 
-    moe = MoE(E=64, H=2048, F=1024, topk=6, precision="bf16")
+    moe = MoE(E=64, H=2048, F=1024, topk=6, precision="bf16")   # or mxfp8, mxfp4, int8
     kbuf = moe.load_weights(w1, w2)          # w1 [E, 2F, H], w2 [E, H, F], bf16, on GPU
     ws = moe.new_workspace(T_cap)
     ids, probs = moe.route(logits, live, ws=ws)
@@ -25,8 +25,8 @@ __all__ = ["MoE", "lib", "LIB_PATH", "MoEError", "DEVERR_BAD_EXPERT_ID", "DEVERR
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
-MOE_BF16, MOE_MXFP8, MOE_MXFP4 = 0, 1, 2
-_PRECISION = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "mxfp4": MOE_MXFP4}
+MOE_BF16, MOE_MXFP8, MOE_MXFP4, MOE_INT8 = 0, 1, 2, 4
+_PRECISION = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "mxfp4": MOE_MXFP4, "int8": MOE_INT8}
 DEVERR_BAD_EXPERT_ID = 1
 DEVERR_DUP_EXPERT_ID = 2
 DEVERR_LIVE_ABOVE_CAP = 4
@@ -50,6 +50,7 @@ _SIGNATURES = {
     "moe_destroy": (None, [_P]),
     "moe_weight_bytes": (ctypes.c_size_t, [_P]),
     "moe_load_weights": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_load_quantized": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int64]),
     "moe_route": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_forward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -129,7 +130,7 @@ class MoE:
 
     def __init__(self, E: int, H: int, F: int, topk: int, precision: str = "bf16"):
         if precision not in _PRECISION:
-            raise NotImplementedError(f"precision {precision!r} is not supported (bf16, mxfp8, mxfp4)")
+            raise NotImplementedError(f"precision {precision!r} is not supported (bf16, mxfp8, mxfp4, int8)")
         h = _P()
         _check(lib().moe_create(E, H, F, topk, _PRECISION[precision], ctypes.byref(h)),
                "moe_create")
@@ -177,6 +178,23 @@ class MoE:
         _check(lib().moe_load_weights(self._h, p1, p2, pk, kbuf.numel(), _stream(stream)),
                "moe_load_weights")
         self.kbuf = kbuf          # keep the buffer alive as long as the handle reads it
+        return kbuf
+
+    def load_quantized(self, w1, w1_scale, w2, w2_scale, kbuf=None, stream=None):
+        """int8 handles: pack weights that are quantized already, as load_weights does
+        for bf16 ones.  w1 int8 [E, 2F, H] (gate rows first) with w1_scale fp32 [E, 2F],
+        w2 int8 [E, H, F] with w2_scale fp32 [E, H]."""
+        torch = _torch()
+        p1 = _dev(w1, "w1", (torch.int8,), (self.E, 2 * self.F, self.H))
+        q1 = _dev(w1_scale, "w1_scale", (torch.float32,), (self.E, 2 * self.F))
+        p2 = _dev(w2, "w2", (torch.int8,), (self.E, self.H, self.F))
+        q2 = _dev(w2_scale, "w2_scale", (torch.float32,), (self.E, self.H))
+        if kbuf is None:
+            kbuf = torch.empty(self.weight_bytes, dtype=torch.uint8, device=w1.device)
+        pk = _dev(kbuf, "kbuf", (torch.uint8,))
+        _check(lib().moe_load_quantized(self._h, p1, q1, p2, q2, pk, kbuf.numel(), _stream(stream)),
+               "moe_load_quantized")
+        self.kbuf = kbuf
         return kbuf
 
     def route(self, logits, live, ids=None, probs=None, ws=None, stream=None):
@@ -282,24 +300,33 @@ class MoE:
 
     def get_rows(self, ws, T_cap: int, n_rows: int, T: int, stream=None) -> dict:
         """Intermediate rows of the last forward (moe_get_rows); for MXFP8 / MXFP4
-        also the quantized activations x_codes [T, H] and x_scales [T, H/32]."""
+        also the quantized activations x_codes [T, H] and x_scales [T, H/32], for
+        int8 x_codes int8 [T, H] and x_scales fp32 [T]."""
         import numpy as np
         O = np.zeros((max(1, n_rows), self.H), np.float32)
+        int8 = self.precision == "int8"
         if self.precision == "bf16":
             hr = np.zeros((max(1, n_rows), self.F), np.uint16)
+        elif int8:
+            hr = np.zeros(max(1, n_rows) * (self.F + 4), np.uint8)
         else:
             hr = np.zeros(max(1, n_rows) * (self.F + self.F // 32), np.uint8)
         sid = np.zeros((max(1, T), self.topk), np.int32)
         sp = np.zeros((max(1, T), self.topk), np.float32)
         mx = self.precision != "bf16"
         xc = np.zeros((max(1, T), self.H), np.uint8) if mx else None
-        xs = np.zeros((max(1, T), self.H // 32), np.uint8) if mx else None
+        xs = (np.zeros(max(1, T), np.float32) if int8 else
+              np.zeros((max(1, T), self.H // 32), np.uint8) if mx else None)
         c = lambda a: None if a is None else a.ctypes.data_as(_P)
         _check(lib().moe_get_rows(self._h, _dev(ws, "ws", (_torch().uint8,)), T_cap, c(O), c(hr),
                                   c(sid), c(sp), c(xc), c(xs), _stream(stream)), "moe_get_rows")
         res = dict(fc2_rows=O[:n_rows], sorted_ids=sid[:T], sorted_probs=sp[:T])
         if self.precision == "bf16":
             res["fc1_out"] = hr[:n_rows]
+        elif int8:
+            res["fc1_codes"] = hr[: n_rows * self.F].reshape(n_rows, self.F).view(np.int8)
+            res["fc1_scales"] = hr[n_rows * self.F: n_rows * (self.F + 4)].view(np.float32)
+            res["x_codes"], res["x_scales"] = xc[:T].view(np.int8), xs[:T]
         else:
             res["fc1_codes"] = hr[: n_rows * self.F].reshape(n_rows, self.F)
             res["fc1_scales"] = hr[n_rows * self.F: n_rows * (self.F + self.F // 32)].reshape(

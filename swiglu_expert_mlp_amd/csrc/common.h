@@ -35,6 +35,15 @@ __host__ __device__ inline int64_t wblock_step(int64_t n16, int64_t nt16)
     return nt16 - 32 * g < 32 ? nt16 - 32 * g : 32;
 }
 
+// Codes per row of an int8 operand with K elements: padded with zero codes to a
+// multiple of 128 (the 256-row tiles' stage), or of 64 (the 64-row tiles' step)
+// below 256, where the 256-row tiles are not used.  FFN 1856 becomes 1920, 3 %
+// more FC2 bytes, for the 256-row tiles on such a K.
+__host__ __device__ inline int int8_pitch(int K)
+{
+    return K < 256 ? (K + 63) / 64 * 64 : (K + 127) / 128 * 128;
+}
+
 constexpr int kBM = 64;              // rows per M tile of the small-expert GEMM tiles
 constexpr int kBigBMRows = 256;      // rows per M tile of the LDS-staged GEMMs
 constexpr int kBigMin = 128;         // experts with more rows than this use the LDS-staged GEMMs
@@ -170,6 +179,9 @@ struct WsLayout {
     size_t obuf;           // float [T_cap * k][H]
     size_t xq;             // E4M3 [T_cap][H] (mxfp8)
     size_t xs;             // E8M0 [T_cap][H / 32] (mxfp8)
+    size_t hq;             // int8: codes [T_cap * k][int8_pitch(F)] of the SwiGLU rows (hbuf is
+                           // bf16, hscale fp32 [T_cap * k]; xq codes [T_cap][int8_pitch(H)],
+                           // xs fp32 [T_cap])
     size_t total;
     int64_t nchunks;
     int64_t max_tiles;

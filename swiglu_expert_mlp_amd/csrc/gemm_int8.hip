@@ -1,0 +1,72 @@
+// K3 / K4, int8: grouped expert GEMMs on the CDNA4 int8 MFMA (32x32x32), int32
+// accumulate, one fp32 scale per activation row and per weight row:
+//   FC1  g, u = (float)(sum_k xq[t,k] wq[n,k]) * sw[n] * sx[t], h = silu(g) u
+//        rounded to bf16 (the FC2 input of the bf16 path, quantized per row by
+//        the launch between the two GEMMs: its scale needs the whole row);
+//   FC2  O = (float)(sum_f hq[r,f] wq[m,f]) * sw[m] * sh[r], fp32 rows.
+// The sums are exact (|code| <= 128 and K < 131072 keep them inside int32), so
+// every tile design gives the same bits whatever its K order; the two fp32
+// multiplies run in one order everywhere (scale_col, scale_row).
+//
+// The tiles are the bf16 ones (gemm_bf16_big.h, gemm_bf16_small.h) with a pair
+// of codes in place of a bf16 element: the same 16 bytes a lane and cycles per
+// MFMA, half the bytes and MFMAs per row.  Rows are padded with zero codes to a
+// multiple of 128 (64 below 256; common.h), so that every K from 256 on takes
+// the 256-row design's 128-byte stages.
+#include <hip/hip_ext.h>
+
+#include "gemm_bf16_big.h"
+#include "gemm_bf16_small.h"
+
+namespace moe {
+
+template <bool FC1, bool PROB>
+__global__ void __launch_bounds__(512, 1) gemm_int8_small_kernel(GemmArgs g)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[kSmallLds];
+    // as the bf16 kernel: the counts and the first tile's entry in one round trip
+    const int n_big = g.small_takes_big ? ld_const(&g.hdr->n_tiles_big) : 0;
+    const int n_small = ld_const(&g.hdr->n_tiles);
+    const int multi = ld_const(&g.hdr->multi_tile);
+    const int* te0 = (const int*)(g.tiles + min(xcd_first_tile() / small_col_tiles(g), g.max_tiles - 1));
+    const int e0 = ld_const(te0), row00 = ld_const(te0 + 1);
+    asm volatile("" : : "s"(n_big), "s"(n_small), "s"(multi), "s"(e0), "s"(row00));
+    if (multi) small_tiles<OpInt8, FC1, PROB, 0, 0>(g, smem, n_small, n_big, e0, row00);
+    else small_tiles<OpInt8, FC1, PROB, 0, kNonTemporal>(g, smem, n_small, n_big, e0, row00);
+}
+
+template <bool FC1, bool PROB>
+__global__ void __launch_bounds__(512, 1) gemm_int8_big_kernel(GemmArgs g)
+{
+    big_tiles<OpInt8, FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
+}
+
+// One GEMM stage: the 256-row launch (unless the 64-row kernel takes its tiles),
+// then the 64-row launch.  t0 / t1 as launch_gemm_bf16.
+hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
+                            hipEvent_t t1)
+{
+    if (!g.a_scale || !g.w_scale || g.K < 32 || g.K % 32 != 0 || g.N < 32 || g.N % 32 != 0)
+        return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
+    auto go = [&](auto kernel, hipEvent_t e0, hipEvent_t e1) {
+        if (e0 || e1)
+            hipExtLaunchKernelGGL(kernel, grid, block, 0, s, e0, e1, 0, g);
+        else
+            hipLaunchKernelGGL(kernel, grid, block, 0, s, g);
+    };
+    const bool prob = fc1 && g.row_prob != nullptr;
+    hipEvent_t small_start = t0;
+    if (!g.small_takes_big) {
+        if (prob) go(gemm_int8_big_kernel<true, true>, t0, nullptr);
+        else if (fc1) go(gemm_int8_big_kernel<true, false>, t0, nullptr);
+        else go(gemm_int8_big_kernel<false, false>, t0, nullptr);
+        small_start = nullptr;
+    }
+    if (prob) go(gemm_int8_small_kernel<true, true>, small_start, t1);
+    else if (fc1) go(gemm_int8_small_kernel<true, false>, small_start, t1);
+    else go(gemm_int8_small_kernel<false, false>, small_start, t1);
+    return hipGetLastError();
+}
+
+}  // namespace moe

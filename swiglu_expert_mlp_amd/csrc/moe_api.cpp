@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "../../include/moe.h"
@@ -28,6 +29,11 @@ void mx_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, s
 hipError_t launch_pack_mxfp4(const uint16_t* w1, const uint16_t* w2, uint8_t* kbuf, int E, int H,
                              int F, int num_cu, hipStream_t s);
 void mx4_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
+hipError_t launch_quant_rows_int8(const uint16_t* src, const int32_t* n_rows, int64_t cap, int K, int Kp,
+                                  uint8_t* codes, float* scales, int num_cu, hipStream_t s);
+hipError_t launch_pack_int8(const void* w1, const float* ws1, const void* w2, const float* ws2, int codes,
+                            uint8_t* kbuf, int E, int H, int F, int num_cu, hipStream_t s);
+void int8_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
 hipError_t launch_quant_x(const uint16_t* x, int64_t T_cap, const int32_t* live, int H,
                           uint8_t* codes, uint8_t* scales, int num_cu, hipStream_t s);
 }  // namespace moe
@@ -39,6 +45,8 @@ hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t
                             hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
                                   hipEvent_t t0, hipEvent_t t1);
+hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
+                            hipEvent_t t1);
 hipError_t launch_gemm_mxfp8(bool fc1, bool w4, const MxGemmArgs& g, int num_cu, hipStream_t s,
                              hipEvent_t t0, hipEvent_t t1);
 }  // namespace moe
@@ -123,7 +131,15 @@ static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
         L.hbuf = take(2 * R * F);
         L.hscale = 0;
         L.xq = L.xs = 0;
+        L.hq = 0;
+    } else if (h->precision == MOE_INT8) {
+        L.hbuf = take(2 * R * F);
+        L.hscale = take(4 * R);
+        L.xq = take(T_cap * int8_pitch(h->H));
+        L.xs = take(4 * T_cap);
+        L.hq = take(R * int8_pitch(h->F));
     } else {
+        L.hq = 0;
         L.hbuf = take(R * F);
         L.hscale = take(R * (F / 32));
         L.xq = take(T_cap * H);
@@ -154,6 +170,7 @@ static moe_status ensure_device(moe_ctx* h)
 // the process ends.  Host code never uses the array's name as an address: the
 // name is a host-side stand-in, so the device address of each GPU's copy is
 // taken once with hipGetSymbolAddress while that GPU is current.
+constexpr int kInt8MaxK = 131072;      // 2^31 / 128^2
 constexpr size_t kScratchBytes = (size_t)64 << 20;
 constexpr int kMaxScratchDevices = 64;
 static __device__ __attribute__((aligned(256))) char scratch[kScratchBytes];
@@ -222,9 +239,10 @@ moe_status moe_create(int E, int H, int F, int topk, int precision, moe_handle* 
 {
     if (!out) return fail(MOE_ERR_INVALID_ARG, "moe_create: out is NULL");
     *out = nullptr;
-    if (precision != MOE_BF16 && precision != MOE_MXFP8 && precision != MOE_MXFP4)
+    if (precision != MOE_BF16 && precision != MOE_MXFP8 && precision != MOE_MXFP4 &&
+        precision != MOE_INT8)
         return fail(MOE_ERR_UNSUPPORTED,
-                    "moe_create: precision %d is not supported (bf16=0, mxfp8=1, mxfp4=2)", precision);
+                    "moe_create: precision %d is not supported (bf16=0, mxfp8=1, mxfp4=2, int8=4)", precision);
     if (E < 1 || E > kMaxExperts)
         return fail(MOE_ERR_INVALID_ARG, "moe_create: E=%d outside [1, %d]", E, kMaxExperts);
     if (topk < 1 || topk > kMaxTopk || topk > E)
@@ -233,7 +251,11 @@ moe_status moe_create(int E, int H, int F, int topk, int precision, moe_handle* 
         return fail(MOE_ERR_INVALID_ARG, "moe_create: H=%d must be a positive multiple of 32", H);
     if (F <= 0 || F % 32 != 0)
         return fail(MOE_ERR_INVALID_ARG, "moe_create: F=%d must be a positive multiple of 32", F);
-    moe_ctx* h = new moe_ctx();
+    // int8: products of codes up to 128 in magnitude stay inside an int32 sum
+    if (precision == MOE_INT8 && (H >= kInt8MaxK || F >= kInt8MaxK))
+        return fail(MOE_ERR_UNSUPPORTED, "moe_create: int8 takes H and F below %d", kInt8MaxK);
+    moe_ctx* h = new (std::nothrow) moe_ctx();
+    if (!h) return fail(MOE_ERR_UNSUPPORTED, "moe_create: out of host memory");
     h->E = E; h->H = H; h->F = F; h->k = topk; h->precision = precision;
     *out = h;
     g_err.clear();
@@ -248,7 +270,9 @@ size_t moe_weight_bytes(moe_handle h)
     size_t n1 = (size_t)h->E * 2 * h->F * h->H, n2 = (size_t)h->E * h->H * h->F;
     if (h->precision == MOE_BF16) return 2 * (n1 + n2);
     size_t c1, c2, s1, s2;
-    if (h->precision == MOE_MXFP4)
+    if (h->precision == MOE_INT8)
+        int8_section_bytes(h->E, h->H, h->F, &c1, &c2, &s1, &s2);
+    else if (h->precision == MOE_MXFP4)
         mx4_section_bytes(h->E, h->H, h->F, &c1, &c2, &s1, &s2);
     else
         mx_section_bytes(h->E, h->H, h->F, &c1, &c2, &s1, &s2);
@@ -280,8 +304,32 @@ moe_status moe_load_weights(moe_handle h, const void* w1, const void* w2, void* 
     hipError_t e =
         h->precision == MOE_BF16    ? launch_pack_bf16(a, b, kb, h->E, h->H, h->F, h->num_cu, stream)
         : h->precision == MOE_MXFP8 ? launch_pack_mxfp8(a, b, kb, h->E, h->H, h->F, h->num_cu, stream)
+        : h->precision == MOE_INT8  ? launch_pack_int8(a, nullptr, b, nullptr, 0, kb, h->E, h->H, h->F,
+                                                       h->num_cu, stream)
                                     : launch_pack_mxfp4(a, b, kb, h->E, h->H, h->F, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_load_weights: launch");
+    h->kbuf = (const uint8_t*)kbuf;
+    return MOE_OK;
+}
+
+moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_scale, const int8_t* w2,
+                              const float* w2_scale, void* kbuf, size_t kbuf_bytes, hipStream_t stream)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: NULL handle");
+    if (h->precision != MOE_INT8)
+        return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: the handle's precision is not int8");
+    if (!w1 || !w1_scale || !w2 || !w2_scale || !kbuf)
+        return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: NULL pointer");
+    if (!aligned16(w1) || !aligned16(w1_scale) || !aligned16(w2) || !aligned16(w2_scale) || !aligned16(kbuf))
+        return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: pointers must be 16-byte aligned");
+    if (kbuf_bytes < moe_weight_bytes(h))
+        return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: kbuf_bytes %zu < %zu", kbuf_bytes,
+                    moe_weight_bytes(h));
+    moe_status st = ensure_device(h);
+    if (st != MOE_OK) return st;
+    const hipError_t e = launch_pack_int8(w1, w1_scale, w2, w2_scale, 1, (uint8_t*)kbuf, h->E, h->H, h->F,
+                                          h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_load_quantized: launch");
     h->kbuf = (const uint8_t*)kbuf;
     return MOE_OK;
 }
@@ -462,6 +510,55 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
             }
         }
         if ((e = mark(h, 4, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
+    } else if (h->precision == MOE_INT8) {
+        const int Kp1 = int8_pitch(H), Kp2 = int8_pitch(F);
+        size_t b1, b2, b3, b4;
+        int8_section_bytes(E, H, F, &b1, &b2, &b3, &b4);
+        e = launch_quant_rows_int8((const uint16_t*)x, live_rows_dev, T_cap, H, Kp1, (uint8_t*)(w + L.xq),
+                                   (float*)(w + L.xs), h->num_cu, stream);
+        if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-x launch");
+        GemmArgs g1{};
+        g1.A = (const uint16_t*)(w + L.xq);
+        g1.W = (const uint16_t*)h->kbuf;
+        g1.perm_src = (const int32_t*)(w + L.perm_src);
+        g1.tiles = (const int2*)(w + L.tiles);
+        g1.tiles_big = (const int2*)(w + L.tiles_big);
+        g1.offsets = (const int32_t*)(w + L.offsets);
+        g1.hdr = hdr;
+        g1.out = w + L.hbuf;
+        g1.N = 2 * F;
+        g1.K = Kp1 / 2;               // pairs of codes
+        g1.topk = h->k;
+        g1.n_tiles_n = ((2 * F / 64) + 3) / 4;
+        g1.max_tiles = (int)L.max_tiles;
+        // the 256-row design as for bf16: capacities above 1024, whole stages of
+        // 128 codes, two at least, and offsets that fit its 32-bit descriptors
+        g1.small_takes_big = T_cap <= 1024 || Kp1 % 128 != 0 || Kp1 < 256 ||
+                             T_cap * Kp1 >= ((int64_t)1 << 31) || (int64_t)2 * F * Kp1 >= ((int64_t)1 << 31);
+        g1.row_prob = fc1_topk ? (const float*)(w + L.sorted_probs) : nullptr;
+        g1.a_scale = (const float*)(w + L.xs);
+        g1.w_scale = (const float*)(h->kbuf + b1 + b2);
+        e = launch_gemm_int8(true, g1, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
+        if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1 launch");
+        e = launch_quant_rows_int8((const uint16_t*)(w + L.hbuf), &hdr->n_rows, T_cap * h->k, F, Kp2,
+                                   (uint8_t*)(w + L.hq), (float*)(w + L.hscale), h->num_cu, stream);
+        if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-h launch");
+        GemmArgs g2 = g1;
+        g2.A = (const uint16_t*)(w + L.hq);
+        g2.W = (const uint16_t*)(h->kbuf + b1);
+        g2.perm_src = nullptr;
+        g2.out = w + L.obuf;
+        g2.N = H;
+        g2.K = Kp2 / 2;
+        g2.n_tiles_n = ((H + 63) / 64 + 3) / 4;
+        g2.row_prob = nullptr;
+        g2.small_takes_big = T_cap <= 1024 || Kp2 % 128 != 0 || Kp2 < 256 ||
+                             (int64_t)H * Kp2 >= ((int64_t)1 << 31);
+        g2.a_scale = (const float*)(w + L.hscale);
+        g2.w_scale = (const float*)(h->kbuf + b1 + b2 + b3);
+        e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr);
+        if (e != hipSuccess) return hip_fail(e, "moe_forward: FC2 launch");
+        if ((e = mark(h, 4, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     } else {
         // MXFP8, or MXFP4 weights with MXFP8 activations
         const bool w4 = h->precision == MOE_MXFP4;
@@ -601,6 +698,10 @@ moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_
     if (e == hipSuccess && fc1_out_rows && n) {
         if (h->precision == MOE_BF16) {
             e = hipMemcpy(fc1_out_rows, w + L.hbuf, 2 * n * h->F, hipMemcpyDeviceToHost);
+        } else if (h->precision == MOE_INT8) {
+            e = hipMemcpy2D(fc1_out_rows, h->F, w + L.hq, int8_pitch(h->F), h->F, n, hipMemcpyDeviceToHost);
+            if (e == hipSuccess)
+                e = hipMemcpy((char*)fc1_out_rows + n * h->F, w + L.hscale, 4 * n, hipMemcpyDeviceToHost);
         } else {
             e = hipMemcpy(fc1_out_rows, w + L.hbuf, n * h->F, hipMemcpyDeviceToHost);
             if (e == hipSuccess)
@@ -612,6 +713,13 @@ moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_
         e = hipMemcpy(sorted_ids, w + L.sorted_ids, 4 * R, hipMemcpyDeviceToHost);
     if (e == hipSuccess && sorted_probs && R)
         e = hipMemcpy(sorted_probs, w + L.sorted_probs, 4 * R, hipMemcpyDeviceToHost);
+    if (h->precision == MOE_INT8) {
+        if (e == hipSuccess && x_codes && T)
+            e = hipMemcpy2D(x_codes, h->H, w + L.xq, int8_pitch(h->H), h->H, T, hipMemcpyDeviceToHost);
+        if (e == hipSuccess && x_scales && T) e = hipMemcpy(x_scales, w + L.xs, 4 * T, hipMemcpyDeviceToHost);
+        if (e != hipSuccess) return hip_fail(e, "moe_get_rows: copy");
+        return MOE_OK;
+    }
     if (e == hipSuccess && x_codes && T)
         e = hipMemcpy(x_codes, w + L.xq, T * h->H, hipMemcpyDeviceToHost);
     if (e == hipSuccess && x_scales && T)
