@@ -82,6 +82,10 @@ typedef enum {
                                          rows ran past 0.2 s (workgroups not all
                                          resident, e.g. other work on the GPU): the
                                          outputs of that call are invalid            */
+#define MOE_DEVERR_NO_ROWS 32u        /* moe_probs_backward: the workspace holds no forward of
+                                         this shape and capacity: nothing was written   */
+#define MOE_DEVERR_WEIGHTED_ROWS 64u  /* moe_probs_backward: the forward applied the
+                                         probabilities inside FC1: nothing was written  */
 
 /* Create a handle for E experts, hidden size H, expert FFN size F, top-k.
  * Checks (Megatron-LM PR #7830, construction-time validation; cudnn-frontend
@@ -304,6 +308,82 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
 moe_status moe_forward_noalloc(moe_handle h, const void* x, const int32_t* expert_ids,
                                const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
                                int combine, void* out, hipStream_t stream);
+
+/* Workspace bytes of moe_balance for a token capacity T_cap (0 for a NULL
+ * handle or a negative T_cap): caller-owned, no required initial contents, not
+ * shared with a call that may overlap in time. */
+size_t moe_balance_workspace_bytes(moe_handle h, int64_t T_cap);
+
+/* Balance loss, z loss and per-expert counts of the router (training).  Over
+ * the counted tokens (live, and with a nonzero token_mask entry if there is a
+ * mask), N of them, with p_t the softmax of token t's E logits:
+ *   counts[e]    = number of their routes to expert e (ids outside [0, E) are
+ *                  left out); counts[E] = N
+ *   prob_sums[e] = sum_t p_t[e]
+ *   losses[0]    = E / (topk N^2) sum_e counts[e] prob_sums[e]   (balance; 1 when
+ *                  every expert has the same share of both)
+ *   losses[1]    = 1 / N sum_t logsumexp(logits[t])^2            (z loss)
+ * both 0 for N = 0.  A token whose logits are all -inf is counted and adds
+ * nothing to prob_sums or the z loss; a NaN or +inf logit of a counted token
+ * makes prob_sums and the losses NaN.
+ *   logits: fp32 [T_cap][E]; expert_ids: int32 [T_cap][topk]; token_mask: uint8
+ *   [T_cap] or NULL; losses: fp32 [2]; counts: int32 [E + 1]; prob_sums: fp32
+ *   [E], all written whole.  live_rows_dev as everywhere (clamped here without
+ *   an error bit: moe_route and moe_forward report it).  ws_bytes >=
+ *   moe_balance_workspace_bytes(h, T_cap).
+ * The sums are fp32 in an order fixed by T_cap, E and the GPU, so repeated
+ * calls give the same bits.  For losses over several GPUs or micro-batches, add
+ * their counts and prob_sums up (the losses follow by the formulas) and give
+ * the summed counts to moe_route_backward.
+ * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer other than a NULL
+ * mask, T_cap outside [0, 2^26], ws_bytes too small), MOE_ERR_HIP. */
+moe_status moe_balance(moe_handle h, const float* logits, const int32_t* expert_ids, int64_t T_cap,
+                       const int32_t* live_rows_dev, const uint8_t* token_mask, float* losses,
+                       int32_t* counts, float* prob_sums, void* ws, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* Gradient of the router's logits (training): of the probabilities that
+ * moe_route returned, of moe_balance's losses, or of both, in one pass.
+ *   d_logits[t][e] = d_losses[0] E / (topk N^2) p_t[e] (counts[e] - sum_i p_t[i] counts[i])
+ *                  + d_losses[1] 2 logsumexp(logits[t]) / N p_t[e]
+ *                  + sum over routes j with id e: probs[t][j] (d_probs[t][j]
+ *                      - sum_i probs[t][i] d_probs[t][i])
+ * with N = counts[E]; the first two terms for counted tokens only (moe_balance),
+ * the last for every live one.  A route whose id is outside [0, E) or repeats
+ * an earlier one of its token is left out of the sums.
+ *   logits, expert_ids, token_mask: as given to moe_route and moe_balance;
+ *   probs, d_probs: fp32 [T_cap][topk], both or neither (then expert_ids may be
+ *   NULL); counts: int32 [E + 1] and d_losses: fp32 [2] (device), both or
+ *   neither; d_logits: fp32 [T_cap][E], may not overlap an input.  Rows of live
+ *   tokens are written whole, rows >= live not at all.  Every row's bits are
+ *   independent of the other rows, given the counts.
+ * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer, half a pair, neither
+ * pair, T_cap outside [0, 2^26]), MOE_ERR_HIP. */
+moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* expert_ids,
+                              const float* probs, const float* d_probs, int64_t T_cap,
+                              const int32_t* live_rows_dev, const uint8_t* token_mask,
+                              const int32_t* counts, const float* d_losses, float* d_logits,
+                              hipStream_t stream);
+
+/* Gradient of the probabilities given to moe_forward / moe_forward_ex
+ * (training), from the fp32 FC2 rows O that it left in its workspace:
+ *   d_probs[t][j] = sum_m d_out[t][m] O(t, j)[m]   (fp32),
+ * 0 for a dropped route, for the live tokens of that forward; other rows are
+ * not written.  The rows are the last forward's on ws, in any precision and
+ * combine; with MOE_APPLY_TOPK_IN_FC1 they carry their probabilities and the
+ * call flags MOE_DEVERR_WEIGHTED_ROWS.  A workspace whose last forward had
+ * another shape, precision or T_cap (or none) is flagged MOE_DEVERR_NO_ROWS.
+ * Both are reported by moe_check, added to the forward's bits, and nothing is
+ * written then.
+ *   d_out: [T_cap][H], fp32 (combine MOE_COMBINE_FP32) or bf16
+ *   (MOE_COMBINE_BF16); expert_ids: as given to that forward; d_probs: fp32
+ *   [T_cap][topk], in the order of expert_ids.
+ * Errors: MOE_ERR_INVALID_ARG (another combine, NULL or misaligned pointer,
+ * T_cap outside [0, 2^26], ws_bytes below moe_workspace_bytes(h, T_cap)),
+ * MOE_ERR_HIP. */
+moe_status moe_probs_backward(moe_handle h, const void* d_out, int combine,
+                              const int32_t* expert_ids, int64_t T_cap, float* d_probs, void* ws,
+                              size_t ws_bytes, hipStream_t stream);
 
 /* Copy the permutation of the last forward to host arrays (synchronizes the
  * stream).  The grouping is cudnn-frontend PR #448's route index (MoeEp class

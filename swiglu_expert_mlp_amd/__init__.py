@@ -20,7 +20,8 @@ import ctypes
 import os
 
 __all__ = ["MoE", "lib", "LIB_PATH", "MoEError", "DEVERR_BAD_EXPERT_ID", "DEVERR_DUP_EXPERT_ID",
-           "DEVERR_LIVE_ABOVE_CAP", "DEVERR_LIVE_NEGATIVE", "DEVERR_FUSED_WAIT"]
+           "DEVERR_LIVE_ABOVE_CAP", "DEVERR_LIVE_NEGATIVE", "DEVERR_FUSED_WAIT", "DEVERR_NO_ROWS",
+           "DEVERR_WEIGHTED_ROWS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -32,6 +33,8 @@ DEVERR_DUP_EXPERT_ID = 2
 DEVERR_LIVE_ABOVE_CAP = 4
 DEVERR_LIVE_NEGATIVE = 8
 DEVERR_FUSED_WAIT = 16
+DEVERR_NO_ROWS = 32
+DEVERR_WEIGHTED_ROWS = 64
 MOE_ERR_DEVICE_CONTRACT = -5
 # moe_forward_ex combines (moe_combine in include/moe.h)
 COMBINES = {"fp32": 0, "bf16": 1, "rows": 2}
@@ -58,6 +61,11 @@ _SIGNATURES = {
                                       ctypes.c_size_t, _P]),
     "moe_forward_noalloc": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int, _P,
                                            _P]),
+    "moe_balance_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int64]),
+    "moe_balance": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_route_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int64] + [_P] * 6),
+    "moe_probs_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int64, _P, _P,
+                                          ctypes.c_size_t, _P]),
     "moe_get_indices": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P]),
     "moe_get_rows": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P]),
     "moe_check": (ctypes.c_int, [_P, _P, _P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -279,6 +287,91 @@ class MoE:
                                          _stream(stream)), "moe_forward_noalloc")
         return out
 
+    # ------------------------------------------------------------- training the router
+
+    def new_balance_workspace(self, T_cap: int, device=None):
+        """A workspace of balance for capacity T_cap (no initial contents are required)."""
+        torch = _torch()
+        return torch.empty(int(lib().moe_balance_workspace_bytes(self._h, int(T_cap))), dtype=torch.uint8,
+                           device=device or "cuda")
+
+    def _mask(self, mask, T_cap: int):
+        torch = _torch()
+        return None if mask is None else _dev(mask, "mask", (torch.bool, torch.uint8), (T_cap,))
+
+    def _balance_args(self, logits, ids, live, losses, counts, prob_sums, ws, mask, stream):
+        torch = _torch()
+        T_cap = logits.shape[0]
+        return (self._h, _dev(logits, "logits", (torch.float32,), (T_cap, self.E)),
+                _dev(ids, "ids", (torch.int32,), (T_cap, self.topk)), T_cap,
+                _dev(live, "live", (torch.int32,)), self._mask(mask, T_cap),
+                _dev(losses, "losses", (torch.float32,), (2,)),
+                _dev(counts, "counts", (torch.int32,), (self.E + 1,)),
+                _dev(prob_sums, "prob_sums", (torch.float32,), (self.E,)),
+                _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
+
+    def balance(self, logits, ids, live, mask=None, losses=None, counts=None, prob_sums=None, ws=None,
+                stream=None):
+        """Balance loss, z loss and per-expert counts (moe_balance): losses fp32 [2], counts
+        int32 [E + 1] (the last entry the counted tokens) and prob_sums fp32 [E].
+        mask: bool or uint8 [T_cap], tokens with 0 are left out."""
+        torch = _torch()
+        dev = logits.device
+        if losses is None:
+            losses = torch.empty(2, dtype=torch.float32, device=dev)
+        if counts is None:
+            counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+        if prob_sums is None:
+            prob_sums = torch.empty(self.E, dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = self.new_balance_workspace(logits.shape[0], dev)
+        _check(lib().moe_balance(*self._balance_args(logits, ids, live, losses, counts, prob_sums, ws, mask,
+                                                     stream)), "moe_balance")
+        return losses, counts, prob_sums
+
+    def _route_backward_args(self, logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask, stream):
+        torch = _torch()
+        T_cap = logits.shape[0]
+        f32, i32 = (torch.float32,), (torch.int32,)
+        opt = lambda t, name, dt, shape: None if t is None else _dev(t, name, dt, shape)
+        return (self._h, _dev(logits, "logits", f32, (T_cap, self.E)),
+                opt(ids, "ids", i32, (T_cap, self.topk)), opt(probs, "probs", f32, (T_cap, self.topk)),
+                opt(d_probs, "d_probs", f32, (T_cap, self.topk)), T_cap, _dev(live, "live", i32),
+                self._mask(mask, T_cap), opt(counts, "counts", i32, (self.E + 1,)),
+                opt(d_losses, "d_losses", f32, (2,)), _dev(d_logits, "d_logits", f32, (T_cap, self.E)),
+                _stream(stream))
+
+    def route_backward(self, logits, ids, live, probs=None, d_probs=None, counts=None, d_losses=None, mask=None,
+                       d_logits=None, stream=None):
+        """Gradient of the logits (moe_route_backward), fp32 [T_cap, E]: of the probabilities
+        (probs with d_probs), of balance's losses (counts with d_losses, fp32 [2]), or of both."""
+        torch = _torch()
+        if d_logits is None:
+            d_logits = torch.empty_like(logits)
+        _check(lib().moe_route_backward(*self._route_backward_args(logits, ids, live, d_logits, probs, d_probs,
+                                                                   counts, d_losses, mask, stream)),
+               "moe_route_backward")
+        return d_logits
+
+    def _probs_backward_args(self, d_out, ids, d_probs, ws, stream):
+        torch = _torch()
+        T_cap = d_out.shape[0]
+        p = _dev(d_out, "d_out", (torch.float32, torch.bfloat16), (T_cap, self.H))
+        return (self._h, p, COMBINES["fp32" if d_out.dtype == torch.float32 else "bf16"],
+                _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk)), T_cap,
+                _dev(d_probs, "d_probs", (torch.float32,), (T_cap, self.topk)),
+                _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
+
+    def probs_backward(self, d_out, ids, ws, d_probs=None, stream=None):
+        """Gradient of the probabilities of the last forward on ws (moe_probs_backward), fp32
+        [T_cap, topk], from d_out [T_cap, H] (fp32 or bf16) and that forward's expert ids."""
+        torch = _torch()
+        if d_probs is None:
+            d_probs = torch.empty((d_out.shape[0], self.topk), dtype=torch.float32, device=d_out.device)
+        _check(lib().moe_probs_backward(*self._probs_backward_args(d_out, ids, d_probs, ws, stream)),
+               "moe_probs_backward")
+        return d_probs
+
     # ------------------------------------------------------------- inspection
 
     def get_indices(self, ws, T_cap: int, stream=None) -> dict:
@@ -396,6 +489,31 @@ class MoE:
             _check(fn(*args), "moe_route")
         call.keep = keep
         return call
+
+    @staticmethod
+    def _bound(fn, what, args, keep):
+        def call():
+            _check(fn(*args), what)
+        call.keep = keep
+        return call
+
+    def bind_balance(self, logits, ids, live, losses, counts, prob_sums, ws, mask=None, stream=None):
+        """As bind_forward, for balance."""
+        args = self._balance_args(logits, ids, live, losses, counts, prob_sums, ws, mask, stream)
+        return self._bound(lib().moe_balance, "moe_balance", args,
+                           (self, logits, ids, live, losses, counts, prob_sums, ws, mask))
+
+    def bind_route_backward(self, logits, ids, live, d_logits, probs=None, d_probs=None, counts=None,
+                            d_losses=None, mask=None, stream=None):
+        """As bind_forward, for route_backward."""
+        args = self._route_backward_args(logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask, stream)
+        return self._bound(lib().moe_route_backward, "moe_route_backward", args,
+                           (self, logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask))
+
+    def bind_probs_backward(self, d_out, ids, d_probs, ws, stream=None):
+        """As bind_forward, for probs_backward."""
+        args = self._probs_backward_args(d_out, ids, d_probs, ws, stream)
+        return self._bound(lib().moe_probs_backward, "moe_probs_backward", args, (self, d_out, ids, d_probs, ws))
 
     def check(self, ws, stream=None) -> int:
         """moe_check: the contract-violation bits (DEVERR_*) of the last route and

@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -56,6 +58,8 @@ constexpr uint32_t kErrDupId = 2u;
 constexpr uint32_t kErrLiveHigh = 4u;
 constexpr uint32_t kErrLiveNeg = 8u;
 constexpr uint32_t kErrFusedWait = 16u;
+constexpr uint32_t kErrNoRows = 32u;
+constexpr uint32_t kErrWeightedRows = 64u;
 
 // ---------------------------------------------------------------- formats
 
@@ -197,8 +201,23 @@ struct WsHeader {
     int32_t n_tiles;       // M tiles in the tile table
     int32_t n_rows;        // routed rows with a valid expert
     int32_t n_tiles_big;   // M tiles in the LDS-staged table
-    int32_t pad[58];
+    uint64_t tag;          // layout of the last forward (forward_tag)
+    int32_t weighted;      // 1: its FC2 rows carry their probabilities (applied inside FC1)
+    int32_t pad[55];
 };
+
+// Identifies a workspace layout: a workspace whose header holds this tag was last
+// used by a forward of this shape and capacity, so its regions are where the
+// caller's layout says.
+inline uint64_t forward_tag(int E, int H, int F, int k, int precision, int64_t T_cap)
+{
+    uint64_t v = 0x9e3779b97f4a7c15ull;
+    for (uint64_t x : {(uint64_t)E, (uint64_t)H, (uint64_t)F, (uint64_t)k, (uint64_t)precision, (uint64_t)T_cap}) {
+        v = (v ^ x) * 0xff51afd7ed558ccdull;
+        v ^= v >> 32;
+    }
+    return v;
+}
 
 static_assert(sizeof(WsHeader) == 256, "header is one 256-byte block");
 

@@ -17,7 +17,17 @@ hipError_t launch_route(const float* logits, int64_t T_cap, const int32_t* live,
                         int32_t* ids, float* probs, WsHeader* hdr, int num_cu, hipStream_t s);
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out);
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted);
+size_t balance_ws_bytes(int E, int64_t T_cap);
+hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap, const int32_t* live,
+                          const uint8_t* mask, int E, int k, float* losses, int32_t* counts, float* prob_sums,
+                          char* ws, int num_cu, hipStream_t s);
+hipError_t launch_route_backward(const float* logits, const int32_t* ids, const float* probs, const float* d_probs,
+                                 int64_t T_cap, const int32_t* live, const uint8_t* mask, const int32_t* counts,
+                                 const float* d_losses, float* d_logits, int E, int k, int num_cu, hipStream_t s);
+hipError_t launch_probs_backward(const WsHeader* hdr, uint64_t tag, const float* O, const int32_t* dst,
+                                 const int32_t* ids, const void* d_out, int bf16, float* d_probs, int64_t T_cap, int k,
+                                 int H, int num_cu, hipStream_t s);
 hipError_t launch_finalize(const float* O, const int32_t* dst, const float* sorted_probs,
                            int64_t T_cap, const int32_t* live, int k, int H, int mode, void* out,
                            int num_cu, hipStream_t s);
@@ -356,6 +366,95 @@ moe_status moe_route(moe_handle h, const float* logits, int64_t T_cap,
     return MOE_OK;
 }
 
+size_t moe_balance_workspace_bytes(moe_handle h, int64_t T_cap)
+{
+    if (!h || T_cap < 0) return 0;
+    return balance_ws_bytes(h->E, T_cap);
+}
+
+moe_status moe_balance(moe_handle h, const float* logits, const int32_t* expert_ids, int64_t T_cap,
+                       const int32_t* live_rows_dev, const uint8_t* token_mask, float* losses,
+                       int32_t* counts, float* prob_sums, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_balance: NULL handle");
+    if (T_cap < 0 || T_cap > (int64_t)1 << 26)
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance: T_cap=%lld out of range", (long long)T_cap);
+    if (!logits || !expert_ids || !live_rows_dev || !losses || !counts || !prob_sums || !ws)
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance: NULL pointer");
+    if (!aligned16(logits) || !aligned16(expert_ids) || !aligned16(token_mask) || !aligned16(losses) ||
+        !aligned16(counts) || !aligned16(prob_sums) || !aligned16(ws))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance: pointers must be 16-byte aligned");
+    if (ws_bytes < balance_ws_bytes(h->E, T_cap))
+        return fail(MOE_ERR_INVALID_ARG, "moe_balance: ws_bytes %zu < %zu for T_cap=%lld", ws_bytes,
+                    balance_ws_bytes(h->E, T_cap), (long long)T_cap);
+    moe_status st = ensure_device(h);
+    if (st != MOE_OK) return st;
+    const hipError_t e = launch_balance(logits, expert_ids, T_cap, live_rows_dev, token_mask, h->E, h->k, losses,
+                                        counts, prob_sums, (char*)ws, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_balance: launch");
+    return MOE_OK;
+}
+
+moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* expert_ids,
+                              const float* probs, const float* d_probs, int64_t T_cap,
+                              const int32_t* live_rows_dev, const uint8_t* token_mask,
+                              const int32_t* counts, const float* d_losses, float* d_logits,
+                              hipStream_t stream)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL handle");
+    if (T_cap < 0 || T_cap > (int64_t)1 << 26)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: T_cap=%lld out of range", (long long)T_cap);
+    if (!logits || !live_rows_dev || !d_logits)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL pointer");
+    if (!probs != !d_probs || (d_probs && !expert_ids))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_probs needs expert_ids and probs, and probs d_probs");
+    if (!counts != !d_losses)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_losses needs counts, and counts d_losses");
+    if (!d_probs && !d_losses)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: neither d_probs nor d_losses");
+    if (logits == d_logits)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_logits must not be the logits");
+    for (const void* p : {(const void*)logits, (const void*)expert_ids, (const void*)probs, (const void*)d_probs,
+                          (const void*)token_mask, (const void*)counts, (const void*)d_losses, (const void*)d_logits})
+        if (!aligned16(p))
+            return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: pointers must be 16-byte aligned");
+    moe_status st = ensure_device(h);
+    if (st != MOE_OK) return st;
+    if (T_cap == 0) return MOE_OK;
+    const hipError_t e = launch_route_backward(logits, expert_ids, probs, d_probs, T_cap, live_rows_dev, token_mask,
+                                               counts, d_losses, d_logits, h->E, h->k, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_route_backward: launch");
+    return MOE_OK;
+}
+
+moe_status moe_probs_backward(moe_handle h, const void* d_out, int combine, const int32_t* expert_ids,
+                              int64_t T_cap, float* d_probs, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: NULL handle");
+    if (T_cap < 0 || T_cap > (int64_t)1 << 26)
+        return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: T_cap=%lld out of range", (long long)T_cap);
+    if (combine != MOE_COMBINE_FP32 && combine != MOE_COMBINE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: combine %d (fp32 and bf16 only)", combine);
+    if (!d_out || !expert_ids || !d_probs || !ws)
+        return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: NULL pointer");
+    if (!aligned16(d_out) || !aligned16(expert_ids) || !aligned16(d_probs) || !aligned16(ws))
+        return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: pointers must be 16-byte aligned");
+    const WsLayout L = layout_of(h, T_cap);
+    if (ws_bytes < L.total)
+        return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: ws_bytes %zu < %zu for T_cap=%lld", ws_bytes, L.total,
+                    (long long)T_cap);
+    moe_status st = ensure_device(h);
+    if (st != MOE_OK) return st;
+    if (T_cap == 0) return MOE_OK;
+    char* w = (char*)ws;
+    const hipError_t e =
+        launch_probs_backward((const WsHeader*)(w + L.hdr), forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap),
+                              (const float*)(w + L.obuf), (const int32_t*)(w + L.dst), expert_ids, d_out,
+                              combine == MOE_COMBINE_BF16, d_probs, T_cap, h->k, h->H, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_probs_backward: launch");
+    return MOE_OK;
+}
+
 moe_status moe_forward(moe_handle h, const void* x, const int32_t* expert_ids,
                        const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
                        float* out, void* ws, size_t ws_bytes, hipStream_t stream)
@@ -404,7 +503,8 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
     hipError_t e = mark(h, 0, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     e = launch_prep(expert_ids, probs, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream,
-                    h->H, combine, fused_fin ? out : nullptr);
+                    h->H, combine, fused_fin ? out : nullptr,
+                    forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap), fc1_topk ? 1 : 0);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: prep launch");
     if ((e = mark(h, 1, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     const int E = h->E, H = h->H, F = h->F;
@@ -752,11 +852,13 @@ moe_status moe_check(moe_handle h, void* ws, hipStream_t stream, uint32_t* err_b
     if (e != hipSuccess) return hip_fail(e, "moe_check: clear");
     if (*err_bits) {
         const uint32_t b = *err_bits;
-        return fail(MOE_ERR_DEVICE_CONTRACT, "moe_check: contract violations 0x%x:%s%s%s%s", b,
+        return fail(MOE_ERR_DEVICE_CONTRACT, "moe_check: contract violations 0x%x:%s%s%s%s%s%s", b,
                     (b & kErrBadId) ? " expert id outside [0, E) (route dropped);" : "",
                     (b & kErrDupId) ? " expert id repeated within a token (repeat dropped);" : "",
                     (b & kErrLiveHigh) ? " live count above capacity (clamped);" : "",
-                    (b & kErrLiveNeg) ? " negative live count (taken as 0);" : "");
+                    (b & kErrLiveNeg) ? " negative live count (taken as 0);" : "",
+                    (b & kErrNoRows) ? " probabilities' gradient without the forward's rows (not written);" : "",
+                    (b & kErrWeightedRows) ? " probabilities' gradient of rows weighted inside FC1 (not written);" : "");
     }
     return MOE_OK;
 }

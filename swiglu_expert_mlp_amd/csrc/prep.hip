@@ -98,6 +98,8 @@ struct PrepArgs {
     int fin_mode;            // combine: 0 fp32, 1 bf16, 2 rows
     void* fin_out;           // the forward's output (tokens with no kept route)
     WsHeader* hdr;
+    uint64_t tag;            // written to the header, with `weighted`
+    int weighted;
     int32_t* perm_src;
     int32_t* dst;
 };
@@ -247,6 +249,8 @@ __device__ void prep_finish(const PrepArgs& a, int T, int nch, int32_t live, int
         a.hdr->n_tiles_big = nbig;
         a.hdr->multi_tile = multi ? 1 : 0;
         a.hdr->n_rows = total;
+        a.hdr->tag = a.tag;
+        a.hdr->weighted = a.weighted;
     }
 }
 
@@ -424,9 +428,11 @@ __global__ void __launch_bounds__(256) prep_scatter_kernel(
 
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out)
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted)
 {
     PrepArgs a;
+    a.tag = tag;
+    a.weighted = weighted;
     a.fin_cnt = fin_out ? (int32_t*)(ws + L.fin_cnt) : nullptr;
     a.fin_nt = (fin_H + kFinCols - 1) / kFinCols;
     a.fin_H = fin_H;
