@@ -10,14 +10,14 @@
 #include <string>
 
 #include "../../include/moe.h"
-#include "common.h"
+#include "quant_int8.h"
 
 namespace moe {
 hipError_t launch_route(const float* logits, int64_t T_cap, const int32_t* live, int E, int k,
                         int32_t* ids, float* probs, WsHeader* hdr, int num_cu, hipStream_t s);
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted);
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x);
 size_t balance_ws_bytes(int E, int64_t T_cap);
 hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap, const int32_t* live,
                           const uint8_t* mask, int E, int k, float* losses, int32_t* counts, float* prob_sums,
@@ -39,8 +39,7 @@ void mx_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, s
 hipError_t launch_pack_mxfp4(const uint16_t* w1, const uint16_t* w2, uint8_t* kbuf, int E, int H,
                              int F, int num_cu, hipStream_t s);
 void mx4_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
-hipError_t launch_quant_rows_int8(const uint16_t* src, const int32_t* n_rows, int64_t cap, int K, int Kp,
-                                  uint8_t* codes, float* scales, int num_cu, hipStream_t s);
+hipError_t launch_quant_rows_int8(const QuantRows& a, int num_cu, hipStream_t s);
 hipError_t launch_pack_int8(const void* w1, const float* ws1, const void* w2, const float* ws2, int codes,
                             uint8_t* kbuf, int E, int H, int F, int num_cu, hipStream_t s);
 void int8_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
@@ -502,9 +501,13 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
     WsHeader* hdr = (WsHeader*)(w + L.hdr);
     hipError_t e = mark(h, 0, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: stage event");
+    // int8: x is quantized by extra workgroups of the permutation's launches
+    const QuantRows quant_x{(const uint16_t*)x, live_rows_dev, T_cap, h->H, int8_pitch(h->H),
+                            (uint8_t*)(w + L.xq), (float*)(w + L.xs)};
     e = launch_prep(expert_ids, probs, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream,
                     h->H, combine, fused_fin ? out : nullptr,
-                    forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap), fc1_topk ? 1 : 0);
+                    forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap), fc1_topk ? 1 : 0,
+                    h->precision == MOE_INT8 ? &quant_x : nullptr);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: prep launch");
     if ((e = mark(h, 1, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     const int E = h->E, H = h->H, F = h->F;
@@ -614,9 +617,6 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
         const int Kp1 = int8_pitch(H), Kp2 = int8_pitch(F);
         size_t b1, b2, b3, b4;
         int8_section_bytes(E, H, F, &b1, &b2, &b3, &b4);
-        e = launch_quant_rows_int8((const uint16_t*)x, live_rows_dev, T_cap, H, Kp1, (uint8_t*)(w + L.xq),
-                                   (float*)(w + L.xs), h->num_cu, stream);
-        if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-x launch");
         GemmArgs g1{};
         g1.A = (const uint16_t*)(w + L.xq);
         g1.W = (const uint16_t*)h->kbuf;
@@ -640,8 +640,8 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
         g1.w_scale = (const float*)(h->kbuf + b1 + b2);
         e = launch_gemm_int8(true, g1, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
         if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1 launch");
-        e = launch_quant_rows_int8((const uint16_t*)(w + L.hbuf), &hdr->n_rows, T_cap * h->k, F, Kp2,
-                                   (uint8_t*)(w + L.hq), (float*)(w + L.hscale), h->num_cu, stream);
+        e = launch_quant_rows_int8(QuantRows{(const uint16_t*)(w + L.hbuf), &hdr->n_rows, T_cap * h->k, F, Kp2,
+                                             (uint8_t*)(w + L.hq), (float*)(w + L.hscale)}, h->num_cu, stream);
         if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-h launch");
         GemmArgs g2 = g1;
         g2.A = (const uint16_t*)(w + L.hq);

@@ -28,7 +28,11 @@
 // the workspace, so a new workspace needs no initialisation.
 // A route whose id is outside [0, E), or repeats an id already listed for the
 // token (contract violations), is dropped: it has no row and dst = -1.
-#include "common.h"
+// int8 experts: the quantization of x needs nothing of the permutation, and the
+// permutation's launches leave most of the GPU idle, so its rows are extra
+// workgroups of the single-chunk launch, or of prep_finish's (64 tokens, hidden
+// 128: 26.6 -> @T us per forward; 256 tokens, hidden 2048: 90.0 -> @D us).
+#include "quant_int8.h"
 
 namespace moe {
 
@@ -254,8 +258,9 @@ __device__ void prep_finish(const PrepArgs& a, int T, int nch, int32_t live, int
     }
 }
 
+// The first `chunks` workgroups of the launch, a 256-token chunk each.
 template <int K>
-__global__ void __launch_bounds__(256) prep_kernel(PrepArgs a)
+__device__ __forceinline__ void prep_chunk(const PrepArgs& a, int chunks)
 {
     __shared__ uint32_t bm[kMaxExperts * (kChunkTok / 32)];
     __shared__ int lds[96];
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(256) prep_kernel(PrepArgs a)
     const int T = clamp_live(live, a.T_cap);
     const int nch = (T + kChunkTok - 1) / kChunkTok;
     const int E = a.E;
-    const bool single = gridDim.x == 1;          // T_cap <= one chunk
+    const bool single = chunks == 1;             // T_cap <= one chunk
     if (c >= nch && !single) return;
     for (int i = threadIdx.x; i < E * (kChunkTok / 32); i += blockDim.x) bm[i] = 0;
     const bool valid = t < T;
@@ -394,9 +399,33 @@ __global__ void __launch_bounds__(256) prep_kernel(PrepArgs a)
     if (threadIdx.x == 0) a.chunk_err[c] = ce;
 }
 
+template <int K>
+__global__ void __launch_bounds__(256) prep_kernel(PrepArgs a)
+{
+    prep_chunk<K>(a, gridDim.x);
+}
+
+// x rows of the int8 experts, by the workgroups after the launch's own
+__device__ __forceinline__ void quant_x_rows(const QuantRows& q)
+{
+    const int b = blockIdx.x - 1, n = gridDim.x - 1;
+    if (q.Kp <= 512) quant_rows<64, 1>(q, b, n);
+    else if (q.Kp <= 1024) quant_rows<64, 2>(q, b, n);
+    else if (q.Kp <= 2048) quant_rows<64, 4>(q, b, n);
+    else if (q.Kp <= 4096) quant_rows<64, 8>(q, b, n);
+    else quant_rows<64, 0>(q, b, n);
+}
+
+template <int K>
+__global__ void __launch_bounds__(256) prep_quant_kernel(PrepArgs a, QuantRows q)
+{
+    if (blockIdx.x == 0) prep_chunk<K>(a, 1);
+    else quant_x_rows(q);
+}
+
 // The prefix over every chunk's counts, run as its own single-workgroup launch
 // once every prep_kernel workgroup has written its chunk (stream order).
-__global__ void __launch_bounds__(256) prep_finish_kernel(PrepArgs a)
+__device__ __forceinline__ void prep_finish_all(const PrepArgs& a)
 {
     __shared__ int slab[kSlab];
     __shared__ int lds[96];
@@ -404,6 +433,14 @@ __global__ void __launch_bounds__(256) prep_finish_kernel(PrepArgs a)
     const int T = clamp_live(live, a.T_cap);
     const int nch = (T + kChunkTok - 1) / kChunkTok;
     prep_finish(a, T, nch, live, lds, slab);
+}
+
+__global__ void __launch_bounds__(256) prep_finish_kernel(PrepArgs a) { prep_finish_all(a); }
+
+__global__ void __launch_bounds__(256) prep_finish_quant_kernel(PrepArgs a, QuantRows q)
+{
+    if (blockIdx.x == 0) prep_finish_all(a);
+    else quant_x_rows(q);
 }
 
 __global__ void __launch_bounds__(256) prep_scatter_kernel(
@@ -428,7 +465,7 @@ __global__ void __launch_bounds__(256) prep_scatter_kernel(
 
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted)
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x)
 {
     PrepArgs a;
     a.tag = tag;
@@ -457,9 +494,19 @@ hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, co
     a.perm_src = (int32_t*)(ws + L.perm_src);
     a.dst = (int32_t*)(ws + L.dst);
     dim3 g1((unsigned)L.nchunks), b1(256);
+    // quantization: a workgroup per four rows, four resident a CU (40 KB of LDS each)
+    dim3 gq(1);
+    if (quant_x) {
+        const int64_t b = (T_cap + 3) / 4, most = (int64_t)num_cu * 4;
+        gq = dim3((unsigned)(1 + (b < most ? b : most)));
+    }
+    const bool quant_here = quant_x && L.nchunks == 1;
 #define PREP_CASE(KK)                                                        \
     case KK:                                                                 \
-        hipLaunchKernelGGL(prep_kernel<KK>, g1, b1, 0, s, a);                \
+        if (quant_here)                                                      \
+            hipLaunchKernelGGL(prep_quant_kernel<KK>, gq, b1, 0, s, a, *quant_x); \
+        else                                                                 \
+            hipLaunchKernelGGL(prep_kernel<KK>, g1, b1, 0, s, a);            \
         break;
     switch (k) {
         PREP_CASE(1) PREP_CASE(2) PREP_CASE(3) PREP_CASE(4) PREP_CASE(5) PREP_CASE(6)
@@ -469,7 +516,10 @@ hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, co
     }
 #undef PREP_CASE
     if (L.nchunks == 1) return hipGetLastError();   // single workgroup scattered its routes
-    hipLaunchKernelGGL(prep_finish_kernel, dim3(1), dim3(256), 0, s, a);
+    if (quant_x)
+        hipLaunchKernelGGL(prep_finish_quant_kernel, gq, dim3(256), 0, s, a, *quant_x);
+    else
+        hipLaunchKernelGGL(prep_finish_kernel, dim3(1), dim3(256), 0, s, a);
     int64_t R = T_cap * k;
     int64_t blocks = (R + 255) / 256;
     if (blocks > (int64_t)num_cu * 4) blocks = (int64_t)num_cu * 4;

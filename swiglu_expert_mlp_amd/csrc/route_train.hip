@@ -250,18 +250,21 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(BalanceArgs a)
     }
 }
 
-// Second launch: a workgroup sums the partials of 64 experts (a lane each, the
-// waves every 16th partial); the last one to finish adds the workgroups' parts of
-// the loss in their order.  Its ticket starts at zero in every call: the first
-// launch clears it.
+// Second launch: a workgroup sums the partials of EP experts, 1024 / EP threads an
+// expert.  With more than one workgroup (E above EP) the last one to finish adds
+// their parts of the loss in order; the ticket that tells starts at zero in every
+// call: the first launch clears it.  A release at device scope writes the L2 back,
+// so up to 128 experts one workgroup takes them all.
+template <int EP>
 __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalanceArgs a, int blocks)
 {
-    __shared__ float ps[kBalWaves][kWave];
-    __shared__ int cs[kBalWaves][kWave];
+    constexpr int PER = kBalThreads / EP;       // threads per expert
+    __shared__ float ps[PER][EP];
+    __shared__ int cs[PER][EP];
     __shared__ float lds_f[kBalWaves];
     __shared__ int lds_i[kBalWaves];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int E = a.E, e = blockIdx.x * kWave + lane, ec = e < E ? e : E - 1;
+    const int E = a.E, x = threadIdx.x % EP, y = threadIdx.x / EP;
+    const int e = blockIdx.x * EP + x, ec = e < E ? e : E - 1;
     float zb = 0.0f;
     int nb = 0;
     if (threadIdx.x < (unsigned)blocks) {        // blocks <= kBalMaxBlocks < the workgroup
@@ -270,43 +273,43 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalanceArgs
     }
     float s = 0.0f;
     int c = 0;
-#pragma unroll 8
-    for (int b = wv; b < blocks; b += kBalWaves) {
+#pragma unroll 16
+    for (int b = y; b < blocks; b += PER) {
         s += a.part_p[(int64_t)b * E + ec];
         c += a.part_c[(int64_t)b * E + ec];
     }
-    ps[wv][lane] = s;
-    cs[wv][lane] = c;
+    ps[y][x] = s;
+    cs[y][x] = c;
     const float z = block_sum<kBalWaves>(wave_sum(zb), lds_f);
     const int n = block_sum<kBalWaves>(wave_sum(nb), lds_i);
-    if (wv == 0) {
+    float dot = 0.0f;
+    if (threadIdx.x < EP) {
         s = 0.0f;
         c = 0;
 #pragma unroll
-        for (int w = 0; w < kBalWaves; ++w) {
-            s += ps[w][lane];
-            c += cs[w][lane];
+        for (int w = 0; w < PER; ++w) {
+            s += ps[w][x];
+            c += cs[w][x];
         }
         if (e < E) {
             a.prob_sums[e] = s;
             a.counts[e] = c;
+            dot = (float)c * s;
         }
-        const float dot = wave_sum(e < E ? (float)c * s : 0.0f);
-        if (lane == 0) {
-            if (gridDim.x == 1) {
-                write_losses(a, dot, z, n);
-            } else {
-                __hip_atomic_store(&a.part_dot[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                const uint32_t before =
-                    __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-                if (before == gridDim.x - 1) {
-                    float d = 0.0f;
-                    for (unsigned g = 0; g < gridDim.x; ++g)
-                        d += __hip_atomic_load(&a.part_dot[g], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    write_losses(a, d, z, n);
-                }
-            }
-        }
+    }
+    dot = block_sum<kBalWaves>(wave_sum(dot), lds_f);
+    if (threadIdx.x != 0) return;
+    if (gridDim.x == 1) {
+        write_losses(a, dot, z, n);
+        return;
+    }
+    __hip_atomic_store(&a.part_dot[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (before == gridDim.x - 1) {
+        float d = 0.0f;
+        for (unsigned g = 0; g < gridDim.x; ++g)
+            d += __hip_atomic_load(&a.part_dot[g], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        write_losses(a, d, z, n);
     }
 }
 
@@ -366,9 +369,13 @@ hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap
     hipLaunchKernelGGL((balance_kernel<LPT, N, VEC>), dim3((unsigned)blocks), dim3(kBalThreads), 0, s, a)
     ROW_DISPATCH(E, BALANCE);
 #undef BALANCE
-    if (blocks > 1)
-        hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)((E + kWave - 1) / kWave)), dim3(kBalThreads), 0, s, a,
-                           (int)blocks);
+    if (blocks > 1) {
+        if (E > 64 && E <= 128)
+            hipLaunchKernelGGL(balance_finish_kernel<128>, dim3(1), dim3(kBalThreads), 0, s, a, (int)blocks);
+        else
+            hipLaunchKernelGGL(balance_finish_kernel<64>, dim3((unsigned)((E + 63) / 64)), dim3(kBalThreads), 0, s, a,
+                               (int)blocks);
+    }
     return hipGetLastError();
 }
 
