@@ -41,31 +41,33 @@ __global__ void __launch_bounds__(512, 1) gemm_int8_big_kernel(GemmArgs g)
     big_tiles<OpInt8, FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
 }
 
-// One GEMM stage: the 256-row launch (unless the 64-row kernel takes its tiles),
-// then the 64-row launch.  t0 / t1 as launch_gemm_bf16.
+// One GEMM stage: the 256-row launch on s (unless the 64-row kernel takes its
+// tiles), the 64-row launch on s_small (s if null).  t0 / t1 as launch_gemm_bf16.
 hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
-                            hipEvent_t t1)
+                            hipEvent_t t1, hipStream_t s_small)
 {
     if (!g.a_scale || !g.w_scale || g.K < 32 || g.K % 32 != 0 || g.N < 32 || g.N % 32 != 0)
         return hipErrorInvalidValue;
     const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
-    auto go = [&](auto kernel, hipEvent_t e0, hipEvent_t e1) {
+    auto go = [&](auto kernel, hipEvent_t e0, hipEvent_t e1, hipStream_t st) {
         if (e0 || e1)
-            hipExtLaunchKernelGGL(kernel, grid, block, 0, s, e0, e1, 0, g);
+            hipExtLaunchKernelGGL(kernel, grid, block, 0, st, e0, e1, 0, g);
         else
-            hipLaunchKernelGGL(kernel, grid, block, 0, s, g);
+            hipLaunchKernelGGL(kernel, grid, block, 0, st, g);
     };
     const bool prob = fc1 && g.row_prob != nullptr;
     hipEvent_t small_start = t0;
+    hipStream_t ss = s;
     if (!g.small_takes_big) {
-        if (prob) go(gemm_int8_big_kernel<true, true>, t0, nullptr);
-        else if (fc1) go(gemm_int8_big_kernel<true, false>, t0, nullptr);
-        else go(gemm_int8_big_kernel<false, false>, t0, nullptr);
+        if (prob) go(gemm_int8_big_kernel<true, true>, t0, nullptr, s);
+        else if (fc1) go(gemm_int8_big_kernel<true, false>, t0, nullptr, s);
+        else go(gemm_int8_big_kernel<false, false>, t0, nullptr, s);
         small_start = nullptr;
+        if (s_small) ss = s_small;
     }
-    if (prob) go(gemm_int8_small_kernel<true, true>, small_start, t1);
-    else if (fc1) go(gemm_int8_small_kernel<true, false>, small_start, t1);
-    else go(gemm_int8_small_kernel<false, false>, small_start, t1);
+    if (prob) go(gemm_int8_small_kernel<true, true>, small_start, t1, ss);
+    else if (fc1) go(gemm_int8_small_kernel<true, false>, small_start, t1, ss);
+    else go(gemm_int8_small_kernel<false, false>, small_start, t1, ss);
     return hipGetLastError();
 }
 

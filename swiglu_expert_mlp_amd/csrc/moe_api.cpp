@@ -39,7 +39,7 @@ void mx_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, s
 hipError_t launch_pack_mxfp4(const uint16_t* w1, const uint16_t* w2, uint8_t* kbuf, int E, int H,
                              int F, int num_cu, hipStream_t s);
 void mx4_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
-hipError_t launch_quant_rows_int8(const QuantRows& a, int num_cu, hipStream_t s);
+hipError_t launch_quant_rows_int8(const QuantRows& a, const QuantTiles* tiles, int num_cu, hipStream_t s);
 hipError_t launch_pack_int8(const void* w1, const float* ws1, const void* w2, const float* ws2, int codes,
                             uint8_t* kbuf, int E, int H, int F, int num_cu, hipStream_t s);
 void int8_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
@@ -55,7 +55,7 @@ hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
                                   hipEvent_t t0, hipEvent_t t1);
 hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
-                            hipEvent_t t1);
+                            hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_mxfp8(bool fc1, bool w4, const MxGemmArgs& g, int num_cu, hipStream_t s,
                              hipEvent_t t0, hipEvent_t t1);
 }  // namespace moe
@@ -205,7 +205,7 @@ static moe_status scratch_of_current_device(void** out)
     return MOE_OK;
 }
 
-// Side stream of the bf16 forward above a 1024-token capacity, where a GEMM
+// Side stream of the bf16 and int8 forwards above a 1024-token capacity, where a GEMM
 // stage is a 256-row launch and a 64-row launch over disjoint experts: the
 // 64-row FC1 -> FC2 chain runs on the side stream while the 256-row chain runs
 // on the caller's, so the 64-row tiles fill the CUs the 256-row launch frees at
@@ -306,7 +306,8 @@ moe_status moe_load_weights(moe_handle h, const void* w1, const void* w2, void* 
                     moe_weight_bytes(h));
     moe_status st = ensure_device(h);
     if (st != MOE_OK) return st;
-    if (h->precision == MOE_BF16 && (st = ensure_side_stream(h->device)) != MOE_OK) return st;
+    if ((h->precision == MOE_BF16 || h->precision == MOE_INT8) && (st = ensure_side_stream(h->device)) != MOE_OK)
+        return st;
     const uint16_t* a = (const uint16_t*)w1;
     const uint16_t* b = (const uint16_t*)w2;
     uint8_t* kb = (uint8_t*)kbuf;
@@ -335,6 +336,7 @@ moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_sc
         return fail(MOE_ERR_INVALID_ARG, "moe_load_quantized: kbuf_bytes %zu < %zu", kbuf_bytes,
                     moe_weight_bytes(h));
     moe_status st = ensure_device(h);
+    if (st == MOE_OK) st = ensure_side_stream(h->device);
     if (st != MOE_OK) return st;
     const hipError_t e = launch_pack_int8(w1, w1_scale, w2, w2_scale, 1, (uint8_t*)kbuf, h->E, h->H, h->F,
                                           h->num_cu, stream);
@@ -638,11 +640,6 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
         g1.row_prob = fc1_topk ? (const float*)(w + L.sorted_probs) : nullptr;
         g1.a_scale = (const float*)(w + L.xs);
         g1.w_scale = (const float*)(h->kbuf + b1 + b2);
-        e = launch_gemm_int8(true, g1, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
-        if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1 launch");
-        e = launch_quant_rows_int8(QuantRows{(const uint16_t*)(w + L.hbuf), &hdr->n_rows, T_cap * h->k, F, Kp2,
-                                             (uint8_t*)(w + L.hq), (float*)(w + L.hscale)}, h->num_cu, stream);
-        if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-h launch");
         GemmArgs g2 = g1;
         g2.A = (const uint16_t*)(w + L.hq);
         g2.W = (const uint16_t*)(h->kbuf + b1);
@@ -656,8 +653,38 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
                              (int64_t)H * Kp2 >= ((int64_t)1 << 31);
         g2.a_scale = (const float*)(w + L.hscale);
         g2.w_scale = (const float*)(h->kbuf + b1 + b2 + b3);
-        e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr);
-        if (e != hipSuccess) return hip_fail(e, "moe_forward: FC2 launch");
+        const QuantRows rows{(const uint16_t*)(w + L.hbuf), &hdr->n_rows, T_cap * h->k, F, Kp2,
+                             (uint8_t*)(w + L.hq), (float*)(w + L.hscale)};
+        const SideStream* ss = (h->device >= 0 && h->device < kMaxScratchDevices) ? &g_side[h->device] : nullptr;
+        // as for bf16: with both stages split in two launches and 64-row experts
+        // likely, the 64-row chain (FC1, its rows' quantization, FC2) runs on the
+        // side stream; each chain covers the experts of one tile table
+        const bool few_small = (int64_t)T_cap * h->k >= (int64_t)4 * kBigMin * E;
+        if (!g1.small_takes_big && !g2.small_takes_big && ss && ss->s && !h->record_stages && !few_small) {
+            const QuantTiles big{(const int2*)(w + L.tiles_big), &hdr->n_tiles_big, g1.offsets, kBigBMRows};
+            const QuantTiles small{(const int2*)(w + L.tiles), &hdr->n_tiles, g1.offsets, kBM};
+            std::lock_guard<std::mutex> lock(g_side_mu);
+            e = hipEventRecord(ss->fork, stream);
+            if (e == hipSuccess) e = hipStreamWaitEvent(ss->s, ss->fork, 0);
+            if (e != hipSuccess) return hip_fail(e, "moe_forward: fork");
+            e = launch_gemm_int8(true, g1, h->num_cu, stream, nullptr, nullptr, ss->s);
+            if (e == hipSuccess) e = launch_quant_rows_int8(rows, &big, h->num_cu, stream);
+            if (e == hipSuccess) e = launch_quant_rows_int8(rows, &small, h->num_cu, ss->s);
+            if (e == hipSuccess) e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr, ss->s);
+            // the join is enqueued whatever was launched, so that a failed call leaves
+            // nothing running beside the caller's stream
+            hipError_t j = hipEventRecord(ss->join, ss->s);
+            if (j == hipSuccess) j = hipStreamWaitEvent(stream, ss->join, 0);
+            if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1, quant-h or FC2 launch");
+            if (j != hipSuccess) return hip_fail(j, "moe_forward: join");
+        } else {
+            e = launch_gemm_int8(true, g1, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
+            if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1 launch");
+            e = launch_quant_rows_int8(rows, nullptr, h->num_cu, stream);
+            if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-h launch");
+            e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr);
+            if (e != hipSuccess) return hip_fail(e, "moe_forward: FC2 launch");
+        }
         if ((e = mark(h, 4, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     } else {
         // MXFP8, or MXFP4 weights with MXFP8 activations

@@ -84,23 +84,18 @@ struct QuantRows {
     float* scales;
 };
 
-// The rows of one workgroup of 256 threads, number `block` of `blocks`.  LPR lanes
-// take a row, each lane 8 elements (16 bytes) at a time; NI chunks a lane hold the
-// row in registers, so it is read once (NI = 0: read twice).  Memory bound: 2 K
-// bytes in, Kp out per row.
+// Rows first, first + step, ... below end, RPW = 64 / LPR at a time (a wave's share).
+// LPR lanes take a row, each lane 8 elements (16 bytes) at a time; NI chunks a lane
+// hold the row in registers, so it is read once (NI = 0: read twice).  Memory bound:
+// 2 K bytes in, Kp out per row.
 template <int LPR, int NI>
-__device__ __forceinline__ void quant_rows(const QuantRows& a, int block, int blocks)
+__device__ __forceinline__ void quant_row_range(const QuantRows& a, int64_t first, int64_t end, int64_t step)
 {
-    const int32_t n = *a.n_rows;
-    const int64_t rows = n < 0 ? 0 : (n > a.cap ? a.cap : n);
-    constexpr int RPW = kWave / LPR;             // rows per wave
     const int lane = threadIdx.x & 63, l = lane % LPR;
     const int kc = a.K / 8, kpc = a.Kp / 8;
-    const int64_t wave = (int64_t)block * 4 + (threadIdx.x >> 6);
-    const int64_t step = (int64_t)blocks * 4 * RPW;
-    for (int64_t r0 = wave * RPW; r0 < rows; r0 += step) {
+    for (int64_t r0 = first; r0 < end; r0 += step) {
         const int64_t r = r0 + lane / LPR;
-        const bool in = r < rows;                // (the other lanes stay for the row maximum)
+        const bool in = r < end;                 // (the other lanes stay for the row maximum)
         const uint4* row = (const uint4*)(a.src + (in ? r : r0) * a.K);
         uint2* out = (uint2*)(a.codes + (in ? r : r0) * a.Kp);
         constexpr int NV = NI > 0 ? NI : 1;
@@ -136,6 +131,37 @@ __device__ __forceinline__ void quant_rows(const QuantRows& a, int block, int bl
             for (int c = l; c < kpc; c += LPR) put(c, c < kc ? row[c] : make_uint4(0, 0, 0, 0));
         }
         if (in && l == 0) a.scales[r] = q.scale;
+    }
+}
+
+// The rows of one workgroup of 256 threads, number `block` of `blocks`.
+template <int LPR, int NI>
+__device__ __forceinline__ void quant_rows(const QuantRows& a, int block, int blocks)
+{
+    constexpr int RPW = kWave / LPR;             // rows per wave
+    const int32_t n = *a.n_rows;
+    const int64_t rows = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+    quant_row_range<LPR, NI>(a, ((int64_t)block * 4 + (threadIdx.x >> 6)) * RPW, rows, (int64_t)blocks * 4 * RPW);
+}
+
+// The rows of M tiles (of bm rows at most, a multiple of 16), 16 at a time.
+struct QuantTiles {
+    const int2* tiles;         // (expert, first row)
+    const int32_t* n_tiles;
+    const int32_t* offsets;    // [E + 1]
+    int bm;
+};
+
+template <int LPR, int NI>
+__device__ __forceinline__ void quant_tile_rows(const QuantRows& a, const QuantTiles& t, int block, int blocks)
+{
+    constexpr int RPW = kWave / LPR;
+    const int per = t.bm / 16, n = *t.n_tiles * per;
+    for (int u = block; u < n; u += blocks) {
+        const int2 te = t.tiles[u / per];
+        const int r0 = te.y + 16 * (u % per);
+        const int end = min(min(r0 + 16, te.y + t.bm), t.offsets[te.x + 1]);
+        quant_row_range<LPR, NI>(a, r0 + (threadIdx.x >> 6) * RPW, end, 4 * RPW);
     }
 }
 

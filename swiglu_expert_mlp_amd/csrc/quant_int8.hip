@@ -4,33 +4,42 @@
 
 namespace moe {
 
-template <int LPR, int NI>
-__global__ void __launch_bounds__(256) quant_rows_int8_kernel(QuantRows a)
+// TILES: the rows of the M tiles of one table (of an expert size); else all of them
+template <int LPR, int NI, bool TILES>
+__global__ void __launch_bounds__(256) quant_rows_int8_kernel(QuantRows a, QuantTiles t)
 {
-    quant_rows<LPR, NI>(a, blockIdx.x, gridDim.x);
+    if constexpr (TILES) quant_tile_rows<LPR, NI>(a, t, blockIdx.x, gridDim.x);
+    else quant_rows<LPR, NI>(a, blockIdx.x, gridDim.x);
 }
 
-hipError_t launch_quant_rows_int8(const QuantRows& a, int num_cu, hipStream_t s)
+template <bool TILES>
+static void launch_quant(const QuantRows& a, const QuantTiles& t, int num_cu, hipStream_t s)
 {
     const int64_t cap = a.cap;
     const int Kp = a.Kp;
-    const dim3 block(256);
     auto go = [&](auto kernel, int rows_per_wg) {
         // as many workgroups as the capacity has rows for, at most 8 per CU
         int64_t blocks = (cap + rows_per_wg - 1) / rows_per_wg;
         if (blocks > (int64_t)num_cu * 8) blocks = (int64_t)num_cu * 8;
         if (blocks < 1) blocks = 1;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), block, 0, s, a);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, t);
     };
     // 16 lanes a row up to 512 codes (a whole wave would leave lanes idle), else 64
-    if (Kp <= 128) go(quant_rows_int8_kernel<16, 1>, 16);
-    else if (Kp <= 256) go(quant_rows_int8_kernel<16, 2>, 16);
-    else if (Kp <= 512) go(quant_rows_int8_kernel<16, 4>, 16);
-    else if (Kp <= 1024) go(quant_rows_int8_kernel<64, 2>, 4);
-    else if (Kp <= 2048) go(quant_rows_int8_kernel<64, 4>, 4);
-    else if (Kp <= 4096) go(quant_rows_int8_kernel<64, 8>, 4);
-    else if (Kp <= 8192) go(quant_rows_int8_kernel<64, 16>, 4);
-    else go(quant_rows_int8_kernel<64, 0>, 4);   // read twice
+    if (Kp <= 128) go(quant_rows_int8_kernel<16, 1, TILES>, 16);
+    else if (Kp <= 256) go(quant_rows_int8_kernel<16, 2, TILES>, 16);
+    else if (Kp <= 512) go(quant_rows_int8_kernel<16, 4, TILES>, 16);
+    else if (Kp <= 1024) go(quant_rows_int8_kernel<64, 2, TILES>, 4);
+    else if (Kp <= 2048) go(quant_rows_int8_kernel<64, 4, TILES>, 4);
+    else if (Kp <= 4096) go(quant_rows_int8_kernel<64, 8, TILES>, 4);
+    else if (Kp <= 8192) go(quant_rows_int8_kernel<64, 16, TILES>, 4);
+    else go(quant_rows_int8_kernel<64, 0, TILES>, 4);   // read twice
+}
+
+// tiles (optional): only the rows of this table's M tiles
+hipError_t launch_quant_rows_int8(const QuantRows& a, const QuantTiles* tiles, int num_cu, hipStream_t s)
+{
+    if (tiles) launch_quant<true>(a, *tiles, num_cu, s);
+    else launch_quant<false>(a, QuantTiles{}, num_cu, s);
     return hipGetLastError();
 }
 

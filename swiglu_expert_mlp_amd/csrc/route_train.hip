@@ -223,11 +223,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(BalanceArgs a)
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) slot[wv * (LPT * 4 * N) + Row<LPT, N, VEC>::at(l, i, q)] = acc[4 * i + q];
-    const float z_all = block_sum<kBalWaves>(zs, lds_f);
-    const int n_all = block_sum<kBalWaves>(n, lds_i);
+    if (lane == 0) {
+        lds_f[wv] = zs;
+        lds_i[wv] = n;
+    }
+    __syncthreads();
     const bool whole = gridDim.x == 1;
     float dot = 0.0f;
-    for (int e = threadIdx.x; e < E; e += kBalThreads) {     // (block_sum's barriers cover slot and cnt)
+    for (int e = threadIdx.x; e < E; e += kBalThreads) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < kBalWaves; ++w) s += slot[w * (LPT * 4 * N) + e];
@@ -240,6 +243,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(BalanceArgs a)
             a.part_c[(int64_t)blockIdx.x * E + e] = cnt[e];
         }
     }
+    float z_all = 0.0f;
+    int n_all = 0;
+    if (threadIdx.x == 0)
+#pragma unroll
+        for (int w = 0; w < kBalWaves; ++w) {
+            z_all += lds_f[w];
+            n_all += lds_i[w];
+        }
     if (whole) {
         dot = block_sum<kBalWaves>(wave_sum(dot), lds_f);
         if (threadIdx.x == 0) write_losses(a, dot, z_all, n_all);
@@ -263,6 +274,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalanceArgs
     __shared__ int cs[PER][EP];
     __shared__ float lds_f[kBalWaves];
     __shared__ int lds_i[kBalWaves];
+    __shared__ float lds_d[EP / kWave];
     const int E = a.E, x = threadIdx.x % EP, y = threadIdx.x / EP;
     const int e = blockIdx.x * EP + x, ec = e < E ? e : E - 1;
     float zb = 0.0f;
@@ -280,8 +292,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalanceArgs
     }
     ps[y][x] = s;
     cs[y][x] = c;
-    const float z = block_sum<kBalWaves>(wave_sum(zb), lds_f);
-    const int n = block_sum<kBalWaves>(wave_sum(nb), lds_i);
+    zb = wave_sum(zb);
+    nb = wave_sum(nb);
+    if ((threadIdx.x & 63) == 0) {
+        lds_f[threadIdx.x >> 6] = zb;
+        lds_i[threadIdx.x >> 6] = nb;
+    }
+    __syncthreads();
     float dot = 0.0f;
     if (threadIdx.x < EP) {
         s = 0.0f;
@@ -297,8 +314,21 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalanceArgs
             dot = (float)c * s;
         }
     }
-    dot = block_sum<kBalWaves>(wave_sum(dot), lds_f);
+    // (only the first EP / 64 waves have a part of it)
+    dot = wave_sum(dot);
+    if (threadIdx.x < EP && (threadIdx.x & 63) == 0) lds_d[threadIdx.x >> 6] = dot;
+    if constexpr (EP > kWave) __syncthreads();
     if (threadIdx.x != 0) return;
+    dot = 0.0f;
+    float z = 0.0f;
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < EP / kWave; ++w) dot += lds_d[w];
+#pragma unroll
+    for (int w = 0; w < kBalWaves; ++w) {
+        z += lds_f[w];
+        n += lds_i[w];
+    }
     if (gridDim.x == 1) {
         write_losses(a, dot, z, n);
         return;

@@ -307,6 +307,96 @@ def test_graph_replays_and_streams_bitwise(name):
         assert torch.equal(out[: w.T - n], eager[: w.T - n]), n
 
 
+def _skewed(w, n_small=100, seed=7):
+    """Routes: the first tokens to the upper half of the experts (about 50 rows each:
+    64-row tiles), the rest to the lower half (256-row tiles)."""
+    rng = np.random.default_rng(seed)
+    half = w.E // 2
+    ids = np.full((w.T_cap, w.k), -1, np.int32)
+    for t in range(w.T):
+        pool = np.arange(half, w.E) if t < n_small else np.arange(half)
+        ids[t] = np.sort(rng.choice(pool, size=w.k, replace=False))
+    probs = rng.uniform(0.1, 0.9, (w.T_cap, w.k)).astype(np.float32)
+    return torch.from_numpy(ids).cuda(), torch.from_numpy(probs).cuda()
+
+
+SPLIT = {
+    # both stages have a 256-row and a 64-row launch: the 64-row chain is forked
+    "both_split": Workload("both_split", 1400, 1500, 256, 288, 8, 2, "int8"),
+    # one stage alone has two launches (the other's K is under 256): serial
+    "fc1_split": Workload("fc1_split", 1400, 1500, 256, 96, 8, 2, "int8"),
+    "fc2_split": Workload("fc2_split", 1400, 1500, 64, 256, 8, 2, "int8"),
+}
+
+
+@pytest.mark.parametrize("name", list(SPLIT))
+def test_forked_chain_equals_the_serial_order(name):
+    """Stage events keep the stages serial; the two orders give the same bits."""
+    w = SPLIT[name]
+    c = Case(w, seed=18)
+    moe = new_moe(c)
+    ids, probs = _skewed(w)
+    x, live = c.dev()[0], live_tensor(w.T)
+    ws = moe.new_workspace(w.T_cap)
+    ws.fill_(0x5A)
+    forked = moe.forward(x, ids, probs, live, out=sentinel_out(w.T_cap, w.H), ws=ws)
+    counts = moe.get_indices(ws, w.T_cap)["counts"]
+    assert counts[: w.E // 2].min() > 128 and 0 < counts[w.E // 2:].max() <= 128
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(6)]     # (the caller's: kept until the end)
+    moe.set_stage_events(events)
+    serial = moe.forward(x, ids, probs, live, out=sentinel_out(w.T_cap, w.H), ws=moe.new_workspace(w.T_cap))
+    moe.set_stage_events(None)
+    assert np.array_equal(forked.cpu().numpy().view(np.uint32), serial.cpu().numpy().view(np.uint32))
+    ref, _, _ = c.oracle_model().forward(c.inp["x_bits"], ids.cpu().numpy(), probs.cpu().numpy(), w.T)
+    assert_close(forked.cpu().numpy()[: w.T], ref[: w.T], name)
+
+
+def test_two_caller_streams_share_one_handle():
+    """Forwards on two streams at once (one handle and so one side stream, two workspaces)."""
+    w = SPLIT["both_split"]
+    c = Case(w, seed=19)
+    moe = new_moe(c)
+    ids, probs = _skewed(w)
+    live = live_tensor(w.T)
+    xs = [c.dev()[0]]
+    xs.append(torch.flip(xs[0][: w.T], dims=[0]).contiguous())
+    xs[1] = torch.cat([xs[1], xs[0][w.T:]])
+    refs = [moe.forward(x, ids, probs, live, out=sentinel_out(w.T_cap, w.H)) for x in xs]
+    outs = [[sentinel_out(w.T_cap, w.H) for _ in range(4)] for _ in xs]
+    wss = [moe.new_workspace(w.T_cap) for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for n in range(4):
+        for i, s in enumerate(streams):
+            moe.forward(xs[i], ids, probs, live, out=outs[i][n], ws=wss[i], stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert np.array_equal(o.cpu().numpy().view(np.uint32), refs[i].cpu().numpy().view(np.uint32))
+
+
+def test_forked_chain_captured_and_replayed():
+    w = SPLIT["both_split"]
+    c = Case(w, seed=20)
+    moe = new_moe(c)
+    ids, probs = _skewed(w)
+    x, live = c.dev()[0], live_tensor(w.T)
+    ws, ws2 = moe.new_workspace(w.T_cap), moe.new_workspace(w.T_cap)
+    out = sentinel_out(w.T_cap, w.H)
+    moe.forward(x, ids, probs, live, out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.forward(x, ids, probs, live, out=out, ws=ws)
+    for n in range(4):
+        x[: w.T] = torch.roll(x[: w.T], 3, 0)
+        live.fill_(w.T - 11 * n)
+        graph.replay()
+        eager = moe.forward(x, ids, probs, live, ws=ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out[: w.T - 11 * n], eager[: w.T - 11 * n]), n
+
+
 def test_refused_options():
     c = get_case("tiny")
     moe = new_moe(c)
