@@ -325,6 +325,15 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
         const bool has_a = wid < ng;                 // this wave loads activation block wid
         const int nl = (has_a ? 1 : 0) + (has_cols ? 4 : 0);
 
+        // int8: lane l's activation row, for its scale in the epilogue; looked up here,
+        // beside the rows' own lookup, so that the epilogue waits for one round trip
+        // less (64 tokens, hidden 128: 24.1 -> 23.6 us a forward; 256 tokens, hidden
+        // 2048: 87.5 -> 86.6)
+        int srow = row0 + min(lane, rows - 1);
+        if constexpr (Op::kScaled && FC1) {
+            srow = g.perm_src[srow] / g.topk;
+            asm volatile("" : "+v"(srow));           // (landed before the loads below)
+        }
         const uint16_t* arow = g.A;
         if (has_a) {
             const int r = min(16 * wid + (lane >> 2), rows - 1);
@@ -413,7 +422,7 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
         // int8: lane l holds the scale of row l, and those of its two columns
         float rs = 1.0f, cs[2] = {1.0f, 1.0f};
         if constexpr (Op::kScaled) {
-            rs = act_scale<FC1>(g, row0 + min(lane, rows - 1));
+            rs = g.a_scale[srow];
             const float* wsc = g.w_scale + (int64_t)e * g.N + c32;
             cs[0] = wsc[cb * 64];
             cs[1] = wsc[min(cb * 64 + 32, g.N - 32)];
