@@ -113,6 +113,45 @@ def test_route_backward(T, cap, E, k, mask, which):
     assert np.all(out[T:] == np.float32(SENTINEL)), "rows past live were written"
 
 
+@pytest.mark.parametrize("E", [64, 128, 256, 512, 1024])
+def test_logits_past_the_infinity_cache(E):
+    """256 MiB of logits and more are read and written non-temporally: the sums against fp64
+    on the GPU, sampled rows of the gradient against the reference."""
+    k, T = 2, (1 << 26) // E + 5
+    g = torch.Generator("cuda").manual_seed(E)
+    z = torch.randn(T, E, generator=g, device="cuda")
+    ids = z.topk(k, dim=1).indices.sort(dim=1).values.to(torch.int32)
+    q = torch.softmax(z.gather(1, ids.long()), 1)
+    d = torch.randn(T, k, generator=g, device="cuda")
+    mask = torch.rand(T, generator=g, device="cuda") < 0.75
+    moe, live = moe_of(E, k), live_tensor(T)
+    losses, counts, sums = moe.balance(z, ids, live, mask=mask)
+    n = int(mask.sum())
+    ref, zl = torch.zeros(E, dtype=torch.float64, device="cuda"), 0.0
+    for c in range(0, T, 1 << 16):
+        zz = z[c: c + (1 << 16)][mask[c: c + (1 << 16)]].double()
+        lse = torch.logsumexp(zz, 1)
+        ref += torch.exp(zz - lse[:, None]).sum(0)
+        zl += float(lse.square().sum())
+    hits = torch.bincount(ids[mask].reshape(-1).long(), minlength=E)
+    assert torch.equal(counts, torch.cat([hits, hits.new_tensor([n])]).to(torch.int32))
+    # (2 |z - m| + 26) roundings a probability, |z - m| < 12, and those of the sum
+    tol = (2 * 12 + 26 + in_order(T, E)) * EPS
+    assert torch.all((sums.double() - ref).abs() <= tol * ref)
+    bal = float((hits * ref).sum()) * E / (k * n * n)
+    assert abs(float(losses[0]) - bal) <= (tol + (E / 64 + 40) * EPS) * bal
+    # lse lies in [0, 13]: 2 (3 * 7 + 22 + |lse|) roundings of it, relative to its mean square
+    assert abs(float(losses[1]) - zl / n) <= (2 * 60 * EPS * 13 / (zl / n) ** 0.5 + in_order(T, E) * EPS) * zl / n
+    dz = moe.route_backward(z, ids, live, probs=q, d_probs=d, counts=counts,
+                            d_losses=torch.tensor([0.5, 0.25], device="cuda"), mask=mask)
+    rows = np.unique(np.r_[0:40, np.random.default_rng(E).integers(0, T, 100), T - 40: T])
+    at = torch.from_numpy(rows).cuda()
+    host = lambda t: t[at].cpu().numpy()
+    ref, off = route_backward_ref(host(z), host(ids), host(mask), host(q), host(d),
+                                  counts.cpu().numpy().astype(np.float64), (0.5, 0.25))
+    assert np.all(np.abs(host(dz) - ref) <= off)
+
+
 def test_kernel_gradient_against_differences():
     """The kernel's gradient against central differences of the losses in fp64."""
     T, E, k = 4, 6, 2
