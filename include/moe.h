@@ -34,11 +34,11 @@
  *     row-major, dense.  bf16 data is passed as its 16-bit patterns.
  *   - The library never allocates device memory and never synchronizes the
  *     stream, except moe_check (which reads the error word) and
- *     moe_get_indices (which copies to host).  moe_route and moe_forward only
- *     enqueue work on `stream`, so they can be captured in a HIP graph; a bf16
- *     forward above 1024 tokens may run its 64-row GEMM launches on a side
- *     stream of the library (one per GPU, default priority, created by the
- *     first bf16 moe_load_weights there and kept until the process ends),
+ *     moe_get_indices (which copies to host).  moe_route, moe_forward and
+ *     the training calls only enqueue work on `stream`, so they can be captured
+ *     in a HIP graph; a bf16 or int8 forward above 1024 tokens may run its 64-row GEMM launches on a
+ *     side stream of the library (one per GPU, default priority, created by the
+ *     first bf16 or int8 weight load there and kept until the process ends),
  *     forked from `stream` and joined back to it with events, so the work
  *     still completes in `stream` order and is captured with it.
  *   - The live token count is read from device memory (live_rows_dev, int32,
@@ -432,8 +432,8 @@ moe_status moe_check(moe_handle h, void* ws, hipStream_t stream, uint32_t* err_b
 /* Stage timing hook (for profiling).  With events != NULL, every later
  * moe_forward on this handle records, on its stream, events[0] before its
  * first kernel and events[i] after stage i: 1 permutation (sort, histogram,
- * scan, scatter), 2 MXFP8 / int8 activation quantization (nothing in bf16), 3
- * FC1 + SwiGLU, 4 FC2 (int8: with the quantization of the SwiGLU rows before
+ * scan, scatter; int8: with the activation quantization), 2 MXFP8 activation
+ * quantization (nothing in bf16 and int8), 3 FC1 + SwiGLU, 4 FC2 (int8: with the quantization of the SwiGLU rows before
  * it), 5 finalize.  events[2] and events[3] are the start and end
  * of the FC1 + SwiGLU launch itself, recorded by its dispatch (no marker
  * packets around it), so events[3] - events[2] is that launch's duration

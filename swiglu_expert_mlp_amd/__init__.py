@@ -133,6 +133,19 @@ def _dev(t, name, dtypes, shape=None):
     return t.data_ptr()
 
 
+def _on_current(stream, inputs, made=()):
+    """The router's training calls run on the current device: every tensor has to be there.
+    Tensors the call itself made are kept until `stream` is done with them."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    for t in inputs:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+
+
 class MoE:
     """Handle of one routed SwiGLU MoE layer (E experts, hidden H, FFN F, top-k)."""
 
@@ -302,6 +315,7 @@ class MoE:
     def _balance_args(self, logits, ids, live, losses, counts, prob_sums, ws, mask, stream):
         torch = _torch()
         T_cap = logits.shape[0]
+        _on_current(None, (logits, ids, live, losses, counts, prob_sums, ws, mask))
         return (self._h, _dev(logits, "logits", (torch.float32,), (T_cap, self.E)),
                 _dev(ids, "ids", (torch.int32,), (T_cap, self.topk)), T_cap,
                 _dev(live, "live", (torch.int32,)), self._mask(mask, T_cap),
@@ -317,6 +331,7 @@ class MoE:
         mask: bool or uint8 [T_cap], tokens with 0 are left out."""
         torch = _torch()
         dev = logits.device
+        given = (losses, counts, prob_sums, ws)
         if losses is None:
             losses = torch.empty(2, dtype=torch.float32, device=dev)
         if counts is None:
@@ -325,6 +340,7 @@ class MoE:
             prob_sums = torch.empty(self.E, dtype=torch.float32, device=dev)
         if ws is None:
             ws = self.new_balance_workspace(logits.shape[0], dev)
+        _on_current(stream, (), [t for t, g in zip((losses, counts, prob_sums, ws), given) if g is None])
         _check(lib().moe_balance(*self._balance_args(logits, ids, live, losses, counts, prob_sums, ws, mask,
                                                      stream)), "moe_balance")
         return losses, counts, prob_sums
@@ -333,6 +349,7 @@ class MoE:
         torch = _torch()
         T_cap = logits.shape[0]
         f32, i32 = (torch.float32,), (torch.int32,)
+        _on_current(None, (logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask))
         opt = lambda t, name, dt, shape: None if t is None else _dev(t, name, dt, shape)
         return (self._h, _dev(logits, "logits", f32, (T_cap, self.E)),
                 opt(ids, "ids", i32, (T_cap, self.topk)), opt(probs, "probs", f32, (T_cap, self.topk)),
@@ -347,7 +364,8 @@ class MoE:
         (probs with d_probs), of balance's losses (counts with d_losses, fp32 [2]), or of both."""
         torch = _torch()
         if d_logits is None:
-            d_logits = torch.empty_like(logits)
+            d_logits = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
+            _on_current(stream, (), (d_logits,))
         _check(lib().moe_route_backward(*self._route_backward_args(logits, ids, live, d_logits, probs, d_probs,
                                                                    counts, d_losses, mask, stream)),
                "moe_route_backward")
@@ -356,6 +374,7 @@ class MoE:
     def _probs_backward_args(self, d_out, ids, d_probs, ws, stream):
         torch = _torch()
         T_cap = d_out.shape[0]
+        _on_current(None, (d_out, ids, d_probs, ws))
         p = _dev(d_out, "d_out", (torch.float32, torch.bfloat16), (T_cap, self.H))
         return (self._h, p, COMBINES["fp32" if d_out.dtype == torch.float32 else "bf16"],
                 _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk)), T_cap,
@@ -368,6 +387,7 @@ class MoE:
         torch = _torch()
         if d_probs is None:
             d_probs = torch.empty((d_out.shape[0], self.topk), dtype=torch.float32, device=d_out.device)
+            _on_current(stream, (), (d_probs,))
         _check(lib().moe_probs_backward(*self._probs_backward_args(d_out, ids, d_probs, ws, stream)),
                "moe_probs_backward")
         return d_probs

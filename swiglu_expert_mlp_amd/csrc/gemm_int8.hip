@@ -13,6 +13,17 @@
 // MFMA, half the bytes and MFMAs per row.  Rows are padded with zero codes to a
 // multiple of 128 (64 below 256; common.h), so that every K from 256 on takes
 // the 256-row design's 128-byte stages.
+//
+// What bounds it (one MI355X).  16,384 tokens, 128 experts, top-8, hidden 2048, FFN
+// 1024: FC1 600 us, FC2 430 us.  The MFMAs and epilogues alone take 430 / 260 us and
+// the loads alone 450 / 270 (FC2's 1.07 GB of fp32 rows another 130), but the shader
+// clock falls to 1.6-1.9 GHz in FC1 and 1.7-2.1 GHz in FC2 (2.4 nominal): the
+// launches run at the power limit, where neither a deeper weight ring (1.3 % of the
+// forward), nor operands resident in the L2 (6 %), nor fewer tiles of mostly empty
+// rows (none) gains much.  With the rows that pad each expert to whole tiles the rate
+// is 2.1 PetaOPS, a library's dense int8 product of 16384 x 8192 x 8192 2.2.  256
+// tokens, 64 experts: FC1 45 us, 5.9 TB/s of weights, FC2 27 us (4.9, a third of it the
+// first loads' and last stores' latency): the HBM rate of contiguous 32 KB reads (6.1).
 #include <hip/hip_ext.h>
 
 #include "gemm_bf16_big.h"

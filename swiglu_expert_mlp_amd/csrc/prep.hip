@@ -31,7 +31,7 @@
 // int8 experts: the quantization of x needs nothing of the permutation, and the
 // permutation's launches leave most of the GPU idle, so its rows are extra
 // workgroups of the single-chunk launch, or of prep_finish's (64 tokens, hidden
-// 128: 26.6 -> @T us per forward; 256 tokens, hidden 2048: 90.0 -> @D us).
+// 128: 26.6 -> 24.2 us per forward; 256 tokens, hidden 2048: 90.0 -> 86.8 us).
 #include "quant_int8.h"
 
 namespace moe {

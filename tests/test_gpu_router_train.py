@@ -558,6 +558,74 @@ def test_training_step_captured_and_replayed():
             assert torch.equal(a[:m], b[:m]), n
 
 
+# ------------------------------------------------------------- far offsets
+
+def test_logit_offsets_past_32_bits():
+    """2.15e9 logits: the last rows' gradients, and sums that hold every row."""
+    E, k, T = 1024, 2, 2_100_007
+    z = torch.empty(T, E, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    at = torch.arange(T, device="cuda", dtype=torch.int32)
+    ids = torch.stack([at % (E - 1), torch.full_like(at, E - 1)], 1).contiguous()
+    q = torch.full((T, k), 0.5, device="cuda")
+    d = torch.stack([at % 7, at % 5], 1).float()
+    moe, live = moe_of(E, k), live_tensor(T)
+    losses, counts, sums = moe.balance(z, ids, live)
+    hits = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    assert torch.equal(counts, torch.cat([hits, hits.new_tensor([T])]).to(torch.int32))
+    total = float(sums.double().sum())               # every row's probabilities sum to 1
+    assert abs(total - T) <= T * (2 * 12 + 26 + in_order(T, E)) * EPS
+    dz = moe.route_backward(z, ids, live, probs=q, d_probs=d, counts=counts,
+                            d_losses=torch.tensor([0.5, 0.25], device="cuda"))
+    sel = torch.cat([torch.arange(0, 20), torch.arange(T // 2, T // 2 + 20), torch.arange(T - 40, T)]).cuda()
+    host = lambda t: t[sel].cpu().numpy()
+    ref, off = route_backward_ref(host(z), host(ids), np.ones(len(sel), bool), host(q), host(d),
+                                  counts.cpu().numpy().astype(np.float64), (0.5, 0.25))
+    assert np.all(np.abs(host(dz) - ref) <= off)
+
+
+def test_row_offsets_past_32_bits():
+    """1.06 million tokens of 2048 int8 codes (past 2^31) and as many fp32 rows: sampled far
+    tokens against a small launch, and the probabilities' gradient <d_out, out> (one route a
+    token, probability 1)."""
+    E, H, F, T = 4, 2048, 64, 1_060_003
+    g = torch.Generator("cuda").manual_seed(3)
+    moe = moe_of(E, 1, H, F, "int8")
+    moe.load_weights((torch.randn(E, 2 * F, H, generator=g, device="cuda") * 0.02).bfloat16(),
+                     (torch.randn(E, H, F, generator=g, device="cuda") * 0.1).bfloat16())
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    ids = (torch.arange(T, device="cuda", dtype=torch.int32) % E)[:, None].contiguous()
+    probs = torch.ones(T, 1, device="cuda")
+    ws = moe.new_workspace(T)
+    out = moe.forward(x, ids, probs, live_tensor(T), ws=ws)
+    sel = torch.cat([torch.arange(0, 50), torch.arange(T - 150, T)]).cuda()
+    small = moe.forward(x[sel].contiguous(), ids[sel].contiguous(), probs[sel].contiguous(), live_tensor(len(sel)))
+    assert torch.equal(out[sel], small)
+    d_out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    got = moe.probs_backward(d_out, ids, ws)
+    assert moe.check(ws) == 0
+    prod = d_out[sel].double() * out[sel].double()
+    assert torch.all((got[sel, 0].double() - prod.sum(1)).abs() <= prod.abs().sum(1) * (H / 64 + 16) * EPS)
+
+
+def test_side_stream_calls_keep_what_they_allocate():
+    """Calls on another stream that allocate their outputs and workspaces."""
+    moe = moe_of(256, 4)
+    z, ids, q, d, _ = (dev(a) for a in make(6000, 6000, 256, 4))
+    live = live_tensor(6000)
+    ref = moe.balance(z, ids, live)
+    grad = moe.route_backward(z, ids, live, probs=q, d_probs=d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(6):
+        got.append((moe.balance(z, ids, live, stream=side), moe.route_backward(z, ids, live, probs=q, d_probs=d,
+                                                                               stream=side)))
+        torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")   # takes what was freed
+    torch.cuda.synchronize()
+    for b, g in got:
+        assert all(torch.equal(u, v) for u, v in zip(b, ref)) and torch.equal(g, grad)
+
+
 def test_python_refusals():
     moe = moe_of(8, 2)
     z, ids = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")

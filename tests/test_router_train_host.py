@@ -109,3 +109,17 @@ def test_reference_gradient_against_differences(T, E, k, masked):
             up[t, e] += 1e-5
             dn[t, e] -= 1e-5
             assert abs((value(up) - value(dn)) / 2e-5 - grad[t, e]) < 1e-8
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    import torch
+    import swiglu_expert_mlp_amd as m
+
+    class Fake:
+        device = torch.device("cuda:1")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        m._on_current(None, (None, Fake()))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    m._on_current(None, (None, Fake()))
