@@ -577,7 +577,7 @@ hipError_t launch_route_backward(const float* logits, const int32_t* ids, const 
 // parameter so that a token's row loads are all in flight.  TPT threads take a
 // token: a wave when there are many, a workgroup of 512 when there are few (16,384
 // tokens, top-8, hidden 2048: 183 us, 6.6 TB/s, against 187 with a workgroup each; 256
-// tokens, top-6: 4.8 us against 14.3 with a wave each).
+// tokens, top-6: 4.7 us against 14.3 with a wave each).
 struct ProbsGradArgs {
     const WsHeader* hdr;
     uint32_t* err;
@@ -597,6 +597,16 @@ __global__ void __launch_bounds__(512) probs_backward_kernel(ProbsGradArgs a)
     static_assert(TPT == 64 || TPT == 512, "a wave or a workgroup per token");
     __shared__ float part[8][K];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    constexpr int TOK = 512 / TPT;              // tokens per workgroup
+    // the first token's row indices go out beside the header (workspace bytes that
+    // exist up to T_cap, unused unless the header says that they are a forward's)
+    int64_t t = (int64_t)blockIdx.x * TOK + (TPT == 64 ? wv : 0);
+    int32_t d[K];
+    auto indices = [&]() {
+#pragma unroll
+        for (int j = 0; j < K; ++j) d[j] = t < a.T_cap ? a.dst[t * K + j] : -1;
+    };
+    indices();
     const bool stale = a.hdr->tag != a.tag;
     if (stale || a.hdr->weighted) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, stale ? kErrNoRows : kErrWeightedRows);
@@ -604,14 +614,11 @@ __global__ void __launch_bounds__(512) probs_backward_kernel(ProbsGradArgs a)
     }
     const uint32_t n_rows = (uint32_t)a.hdr->n_rows;
     const int64_t T = a.hdr->T < a.T_cap ? a.hdr->T : a.T_cap;
-    constexpr int TOK = 512 / TPT;              // tokens per workgroup
     const int H4 = a.H >> 2;                    // H is a multiple of 32
-    for (int64_t t = (int64_t)blockIdx.x * TOK + (TPT == 64 ? wv : 0); t < T; t += (int64_t)gridDim.x * TOK) {
-        int32_t d[K];
+    for (; t < T; t += (int64_t)gridDim.x * TOK, indices()) {
         float acc[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            d[j] = a.dst[t * K + j];
             if ((uint32_t)d[j] >= n_rows) d[j] = -1;
             acc[j] = 0.0f;
         }
