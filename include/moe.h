@@ -39,8 +39,9 @@
  *     in a HIP graph; a bf16 or int8 forward above 1024 tokens may run its
  *     64-row GEMM launches on a side stream of the library (one per GPU,
  *     default priority, created by the first bf16 or int8 weight load there
- *     and kept until the process ends), forked from `stream` and joined back to it with events, so the work
- *     still completes in `stream` order and is captured with it.
+ *     and kept until the process ends), forked from `stream` and joined back
+ *     to it with events, so the work still completes in `stream` order and is
+ *     captured with it.
  *   - The live token count is read from device memory (live_rows_dev, int32,
  *     in TOKENS).  It is clamped to [0, T_cap]; a value outside sets an error
  *     bit (see moe_check).  Token rows >= live are never read and rows >= live
@@ -311,14 +312,16 @@ moe_status moe_forward_noalloc(moe_handle h, const void* x, const int32_t* exper
 
 /* Workspace bytes of moe_balance for a token capacity T_cap (0 for a NULL
  * handle or a negative T_cap): caller-owned, no required initial contents, not
- * shared with a call that may overlap in time. */
+ * shared with a call that may overlap in time.  A moe_workspace_bytes workspace
+ * of that size may serve, but a forward's rows, indices and error bits there
+ * are lost by it (moe_probs_backward then flags MOE_DEVERR_NO_ROWS). */
 size_t moe_balance_workspace_bytes(moe_handle h, int64_t T_cap);
 
 /* Balance loss, z loss and per-expert counts of the router (training).  Over
  * the counted tokens (live, and with a nonzero token_mask entry if there is a
  * mask), N of them, with p_t the softmax of token t's E logits:
  *   counts[e]    = number of their routes to expert e (ids outside [0, E) are
- *                  left out); counts[E] = N
+ *                  left out, a repeated id counts each time); counts[E] = N
  *   prob_sums[e] = sum_t p_t[e]
  *   losses[0]    = E / (topk N^2) sum_e counts[e] prob_sums[e]   (balance; 1 when
  *                  every expert has the same share of both)
@@ -433,8 +436,8 @@ moe_status moe_check(moe_handle h, void* ws, hipStream_t stream, uint32_t* err_b
  * moe_forward on this handle records, on its stream, events[0] before its
  * first kernel and events[i] after stage i: 1 permutation (sort, histogram,
  * scan, scatter; int8: with the activation quantization), 2 MXFP8 activation
- * quantization (nothing in bf16 and int8), 3 FC1 + SwiGLU, 4 FC2 (int8: with the quantization of the SwiGLU rows before
- * it), 5 finalize.  events[2] and events[3] are the start and end
+ * quantization (nothing in bf16 and int8), 3 FC1 + SwiGLU, 4 FC2 (int8: with
+ * the quantization of the SwiGLU rows before it), 5 finalize.  events[2] and events[3] are the start and end
  * of the FC1 + SwiGLU launch itself, recorded by its dispatch (no marker
  * packets around it), so events[3] - events[2] is that launch's duration
  * (MXFP4 above a 1024-token capacity, where the stage is two launches: the

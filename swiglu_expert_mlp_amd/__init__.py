@@ -139,8 +139,9 @@ def _on_current(stream, inputs, made=()):
     torch = _torch()
     dev = torch.cuda.current_device()
     for t in inputs:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+        d = getattr(t, "device", None)      # (_dev refuses what is no GPU tensor)
+        if isinstance(d, torch.device) and d.type == "cuda" and d.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {d}")
     if stream is not None:
         for t in made:
             t.record_stream(stream)

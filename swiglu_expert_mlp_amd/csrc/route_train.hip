@@ -153,6 +153,7 @@ struct BalanceArgs {
     int32_t* counts;           // [E + 1]: per expert, then the counted tokens
     float* prob_sums;          // [E]
     // workspace: partials of each workgroup of the first launch
+    WsHeader* hdr;             // a forward's, if the buffer held one: its tag is cleared
     uint32_t* ticket;          // second launch's workgroups that are done
     float* part_dot;           // their sums of c_e sum_t p_te
     float* part_z;
@@ -262,7 +263,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(BalanceArgs a)
     } else if (threadIdx.x == 0) {
         a.part_z[blockIdx.x] = z_all;
         a.part_n[blockIdx.x] = n_all;
-        if (blockIdx.x == 0) *a.ticket = 0;
+        if (blockIdx.x == 0) {
+            *a.ticket = 0;
+            a.hdr->err = 0;
+            a.hdr->tag = 0;
+        }
     }
 }
 
@@ -372,7 +377,7 @@ static bool stream_logits(int E, int64_t T_cap) { return T_cap * E * 4 >= ((int6
 size_t balance_ws_bytes(int E, int64_t T_cap)
 {
     const size_t b = (size_t)balance_blocks(E, T_cap, kBalMaxBlocks);
-    return 256 + up256(4 * kMaxExperts / kWave) + 2 * up256(4 * b) + 2 * up256(4 * b * E);
+    return sizeof(WsHeader) + up256(4) + up256(4 * kMaxExperts / kWave) + 2 * up256(4 * b) + 2 * up256(4 * b * E);
 }
 
 #define ROW_BY_E(E, CALL, VEC, STREAM)                                                            \
@@ -399,7 +404,8 @@ hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap
     BalanceArgs a{logits, ids, live, mask, T_cap, E, k, losses, counts, prob_sums};
     size_t o = 0;
     auto take = [&](size_t bytes) { char* p = ws + o; o += up256(bytes); return p; };
-    a.ticket = (uint32_t*)take(256);
+    a.hdr = (WsHeader*)take(sizeof(WsHeader));
+    a.ticket = (uint32_t*)take(4);
     a.part_dot = (float*)take(4 * kMaxExperts / kWave);
     a.part_z = (float*)take(4 * blocks);
     a.part_n = (int32_t*)take(4 * blocks);

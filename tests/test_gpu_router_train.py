@@ -445,6 +445,27 @@ def test_workspaces_without_the_rows_are_flagged():
     assert moe.check(ws) == 0 and not torch.any(got[: w.T] == SENTINEL)
 
 
+def test_balance_in_a_forward_workspace_is_flagged():
+    """A buffer that held a forward and then balance's partials holds no rows: the
+    probabilities' gradient says so instead of reading the partials as indices."""
+    from swiglu_expert_mlp_amd import DEVERR_NO_ROWS
+    T, E, k, H = 1200, 64, 6, 64
+    moe = moe_of(E, k, H, 32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    draw = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    moe.load_weights(draw(E, 64, H).bfloat16(), draw(E, H, 32).bfloat16())
+    z, live = draw(T, E), live_tensor(T)
+    ws = moe.new_workspace(T)
+    ids, probs = moe.route(z, live, ws=ws)
+    moe.forward(draw(T, H).bfloat16(), ids, probs, live, ws=ws)
+    assert moe.check(ws) == 0
+    moe.balance(z, ids, live, ws=ws)
+    got = torch.full((T, k), SENTINEL, device="cuda")
+    moe.probs_backward(draw(T, H), ids, ws, d_probs=got)
+    assert moe.check(ws) == DEVERR_NO_ROWS
+    assert torch.all(got == SENTINEL)
+
+
 def test_probs_backward_after_the_single_launch_modes():
     c, moe = probs_case("tiny")
     w = c.w
