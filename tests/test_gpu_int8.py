@@ -351,6 +351,38 @@ def test_forked_chain_equals_the_serial_order(name):
     assert_close(forked.cpu().numpy()[: w.T], ref[: w.T], name)
 
 
+@pytest.mark.parametrize("F", [256, 1024, 2048, 4096, 8192, 8224])
+def test_swiglu_rows_of_every_width(F):
+    """Each width class of the SwiGLU rows' quantization, by all rows (serial) and by the
+    tiles of each chain (forked), against the oracle's rows."""
+    w = Workload(f"width_{F}", 1300, 1310, 256, F, 4, 1, "int8")
+    c = Case(w, seed=19)
+    moe = new_moe(c)
+    ids, probs = _skewed(w)
+    x, live = c.dev()[0], live_tensor(w.T)
+    ref, err, extras = c.oracle_model().forward(c.inp["x_bits"], ids.cpu().numpy(), probs.cpu().numpy(), w.T,
+                                                want_rows=True)
+    assert err == 0
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(6)]
+    seen = []
+    for ev in (None, events):
+        moe.set_stage_events(ev)
+        ws = moe.new_workspace(w.T_cap)
+        ws.fill_(0x5A)
+        out = moe.forward(x, ids, probs, live, out=sentinel_out(w.T_cap, w.H), ws=ws).cpu().numpy()
+        assert moe.check(ws) == 0
+        _, rows = rows_of(moe, ws, w)
+        codes, scales = rows["fc1_codes"], rows["fc1_scales"]
+        n = codes.shape[0]
+        assert n == w.T and np.all(np.abs(codes.astype(np.int32)).max(axis=1) == 127)
+        step = np.abs(extras["H"][:n]).max(axis=1, keepdims=True) / 127
+        assert np.all(np.abs(codes * scales[:, None] - extras["H"][:n]) <= 2.01 * step + 1e-30)
+        assert_close(out[: w.T], ref[: w.T], w.name)
+        seen.append((codes, scales, out.view(np.uint32)))
+    moe.set_stage_events(None)
+    assert all(np.array_equal(a, b) for a, b in zip(*seen))
+
+
 def test_two_caller_streams_share_one_handle():
     """Forwards on two streams at once (one handle and so one side stream, two workspaces)."""
     w = SPLIT["both_split"]
