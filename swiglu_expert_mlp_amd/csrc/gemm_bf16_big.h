@@ -311,7 +311,8 @@ __device__ __forceinline__ void big_kloop(const BigSrc& t, char* s0, char* s1, c
 // The 256-row tile loop of one 8-wave workgroup (one workgroup per CU).
 // n_mt: the number of 256-row M tiles.  Requires K % 64 == 0 and K >= 128
 // (the launch sends other shapes to the 64-row kernel).
-template <typename Op, bool FC1, bool PROB>
+// WPOL, RPOL: the cache policies of the weights' loads and of FC2's row stores.
+template <typename Op, bool FC1, bool PROB, int WPOL = FC1 ? 0 : kNonTemporal, int RPOL = 0>
 __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
 {
     __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
@@ -389,9 +390,8 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
     if (tile >= t_end) return;
     TilePos pos = locate(tile);
     sources(pos);
-    constexpr int kWPol = FC1 ? 0 : kNonTemporal;
-    big_issue<kWPol>(t, lds0, 0);
-    big_issue<kWPol>(t, lds1, 1);
+    big_issue<WPOL>(t, lds0, 0);
+    big_issue<WPOL>(t, lds1, 1);
     // the K loop counts the previous tile's stores among the operations after
     // its first stages; before the first tile the same number of stores go to
     // an empty descriptor (the range check drops them all; distinct offsets, so
@@ -419,7 +419,7 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
         // the tile's rows (its results are dropped by the store descriptor): a
         // second, load-only loop for such waves made the compiler wait for all
         // loads and stores in flight at every tile's first fragment reads
-        big_kloop<Op, kStores, kWPol>(t, lds0, lds1, ln, wm, wn, acc);
+        big_kloop<Op, kStores, WPOL>(t, lds0, lds1, ln, wm, wn, acc);
 
         // every wave finished reading the stages: the next tile's two stages go
         // out before this tile's epilogue (which has LDS of its own), so they
@@ -458,8 +458,8 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
             sources(npos);
         }
         if constexpr (Op::kScaled) asm volatile("" : : "v"(rs0), "v"(rs1), "v"(cs0), "v"(cs1));
-        big_issue<kWPol>(t, lds0, 0);
-        big_issue<kWPol>(t, lds1, 1);
+        big_issue<WPOL>(t, lds0, 0);
+        big_issue<WPOL>(t, lds1, 1);
 
         // epilogue: lane holds column l % 32 of each 32-column block and rows
         // 8 (v / 4) + 4 (l / 32) + v % 4 of each 32-row block.  The lane index
@@ -516,10 +516,6 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
         } else {
             const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)((float*)g.out + (int64_t)row0 * g.N), (short)0, rows * g.N * 4, kBigRsrcWord3);
-            // int8: the rows are stored non-temporal, so that they do not displace the
-            // operands in the Infinity Cache (the finalize at 16K tokens 203 -> 185
-            // us, 4,096 tokens 508 -> 501 us a forward; bf16 rows measured slower)
-            constexpr int kRowPol = Op::kScaled ? kNonTemporal : 0;
             const int c = elane & 15;
             const int col = n0 + 64 * wn + 4 * c;       // this lane's 4 stored columns
 #pragma unroll
@@ -550,7 +546,7 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
                         }
                         const int off = col < g.N ? ((128 * wm + 32 * i + 16 * hv + lr) * g.N + col) * 4
                                                   : 0x7ffffff0;
-                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, kRowPol);
+                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, RPOL);
                     }
                 }
         }

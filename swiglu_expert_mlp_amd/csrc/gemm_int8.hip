@@ -46,15 +46,23 @@ __global__ void __launch_bounds__(512, 1) gemm_int8_small_kernel(GemmArgs g)
     else small_tiles<OpInt8, FC1, PROB, 0, kNonTemporal>(g, smem, n_small, n_big, e0, row00);
 }
 
-template <bool FC1, bool PROB>
+// FC2's policies follow the bytes of its fp32 rows (hidden 2048, FFN 1024, a forward):
+// rows that fit the 256 MB Infinity Cache are stored as usual, for the combine to find
+// there (2,048 tokens x top-6: 188 us, 192 non-temporally; 3,000 x 8: 340 / 347), larger
+// ones non-temporally, so that they do not displace the operands (4,096 x 8: 455, 463 as
+// usual; 16,384 x 8: 1289 / 1308).  Weights are read non-temporally too where the rows are
+// past twice that cache (12,000 x 8: 981, 994 as usual; 16,384 x 8: 1336 / 1360); below,
+// some are found in it (6,000 x 8: 595, 607 non-temporally; 8,192 x 6: 558 / 562).
+template <bool FC1, bool PROB, int WPOL, int RPOL>
 __global__ void __launch_bounds__(512, 1) gemm_int8_big_kernel(GemmArgs g)
 {
-    big_tiles<OpInt8, FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
+    big_tiles<OpInt8, FC1, PROB, WPOL, RPOL>(g, ld_const(&g.hdr->n_tiles_big));
 }
 
 // One GEMM stage: the 256-row launch on s (unless the 64-row kernel takes its
 // tiles), the 64-row launch on s_small (s if null).  t0 / t1 as launch_gemm_bf16.
-hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
+// max_rows: the most grouped rows that the capacity can have.
+hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int64_t max_rows, int num_cu, hipStream_t s, hipEvent_t t0,
                             hipEvent_t t1, hipStream_t s_small)
 {
     if (!g.a_scale || !g.w_scale || g.K < 32 || g.K % 32 != 0 || g.N < 32 || g.N % 32 != 0)
@@ -70,9 +78,12 @@ hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t
     hipEvent_t small_start = t0;
     hipStream_t ss = s;
     if (!g.small_takes_big) {
-        if (prob) go(gemm_int8_big_kernel<true, true>, t0, nullptr, s);
-        else if (fc1) go(gemm_int8_big_kernel<true, false>, t0, nullptr, s);
-        else go(gemm_int8_big_kernel<false, false>, t0, nullptr, s);
+        const int64_t row_bytes = max_rows * g.N * 4, cache = (int64_t)256 << 20;
+        if (prob) go(gemm_int8_big_kernel<true, true, 0, 0>, t0, nullptr, s);
+        else if (fc1) go(gemm_int8_big_kernel<true, false, 0, 0>, t0, nullptr, s);
+        else if (row_bytes < cache) go(gemm_int8_big_kernel<false, false, 0, 0>, t0, nullptr, s);
+        else if (row_bytes < 2 * cache) go(gemm_int8_big_kernel<false, false, 0, kNonTemporal>, t0, nullptr, s);
+        else go(gemm_int8_big_kernel<false, false, kNonTemporal, kNonTemporal>, t0, nullptr, s);
         small_start = nullptr;
         if (s_small) ss = s_small;
     }

@@ -54,8 +54,8 @@ hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t
                             hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
                                   hipEvent_t t0, hipEvent_t t1);
-hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
-                            hipEvent_t t1, hipStream_t s_small = nullptr);
+hipError_t launch_gemm_int8(bool fc1, const GemmArgs& g, int64_t max_rows, int num_cu, hipStream_t s,
+                            hipEvent_t t0, hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_mxfp8(bool fc1, bool w4, const MxGemmArgs& g, int num_cu, hipStream_t s,
                              hipEvent_t t0, hipEvent_t t1);
 }  // namespace moe
@@ -667,10 +667,10 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
             e = hipEventRecord(ss->fork, stream);
             if (e == hipSuccess) e = hipStreamWaitEvent(ss->s, ss->fork, 0);
             if (e != hipSuccess) return hip_fail(e, "moe_forward: fork");
-            e = launch_gemm_int8(true, g1, h->num_cu, stream, nullptr, nullptr, ss->s);
+            e = launch_gemm_int8(true, g1, rows.cap, h->num_cu, stream, nullptr, nullptr, ss->s);
             if (e == hipSuccess) e = launch_quant_rows_int8(rows, &big, h->num_cu, stream);
             if (e == hipSuccess) e = launch_quant_rows_int8(rows, &small, h->num_cu, ss->s);
-            if (e == hipSuccess) e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr, ss->s);
+            if (e == hipSuccess) e = launch_gemm_int8(false, g2, rows.cap, h->num_cu, stream, nullptr, nullptr, ss->s);
             // the join is enqueued whatever was launched, so that a failed call leaves
             // nothing running beside the caller's stream
             hipError_t j = hipEventRecord(ss->join, ss->s);
@@ -678,11 +678,11 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
             if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1, quant-h or FC2 launch");
             if (j != hipSuccess) return hip_fail(j, "moe_forward: join");
         } else {
-            e = launch_gemm_int8(true, g1, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
+            e = launch_gemm_int8(true, g1, rows.cap, h->num_cu, stream, stage_event(h, 2), stage_event(h, 3));
             if (e != hipSuccess) return hip_fail(e, "moe_forward: FC1 launch");
             e = launch_quant_rows_int8(rows, nullptr, h->num_cu, stream);
             if (e != hipSuccess) return hip_fail(e, "moe_forward: quant-h launch");
-            e = launch_gemm_int8(false, g2, h->num_cu, stream, nullptr, nullptr);
+            e = launch_gemm_int8(false, g2, rows.cap, h->num_cu, stream, nullptr, nullptr);
             if (e != hipSuccess) return hip_fail(e, "moe_forward: FC2 launch");
         }
         if ((e = mark(h, 4, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
