@@ -325,20 +325,26 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
         const bool has_a = wid < ng;                 // this wave loads activation block wid
         const int nl = (has_a ? 1 : 0) + (has_cols ? 4 : 0);
 
-        // int8: lane l's activation row, for its scale in the epilogue; looked up here,
-        // beside the rows' own lookup, so that the epilogue waits for one round trip
-        // less (64 tokens, hidden 128: 24.1 -> 23.6 us a forward; 256 tokens, hidden
-        // 2048: 87.5 -> 86.6)
+        // int8: lane l holds the activation row of tile row l and its scale, and the scales
+        // of its two columns.  They are fetched here, older than the ring's loads, so that
+        // the epilogue waits for nothing and the rows' loads need no lookup of their own
+        // (against the rows' lookup alone here, scales in the epilogue: 64 tokens, hidden
+        // 128, 23.65 -> 23.36 us a forward; 256 tokens, hidden 2048, 86.4 / 86.7)
         int srow = row0 + min(lane, rows - 1);
-        if constexpr (Op::kScaled && FC1) {
-            srow = g.perm_src[srow] / g.topk;
-            asm volatile("" : "+v"(srow));           // (landed before the loads below)
+        float rs = 1.0f, cs[2] = {1.0f, 1.0f};
+        if constexpr (Op::kScaled) {
+            if constexpr (FC1) srow = g.perm_src[srow] / g.topk;
+            rs = g.a_scale[srow];
+            const float* wsc = g.w_scale + (int64_t)e * g.N + c32;
+            cs[0] = wsc[min(cb * 64, g.N - 32)];
+            cs[1] = wsc[min(cb * 64 + 32, g.N - 32)];
         }
         const uint16_t* arow = g.A;
         if (has_a) {
             const int r = min(16 * wid + (lane >> 2), rows - 1);
             int64_t src = row0 + r;
-            if constexpr (FC1) src = g.perm_src[src] / g.topk;
+            if constexpr (Op::kScaled) src = __builtin_amdgcn_ds_bpermute(4 * r, srow);
+            else if constexpr (FC1) src = g.perm_src[src] / g.topk;
             arow = g.A + src * K + 8 * ((lane & 3) ^ big_swz(lane >> 2));
         }
         if constexpr (FUSE >= 2) {
@@ -418,14 +424,6 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
             if constexpr (FUSE == 1) small_release(g, mt);
             if constexpr (FUSE == 3) small_finalize(g, fin_lds, ct, row0, rows);
             continue;
-        }
-        // int8: lane l holds the scale of row l, and those of its two columns
-        float rs = 1.0f, cs[2] = {1.0f, 1.0f};
-        if constexpr (Op::kScaled) {
-            rs = g.a_scale[srow];
-            const float* wsc = g.w_scale + (int64_t)e * g.N + c32;
-            cs[0] = wsc[cb * 64];
-            cs[1] = wsc[min(cb * 64 + 32, g.N - 32)];
         }
         if constexpr (FC1) {
             // column block 0 is the gate half, 1 the up half of interleave block cb
