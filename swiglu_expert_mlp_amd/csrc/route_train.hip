@@ -119,15 +119,16 @@ struct Row {
         }
     }
     // z becomes the softmax (all 0 for a row of -inf, which leaves nothing, and
-    // then lse is 0 too); returns lse
+    // then lse is 0 too); returns lse.  fmaxf drops NaN, so the maximum does not
+    // tell a row of -inf from one that has NaN besides: the sum does, being 0 only
+    // for the first (a finite maximum adds exp(0)) and NaN for the second.
     __device__ __forceinline__ float softmax()
     {
         float m = z[0];
 #pragma unroll
         for (int i = 1; i < 4 * N; ++i) m = fmaxf(m, z[i]);
         m = token_max<LPT>(m);
-        const bool none = m == -INFINITY;
-        if (none) m = 0.0f;
+        if (m == -INFINITY) m = 0.0f;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i) {
@@ -135,6 +136,7 @@ struct Row {
             s += z[i];
         }
         s = token_sum<LPT>(s);
+        const bool none = s == 0.0f;
         const float r = none ? 0.0f : 1.0f / s;
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i) z[i] *= r;
