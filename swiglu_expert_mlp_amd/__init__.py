@@ -133,18 +133,31 @@ def _dev(t, name, dtypes, shape=None):
     return t.data_ptr()
 
 
-def _on_current(stream, inputs, made=()):
-    """The router's training calls run on the current device: every tensor has to be there.
-    Tensors the call itself made are kept until `stream` is done with them."""
+def _on_current(stream, inputs):
+    """A call runs on the current device: its stream and every tensor have to be there."""
     torch = _torch()
     dev = torch.cuda.current_device()
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream must be of the current device cuda:{dev}, got {stream.device}")
     for t in inputs:
         d = getattr(t, "device", None)      # (_dev refuses what is no GPU tensor)
         if isinstance(d, torch.device) and d.type == "cuda" and d.index != dev:
             raise ValueError(f"tensors must be on the current device cuda:{dev}, got {d}")
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
+
+
+def _empty(stream, shape, dtype, device, returned=True):
+    """A tensor that a call on `stream` makes itself.  With another stream than the current
+    one it comes from that stream's memory: a block freed on the current stream may have work
+    pending there, which `stream` does not wait for.  One that is `returned` for use on the
+    current stream is not reused before that stream is done with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 class MoE:
@@ -316,7 +329,7 @@ class MoE:
     def _balance_args(self, logits, ids, live, losses, counts, prob_sums, ws, mask, stream):
         torch = _torch()
         T_cap = logits.shape[0]
-        _on_current(None, (logits, ids, live, losses, counts, prob_sums, ws, mask))
+        _on_current(stream, (logits, ids, live, losses, counts, prob_sums, ws, mask))
         return (self._h, _dev(logits, "logits", (torch.float32,), (T_cap, self.E)),
                 _dev(ids, "ids", (torch.int32,), (T_cap, self.topk)), T_cap,
                 _dev(live, "live", (torch.int32,)), self._mask(mask, T_cap),
@@ -332,16 +345,15 @@ class MoE:
         mask: bool or uint8 [T_cap], tokens with 0 are left out."""
         torch = _torch()
         dev = logits.device
-        given = (losses, counts, prob_sums, ws)
         if losses is None:
-            losses = torch.empty(2, dtype=torch.float32, device=dev)
+            losses = _empty(stream, 2, torch.float32, dev)
         if counts is None:
-            counts = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+            counts = _empty(stream, self.E + 1, torch.int32, dev)
         if prob_sums is None:
-            prob_sums = torch.empty(self.E, dtype=torch.float32, device=dev)
+            prob_sums = _empty(stream, self.E, torch.float32, dev)
         if ws is None:
-            ws = self.new_balance_workspace(logits.shape[0], dev)
-        _on_current(stream, (), [t for t, g in zip((losses, counts, prob_sums, ws), given) if g is None])
+            ws = _empty(stream, int(lib().moe_balance_workspace_bytes(self._h, logits.shape[0])), torch.uint8, dev,
+                        returned=False)
         _check(lib().moe_balance(*self._balance_args(logits, ids, live, losses, counts, prob_sums, ws, mask,
                                                      stream)), "moe_balance")
         return losses, counts, prob_sums
@@ -350,7 +362,7 @@ class MoE:
         torch = _torch()
         T_cap = logits.shape[0]
         f32, i32 = (torch.float32,), (torch.int32,)
-        _on_current(None, (logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask))
+        _on_current(stream, (logits, ids, live, d_logits, probs, d_probs, counts, d_losses, mask))
         opt = lambda t, name, dt, shape: None if t is None else _dev(t, name, dt, shape)
         return (self._h, _dev(logits, "logits", f32, (T_cap, self.E)),
                 opt(ids, "ids", i32, (T_cap, self.topk)), opt(probs, "probs", f32, (T_cap, self.topk)),
@@ -365,8 +377,7 @@ class MoE:
         (probs with d_probs), of balance's losses (counts with d_losses, fp32 [2]), or of both."""
         torch = _torch()
         if d_logits is None:
-            d_logits = torch.empty(logits.shape, dtype=torch.float32, device=logits.device)
-            _on_current(stream, (), (d_logits,))
+            d_logits = _empty(stream, logits.shape, torch.float32, logits.device)
         _check(lib().moe_route_backward(*self._route_backward_args(logits, ids, live, d_logits, probs, d_probs,
                                                                    counts, d_losses, mask, stream)),
                "moe_route_backward")
@@ -375,7 +386,7 @@ class MoE:
     def _probs_backward_args(self, d_out, ids, d_probs, ws, stream):
         torch = _torch()
         T_cap = d_out.shape[0]
-        _on_current(None, (d_out, ids, d_probs, ws))
+        _on_current(stream, (d_out, ids, d_probs, ws))
         p = _dev(d_out, "d_out", (torch.float32, torch.bfloat16), (T_cap, self.H))
         return (self._h, p, COMBINES["fp32" if d_out.dtype == torch.float32 else "bf16"],
                 _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk)), T_cap,
@@ -387,8 +398,7 @@ class MoE:
         [T_cap, topk], from d_out [T_cap, H] (fp32 or bf16) and that forward's expert ids."""
         torch = _torch()
         if d_probs is None:
-            d_probs = torch.empty((d_out.shape[0], self.topk), dtype=torch.float32, device=d_out.device)
-            _on_current(stream, (), (d_probs,))
+            d_probs = _empty(stream, (d_out.shape[0], self.topk), torch.float32, d_out.device)
         _check(lib().moe_probs_backward(*self._probs_backward_args(d_out, ids, d_probs, ws, stream)),
                "moe_probs_backward")
         return d_probs

@@ -61,3 +61,70 @@ def test_one_bad_row_reaches_both_losses_and_its_gradient(bad, E, T):
     assert np.array_equal(counts, rc) and np.all(np.abs(sums - rs) <= bs) and np.all(np.abs(losses - rl) <= bl)
     grad = moe.route_backward(dev(z), None, live_tensor(T), mask=dev(others), **g).cpu().numpy()
     assert not grad[at].any() and np.isfinite(grad).all()
+
+
+# ------------------------------------------------------------- calls on another stream
+
+def _pending_writes(sizes):
+    """Blocks of these sizes, freed on the current stream behind some milliseconds of its work
+    that ends by overwriting them."""
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    busy = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    for _ in range(40):
+        busy.fill_(1.0)
+    for b in blocks:
+        b.fill_(0xFF)
+
+
+def _nbytes(*tensors):
+    return [t.numel() * t.element_size() for t in tensors]
+
+
+@pytest.mark.parametrize("T", [200, 6000])
+def test_training_calls_on_a_stream_do_not_write_where_work_is_pending(T):
+    """What a call on another stream makes for itself is not memory that the current stream
+    has freed with writes to it still to come."""
+    E, k, H = 256, 4, 64
+    moe = moe_of(E, k, H)
+    z, ids, q, d, _ = (dev(a) for a in make(T, T, E, k))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    moe.load_weights(torch.randn(E, 64, H, device="cuda", generator=g).bfloat16(),
+                     torch.randn(E, H, 32, device="cuda", generator=g).bfloat16())
+    x, d_out = torch.randn(T, H, device="cuda", generator=g).bfloat16(), torch.randn(T, H, device="cuda", generator=g)
+    live, ws = live_tensor(T), moe.new_workspace(T)
+    moe.forward(x, ids, q, live, ws=ws)
+    calls = {
+        "balance": lambda **kw: moe.balance(z, ids, live, **kw),
+        "route_backward": lambda **kw: (moe.route_backward(z, ids, live, probs=q, d_probs=d, **kw),),
+        "probs_backward": lambda **kw: (moe.probs_backward(d_out, ids, ws, **kw),),
+    }
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        ref = [r.cpu() for r in call()]
+        torch.cuda.synchronize()
+        _pending_writes(_nbytes(*ref, moe.new_balance_workspace(T)))
+        got = call(stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b.cpu()) for a, b in zip(ref, got)), name
+
+
+def test_a_returned_tensor_is_kept_for_the_current_stream():
+    """A result of a call on another stream, read by pending work of the current one when it
+    is dropped, is not handed to the next call on that stream."""
+    E, k, T = 256, 4, 6000
+    moe = moe_of(E, k)
+    z, ids, q, d, _ = (dev(a) for a in make(T, T, E, k))
+    live, side = live_tensor(T), torch.cuda.Stream()
+    ref, other = moe.route_backward(z, ids, live, probs=q, d_probs=d), q * 2
+    busy = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    grad = moe.route_backward(z, ids, live, probs=q, d_probs=d, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(40):
+        busy.fill_(1.0)
+    copy = grad.clone()
+    del grad
+    for _ in range(3):
+        moe.route_backward(z, ids, live, probs=other, d_probs=d, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, ref)

@@ -123,3 +123,17 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         m._on_current(None, (None, Fake()))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     m._on_current(None, (None, Fake()))
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    import torch
+    import swiglu_expert_mlp_amd as m
+
+    class Stream:
+        device = torch.device("cuda:1")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="stream"):
+        m._on_current(Stream(), ())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    m._on_current(Stream(), ())
