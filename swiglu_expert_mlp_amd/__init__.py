@@ -175,6 +175,7 @@ class MoE:
         self._destroy = lib().moe_destroy
         self.E, self.H, self.F, self.topk, self.precision = E, H, F, topk, precision
         self.kbuf = None
+        self._bound_streams = {}
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -202,18 +203,18 @@ class MoE:
 
     def load_weights(self, w1, w2, kbuf=None, stream=None):
         """Pack bf16 w1 [E, 2F, H] (gate rows first) and w2 [E, H, F] into kbuf
-        (allocated if None).  Calling again with the same kbuf is the refit."""
+        (allocated if None).  Calling again with the same kbuf is the refit; with
+        another one, forwards enqueued before keep theirs until they are done."""
         torch = _torch()
         bf = (torch.bfloat16, torch.int16, torch.uint16)
         p1 = _dev(w1, "w1", bf, (self.E, 2 * self.F, self.H))
         p2 = _dev(w2, "w2", bf, (self.E, self.H, self.F))
         if kbuf is None:
-            kbuf = torch.empty(self.weight_bytes, dtype=torch.uint8, device=w1.device)
+            kbuf = _empty(stream, self.weight_bytes, torch.uint8, w1.device)
         pk = _dev(kbuf, "kbuf", (torch.uint8,))
         _check(lib().moe_load_weights(self._h, p1, p2, pk, kbuf.numel(), _stream(stream)),
                "moe_load_weights")
-        self.kbuf = kbuf          # keep the buffer alive as long as the handle reads it
-        return kbuf
+        return self._set_kbuf(kbuf)
 
     def load_quantized(self, w1, w1_scale, w2, w2_scale, kbuf=None, stream=None):
         """int8 handles: pack weights that are quantized already, as load_weights does
@@ -225,11 +226,29 @@ class MoE:
         p2 = _dev(w2, "w2", (torch.int8,), (self.E, self.H, self.F))
         q2 = _dev(w2_scale, "w2_scale", (torch.float32,), (self.E, self.H))
         if kbuf is None:
-            kbuf = torch.empty(self.weight_bytes, dtype=torch.uint8, device=w1.device)
+            kbuf = _empty(stream, self.weight_bytes, torch.uint8, w1.device)
         pk = _dev(kbuf, "kbuf", (torch.uint8,))
         _check(lib().moe_load_quantized(self._h, p1, q1, p2, q2, pk, kbuf.numel(), _stream(stream)),
                "moe_load_quantized")
-        self.kbuf = kbuf
+        return self._set_kbuf(kbuf)
+
+    def _kbuf_used_on(self, stream, bound=False):
+        """The weights' memory, once the handle drops it, is not reused before `stream` (the
+        current one if None) is done with it; bound: nor is that of later weights.  An
+        external stream may be gone by then: its owner orders the refit."""
+        torch = _torch()
+        if isinstance(stream, torch.cuda.ExternalStream):
+            return
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if bound:
+            self._bound_streams[s.cuda_stream] = s
+        if self.kbuf is not None:
+            self.kbuf.record_stream(s)
+
+    def _set_kbuf(self, kbuf):
+        self.kbuf = kbuf          # keep the buffer alive as long as the handle reads it
+        for s in self._bound_streams.values():
+            kbuf.record_stream(s)
         return kbuf
 
     def route(self, logits, live, ids=None, probs=None, ws=None, stream=None):
@@ -238,11 +257,11 @@ class MoE:
         pl = _dev(logits, "logits", (torch.float32,), (T_cap, self.E))
         plive = _dev(live, "live", (torch.int32,))
         if ids is None:
-            ids = torch.empty((T_cap, self.topk), dtype=torch.int32, device=logits.device)
+            ids = _empty(stream, (T_cap, self.topk), torch.int32, logits.device)
         if probs is None:
-            probs = torch.empty((T_cap, self.topk), dtype=torch.float32, device=logits.device)
+            probs = _empty(stream, (T_cap, self.topk), torch.float32, logits.device)
         if ws is None:
-            ws = self.new_workspace(T_cap, logits.device)
+            ws = _empty(stream, self.workspace_bytes(T_cap), torch.uint8, logits.device, returned=False)
         pi = _dev(ids, "ids", (torch.int32,), (T_cap, self.topk))
         pp = _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         pw = _dev(ws, "ws", (torch.uint8,))
@@ -284,11 +303,12 @@ class MoE:
         pp = None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         plive = _dev(live, "live", (torch.int32,))
         if out is None:
-            out = torch.empty(shape, dtype=alloc, device=x.device)
+            out = _empty(stream, shape, alloc, x.device)
         po = _dev(out, "out", dts, shape)
         if ws is None:
-            ws = self.new_workspace(T_cap, x.device)
+            ws = _empty(stream, self.workspace_bytes(T_cap), torch.uint8, x.device, returned=False)
         pw = _dev(ws, "ws", (torch.uint8,))
+        self._kbuf_used_on(stream)
         _check(lib().moe_forward_ex(self._h, px, pi, pp, T_cap, plive,
                                     self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize), po, pw,
                                     ws.numel(), _stream(stream)), "moe_forward")
@@ -307,8 +327,9 @@ class MoE:
         pp = None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         plive = _dev(live, "live", (torch.int32,))
         if out is None:
-            out = torch.empty(shape, dtype=alloc, device=x.device)
+            out = _empty(stream, shape, alloc, x.device)
         po = _dev(out, "out", dts, shape)
+        self._kbuf_used_on(stream)
         _check(lib().moe_forward_noalloc(self._h, px, pi, pp, T_cap, plive,
                                          self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize), po,
                                          _stream(stream)), "moe_forward_noalloc")
@@ -496,6 +517,7 @@ class MoE:
                 self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize),
                 _dev(out, "out", dts, shape),
                 _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
+        self._kbuf_used_on(stream, bound=True)
         fn = lib().moe_forward_ex
         keep = (x, ids, probs, live, out, ws)
 

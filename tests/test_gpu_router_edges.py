@@ -128,3 +128,76 @@ def test_a_returned_tensor_is_kept_for_the_current_stream():
         moe.route_backward(z, ids, live, probs=other, d_probs=d, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, ref)
+
+
+# ------------------------------------------------------------- weights and forwards on another stream
+
+def _int8_layer(E=6, k=2, H=128, F=96, T=900, seed=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    draw = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    w1 = (draw(E, 2 * F, H) * 20).round().clamp(-127, 127).to(torch.int8)
+    w2 = (draw(E, H, F) * 20).round().clamp(-127, 127).to(torch.int8)
+    codes = (w1, torch.full((E, 2 * F), 0.01, device="cuda"), w2, torch.full((E, H), 0.01, device="cuda"))
+    z = draw(T, E)
+    return moe_of(E, k, H, F, "int8"), codes, draw(T, H).bfloat16(), z, live_tensor(T)
+
+
+def test_loads_and_forwards_on_a_stream_do_not_write_where_work_is_pending():
+    """As the training calls: the packed weights, the router's results, the forward's output
+    and its workspace."""
+    moe, codes, x, z, live = _int8_layer()
+    T = x.shape[0]
+    moe.load_quantized(*codes)
+    ids, probs = moe.route(z, live)
+    out = moe.forward(x, ids, probs, live)
+    ref = [t.cpu() for t in (moe.kbuf, ids, probs, out)]
+    side = torch.cuda.Stream()
+    calls = {
+        "load": lambda: (moe.load_quantized(*codes, stream=side),),
+        "route": lambda: moe.route(z, live, stream=side),
+        "forward": lambda: (moe.forward(x, ids, probs, live, stream=side),),
+        "forward_noalloc": lambda: (moe.forward_noalloc(x[:300], ids[:300], probs[:300], live, stream=side),),
+    }
+    want = {"load": ref[:1], "route": ref[1:3], "forward": ref[3:], "forward_noalloc": [ref[3][:300]]}
+    for name, call in calls.items():
+        torch.cuda.synchronize()
+        _pending_writes(_nbytes(*want[name], moe.new_workspace(T)))
+        got = call()
+        torch.cuda.synchronize()
+        if name == "load":        # (the padding of the sections is not written)
+            got = (moe.forward(x, ids, probs, live),)
+            assert torch.equal(got[0].cpu(), ref[3])
+        else:
+            assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want[name])), name
+
+
+@pytest.mark.parametrize("bound", [False, True])
+@pytest.mark.parametrize("load", ["load_weights", "load_quantized"])
+def test_a_refit_keeps_the_old_weights_for_forwards_in_flight(load, bound):
+    """A forward waits on its stream for earlier work; the refit drops the weights that it will
+    read and the next allocations of the same size are overwritten at once."""
+    moe, codes, x, z, live = _int8_layer(seed=2)
+    w = codes if load == "load_quantized" else tuple(
+        (codes[i].float() * codes[i + 1][..., None]).bfloat16() for i in (0, 2))
+    ids, probs = moe.route(z, live)
+    ws, out = moe.new_workspace(x.shape[0]), torch.zeros(x.shape[0], moe.H, device="cuda")
+    getattr(moe, load)(*w)
+    moe.forward(x, ids, probs, live, out=out, ws=ws)
+    ref = out.clone()
+    side = torch.cuda.Stream()
+    call = moe.bind_forward(x, ids, probs, live, out, ws, stream=side)
+    getattr(moe, load)(*w)                      # weights newer than the binding
+    out.zero_()
+    busy = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            busy.fill_(1.0)
+    if bound:
+        call()
+    else:
+        moe.forward(x, ids, probs, live, out=out, ws=ws, stream=side)
+    getattr(moe, load)(*w)                      # drops them
+    junk = [torch.full((moe.weight_bytes,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and len(junk) == 3
