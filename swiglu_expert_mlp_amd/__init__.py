@@ -206,6 +206,7 @@ class MoE:
         (allocated if None).  Calling again with the same kbuf is the refit; with
         another one, forwards enqueued before keep theirs until they are done."""
         torch = _torch()
+        _on_current(stream, (w1, w2, kbuf))
         bf = (torch.bfloat16, torch.int16, torch.uint16)
         p1 = _dev(w1, "w1", bf, (self.E, 2 * self.F, self.H))
         p2 = _dev(w2, "w2", bf, (self.E, self.H, self.F))
@@ -221,6 +222,7 @@ class MoE:
         for bf16 ones.  w1 int8 [E, 2F, H] (gate rows first) with w1_scale fp32 [E, 2F],
         w2 int8 [E, H, F] with w2_scale fp32 [E, H]."""
         torch = _torch()
+        _on_current(stream, (w1, w1_scale, w2, w2_scale, kbuf))
         p1 = _dev(w1, "w1", (torch.int8,), (self.E, 2 * self.F, self.H))
         q1 = _dev(w1_scale, "w1_scale", (torch.float32,), (self.E, 2 * self.F))
         p2 = _dev(w2, "w2", (torch.int8,), (self.E, self.H, self.F))
@@ -253,6 +255,7 @@ class MoE:
 
     def route(self, logits, live, ids=None, probs=None, ws=None, stream=None):
         torch = _torch()
+        _on_current(stream, (logits, live, ids, probs, ws))
         T_cap = logits.shape[0]
         pl = _dev(logits, "logits", (torch.float32,), (T_cap, self.E))
         plive = _dev(live, "live", (torch.int32,))
@@ -296,6 +299,7 @@ class MoE:
         fused_ffn: FC1 and FC2 in one persistent launch (bf16 weights).
         fused_finalize: FC1, FC2 and the finalize in one persistent launch (bf16 weights)."""
         torch = _torch()
+        _on_current(stream, (x, ids, probs, live, out, ws))
         T_cap = x.shape[0]
         dts, shape, alloc = self._out_spec(T_cap, combine)
         px = _dev(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (T_cap, self.H))
@@ -320,6 +324,7 @@ class MoE:
         as workspace (no caller workspace, nothing allocated by the library).
         Calls that overlap on one GPU race; the capacity is bounded."""
         torch = _torch()
+        _on_current(stream, (x, ids, probs, live, out))
         T_cap = x.shape[0]
         dts, shape, alloc = self._out_spec(T_cap, combine)
         px = _dev(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (T_cap, self.H))
@@ -508,6 +513,7 @@ class MoE:
         enqueues this forward (for launch loops where per-call checks would
         cost more host time than the GPU work)."""
         torch = _torch()
+        _on_current(stream, (x, ids, probs, live, out, ws))
         T_cap = x.shape[0]
         dts, shape, _ = self._out_spec(T_cap, combine)
         args = (self._h, _dev(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (T_cap, self.H)),
@@ -529,6 +535,7 @@ class MoE:
     def bind_route(self, logits, live, ids, probs, ws, stream=None):
         """As bind_forward, for the router."""
         torch = _torch()
+        _on_current(stream, (logits, live, ids, probs, ws))
         T_cap = logits.shape[0]
         args = (self._h, _dev(logits, "logits", (torch.float32,), (T_cap, self.E)), T_cap,
                 _dev(live, "live", (torch.int32,)),

@@ -137,3 +137,22 @@ def test_streams_of_another_device_are_refused(monkeypatch):
         m._on_current(Stream(), ())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     m._on_current(Stream(), ())
+
+
+@pytest.mark.parametrize("call", ["load_weights", "load_quantized", "route", "forward", "forward_noalloc",
+                                  "bind_forward", "bind_route"])
+def test_every_call_refuses_tensors_of_another_device(call, monkeypatch):
+    """The kernels run on the current device: another one's memory would be read from there."""
+    import torch
+    import swiglu_expert_mlp_amd as m
+
+    class Fake:
+        device = torch.device("cuda:1")
+        shape = (4, 8)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    moe = m.MoE(8, 32, 32, 2, "int8")
+    n = {"load_weights": 2, "load_quantized": 4, "route": 2, "forward": 4, "forward_noalloc": 4, "bind_forward": 6,
+         "bind_route": 5}[call]
+    with pytest.raises(ValueError, match="current device"):
+        getattr(moe, call)(*[Fake()] * n)
