@@ -525,7 +525,7 @@ class MoE:
                 _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
         self._kbuf_used_on(stream, bound=True)
         fn = lib().moe_forward_ex
-        keep = (x, ids, probs, live, out, ws)
+        keep = (self, x, ids, probs, live, out, ws)
 
         def call():
             _check(fn(*args), "moe_forward")
@@ -543,7 +543,7 @@ class MoE:
                 _dev(probs, "probs", (torch.float32,), (T_cap, self.topk)),
                 _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
         fn = lib().moe_route
-        keep = (logits, live, ids, probs, ws)
+        keep = (self, logits, live, ids, probs, ws)
 
         def call():
             _check(fn(*args), "moe_route")

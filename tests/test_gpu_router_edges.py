@@ -201,3 +201,25 @@ def test_a_refit_keeps_the_old_weights_for_forwards_in_flight(load, bound):
     junk = [torch.full((moe.weight_bytes,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(out, ref) and len(junk) == 3
+
+
+def test_bound_calls_keep_their_handle():
+    """A bound call outlives the name of its layer: the handle it passes is not freed."""
+    import gc
+    import weakref
+    moe, codes, x, z, live = _int8_layer(T=40)
+    moe.load_quantized(*codes)
+    ids, probs = moe.route(z, live)
+    ws, out = moe.new_workspace(40), torch.zeros(40, moe.H, device="cuda")
+    ref = moe.forward(x, ids, probs, live)
+    calls = [moe.bind_route(z, live, ids, probs, ws), moe.bind_forward(x, ids, probs, live, out, ws)]
+    seen = weakref.ref(moe)
+    del moe
+    gc.collect()
+    assert seen() is not None
+    for call in calls:
+        call()
+    assert torch.equal(out, ref)
+    del call, calls
+    gc.collect()
+    assert seen() is None
