@@ -376,7 +376,8 @@ moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* 
  * combine; with MOE_APPLY_TOPK_IN_FC1 they carry their probabilities and the
  * call flags MOE_DEVERR_WEIGHTED_ROWS.  A workspace whose last forward had
  * another shape, precision or T_cap (or none) is flagged MOE_DEVERR_NO_ROWS.
- * Both are reported by moe_check, added to the forward's bits, and nothing is
+ * Both are reported by moe_check, added to the bits that the last call on ws
+ * left there (none in a workspace that no call has run on), and nothing else is
  * written then.
  *   d_out: [T_cap][H], fp32 (combine MOE_COMBINE_FP32) or bf16
  *   (MOE_COMBINE_BF16); expert_ids: as given to that forward; d_probs: fp32

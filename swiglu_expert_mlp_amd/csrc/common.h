@@ -60,6 +60,7 @@ constexpr uint32_t kErrLiveNeg = 8u;
 constexpr uint32_t kErrFusedWait = 16u;
 constexpr uint32_t kErrNoRows = 32u;
 constexpr uint32_t kErrWeightedRows = 64u;
+constexpr uint32_t kErrMark = 0x6d6f6531u;      // WsHeader::mark
 
 // ---------------------------------------------------------------- formats
 
@@ -203,7 +204,8 @@ struct WsHeader {
     int32_t n_tiles_big;   // M tiles in the LDS-staged table
     uint64_t tag;          // layout of the last forward (forward_tag)
     int32_t weighted;      // 1: its FC2 rows carry their probabilities (applied inside FC1)
-    int32_t pad[55];
+    uint32_t mark;         // kErrMark: a call has written err (in a new workspace it is anything)
+    int32_t pad[54];
 };
 
 // Identifies a workspace layout: a workspace whose header holds this tag was last

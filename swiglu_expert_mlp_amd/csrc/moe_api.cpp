@@ -25,7 +25,7 @@ hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap
 hipError_t launch_route_backward(const float* logits, const int32_t* ids, const float* probs, const float* d_probs,
                                  int64_t T_cap, const int32_t* live, const uint8_t* mask, const int32_t* counts,
                                  const float* d_losses, float* d_logits, int E, int k, int num_cu, hipStream_t s);
-hipError_t launch_probs_backward(const WsHeader* hdr, uint64_t tag, const float* O, const int32_t* dst,
+hipError_t launch_probs_backward(WsHeader* hdr, uint64_t tag, const float* O, const int32_t* dst,
                                  const int32_t* ids, const void* d_out, int bf16, float* d_probs, int64_t T_cap, int k,
                                  int H, int num_cu, hipStream_t s);
 hipError_t launch_finalize(const float* O, const int32_t* dst, const float* sorted_probs,
@@ -449,7 +449,7 @@ moe_status moe_probs_backward(moe_handle h, const void* d_out, int combine, cons
     if (T_cap == 0) return MOE_OK;
     char* w = (char*)ws;
     const hipError_t e =
-        launch_probs_backward((const WsHeader*)(w + L.hdr), forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap),
+        launch_probs_backward((WsHeader*)(w + L.hdr), forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap),
                               (const float*)(w + L.obuf), (const int32_t*)(w + L.dst), expert_ids, d_out,
                               combine == MOE_COMBINE_BF16, d_probs, T_cap, h->k, h->H, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_probs_backward: launch");

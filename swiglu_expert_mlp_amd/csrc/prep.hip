@@ -248,6 +248,7 @@ __device__ void prep_finish(const PrepArgs& a, int T, int nch, int32_t live, int
         uint32_t all = (live < 0 ? kErrLiveNeg : 0u) | (live > a.T_cap ? kErrLiveHigh : 0u);
         for (int w = 0; w < (int)(blockDim.x >> 6); ++w) all |= (uint32_t)lds[w];
         a.hdr->err = all;
+        a.hdr->mark = kErrMark;
         a.hdr->T = T;
         a.hdr->n_tiles = ntotal;
         a.hdr->n_tiles_big = nbig;

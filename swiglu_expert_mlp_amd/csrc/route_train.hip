@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(BalanceArgs a)
         if (blockIdx.x == 0) {
             *a.ticket = 0;
             a.hdr->err = 0;
+            a.hdr->mark = kErrMark;
             a.hdr->tag = 0;
         }
     }
@@ -587,8 +588,7 @@ hipError_t launch_route_backward(const float* logits, const int32_t* ids, const 
 // tokens, top-8, hidden 2048: 183 us, 6.6 TB/s, against 187 with a workgroup each; 256
 // tokens, top-6: 4.7 us against 14.3 with a wave each).
 struct ProbsGradArgs {
-    const WsHeader* hdr;
-    uint32_t* err;
+    WsHeader* hdr;
     uint64_t tag;              // of the forward whose rows are read (WsHeader::tag)
     const float* O;
     const int32_t* dst;
@@ -617,7 +617,11 @@ __global__ void __launch_bounds__(512) probs_backward_kernel(ProbsGradArgs a)
     indices();
     const bool stale = a.hdr->tag != a.tag;
     if (stale || a.hdr->weighted) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, stale ? kErrNoRows : kErrWeightedRows);
+        // the bit joins those of an earlier call; in a workspace of none it is the word
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            a.hdr->err = (a.hdr->mark == kErrMark ? a.hdr->err : 0u) | (stale ? kErrNoRows : kErrWeightedRows);
+            a.hdr->mark = kErrMark;
+        }
         return;
     }
     const uint32_t n_rows = (uint32_t)a.hdr->n_rows;
@@ -682,11 +686,11 @@ __global__ void __launch_bounds__(512) probs_backward_kernel(ProbsGradArgs a)
     }
 }
 
-hipError_t launch_probs_backward(const WsHeader* hdr, uint64_t tag, const float* O, const int32_t* dst,
+hipError_t launch_probs_backward(WsHeader* hdr, uint64_t tag, const float* O, const int32_t* dst,
                                  const int32_t* ids, const void* d_out, int bf16, float* d_probs, int64_t T_cap, int k,
                                  int H, int num_cu, hipStream_t s)
 {
-    const ProbsGradArgs a{hdr, (uint32_t*)&hdr->err, tag, O, dst, ids, d_out, d_probs, T_cap, H};
+    const ProbsGradArgs a{hdr, tag, O, dst, ids, d_out, d_probs, T_cap, H};
     const bool few = T_cap <= (int64_t)num_cu * 8;
     int64_t blocks = few ? T_cap : (T_cap + 7) / 8;
     if (blocks > (int64_t)num_cu * 8) blocks = (int64_t)num_cu * 8;

@@ -223,3 +223,57 @@ def test_bound_calls_keep_their_handle():
     del call, calls
     gc.collect()
     assert seen() is None
+
+
+# ------------------------------------------------------------- error bits without a forward
+
+def _probs_setup():
+    moe, codes, x, z, live = _int8_layer(T=40)
+    moe.load_quantized(*codes)
+    d_out = torch.randn(40, moe.H, device="cuda")
+    got = torch.full((40, moe.topk), 12345.0, device="cuda")
+    return moe, x, z, live, d_out, got
+
+
+@pytest.mark.parametrize("fill", [0, 0x5A, 0xA5, 0xFF])
+def test_a_workspace_of_any_contents_gives_the_one_bit(fill):
+    """No call has run on the workspace: its error word is not one to add to."""
+    from swiglu_expert_mlp_amd import DEVERR_NO_ROWS
+    moe, x, z, live, d_out, got = _probs_setup()
+    ids = torch.zeros(40, moe.topk, dtype=torch.int32, device="cuda")
+    ws = moe.new_workspace(40)
+    ws.fill_(fill)
+    for _ in range(2):
+        moe.probs_backward(d_out, ids, ws, d_probs=got)
+        moe.probs_backward(d_out, ids, ws, d_probs=got)
+        assert moe.check(ws) == DEVERR_NO_ROWS
+        assert moe.check(ws) == 0
+    assert torch.all(got == 12345.0)
+
+
+def test_bits_of_earlier_calls_stay_beside_it():
+    from swiglu_expert_mlp_amd import (DEVERR_BAD_EXPERT_ID, DEVERR_LIVE_ABOVE_CAP, DEVERR_NO_ROWS,
+                                       DEVERR_WEIGHTED_ROWS)
+    moe, x, z, live, d_out, got = _probs_setup()
+    ws = moe.new_workspace(40)
+    ws.fill_(0x5A)
+    ids, probs = moe.route(z, live_tensor(50), ws=ws)            # a router alone: no rows
+    moe.probs_backward(d_out, ids, ws, d_probs=got)
+    assert moe.check(ws) == DEVERR_LIVE_ABOVE_CAP | DEVERR_NO_ROWS
+    bad = ids.clone()
+    bad[3, 0] = -1
+    moe.forward(x, bad, probs, live_tensor(40), ws=ws)
+    moe.probs_backward(d_out[:30], bad[:30].contiguous(), ws, d_probs=got[:30])      # another capacity
+    assert moe.check(ws) == DEVERR_BAD_EXPERT_ID | DEVERR_NO_ROWS
+    moe.forward(x, bad, probs, live_tensor(40), ws=ws, topk_in_fc1=True)
+    moe.probs_backward(d_out, bad, ws, d_probs=got)
+    assert moe.check(ws) == DEVERR_BAD_EXPERT_ID | DEVERR_WEIGHTED_ROWS
+    assert torch.all(got == 12345.0)
+    # balance's partials in the workspace: its word is known, and holds nothing
+    big, T = moe_of(64, 2), 1200
+    ws = big.new_workspace(T)
+    ws.fill_(0x5A)
+    zz = torch.randn(T, 64, device="cuda")
+    ids = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    big.balance(zz, ids, live_tensor(T), ws=ws)
+    assert big.check(ws) == 0
