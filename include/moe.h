@@ -41,7 +41,8 @@
  *     default priority, created by the first bf16 or int8 weight load there
  *     and kept until the process ends), forked from `stream` and joined back
  *     to it with events, so the work still completes in `stream` order and is
- *     captured with it.
+ *     captured with it.  While a capture holds the side stream, forwards outside
+ *     it run on their own stream alone.
  *   - The live token count is read from device memory (live_rows_dev, int32,
  *     in TOKENS).  It is clamped to [0, T_cap]; a value outside sets an error
  *     bit (see moe_check).  Token rows >= live are never read and rows >= live

@@ -240,6 +240,25 @@ static moe_status ensure_side_stream(int dev)
     return MOE_OK;
 }
 
+// Whether a forward on `stream` may fork onto the side stream (g_side_mu held).
+// A captured forward leaves the side stream in its capture until that ends: until
+// then no forward outside the capture may use it (its launches would go into the
+// graph, or the wait on an event from outside would end the capture), and such
+// a forward keeps its stages on its own stream.
+static bool side_stream_free(const SideStream& ss, hipStream_t stream)
+{
+    hipStreamCaptureStatus side = hipStreamCaptureStatusNone, own = hipStreamCaptureStatusNone;
+    unsigned long long side_id = 0, own_id = 0;
+    hipError_t e = hipStreamGetCaptureInfo(ss.s, &side, &side_id);
+    if (e == hipSuccess && side == hipStreamCaptureStatusNone) return true;
+    if (e == hipSuccess) e = hipStreamGetCaptureInfo(stream, &own, &own_id);
+    if (e != hipSuccess) {
+        (void)hipGetLastError();                 // (the launches' own error checks follow)
+        return false;
+    }
+    return side == hipStreamCaptureStatusActive && own == side && own_id == side_id;
+}
+
 extern "C" {
 
 const char* moe_last_error(void) { return g_err.c_str(); }
@@ -578,13 +597,18 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
             // 748 -> 721-728 us/step); above it, as at 16,384 tokens, the
             // 64-row launches rarely find a tile and the stages stay serial
             const bool few_small = (int64_t)T_cap * h->k >= (int64_t)4 * kBigMin * E;
-            if ((split1 || split2) && ss && ss->s && !h->record_stages && !few_small) {
+            std::unique_lock<std::mutex> lock(g_side_mu, std::defer_lock);
+            bool forked = (split1 || split2) && ss && ss->s && !h->record_stages && !few_small;
+            if (forked) {
+                lock.lock();
+                forked = side_stream_free(*ss, stream);
+            }
+            if (forked) {
                 // the 256-row chain on `stream`, the 64-row chain on the side
                 // stream: the two launches of a stage cover disjoint experts,
                 // and FC2's tiles of a design read only the rows its own
                 // design's FC1 tiles wrote; a stage of one launch (the 64-row
                 // kernel taking every tile) waits for both chains
-                std::lock_guard<std::mutex> lock(g_side_mu);
                 auto fork = [&]() {
                     hipError_t r = hipEventRecord(ss->fork, stream);
                     return r == hipSuccess ? hipStreamWaitEvent(ss->s, ss->fork, 0) : r;
@@ -660,10 +684,15 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
         // likely, the 64-row chain (FC1, its rows' quantization, FC2) runs on the
         // side stream; each chain covers the experts of one tile table
         const bool few_small = (int64_t)T_cap * h->k >= (int64_t)4 * kBigMin * E;
-        if (!g1.small_takes_big && !g2.small_takes_big && ss && ss->s && !h->record_stages && !few_small) {
+        std::unique_lock<std::mutex> lock(g_side_mu, std::defer_lock);
+        bool forked = !g1.small_takes_big && !g2.small_takes_big && ss && ss->s && !h->record_stages && !few_small;
+        if (forked) {
+            lock.lock();
+            forked = side_stream_free(*ss, stream);
+        }
+        if (forked) {
             const QuantTiles big{(const int2*)(w + L.tiles_big), &hdr->n_tiles_big, g1.offsets, kBigBMRows};
             const QuantTiles small{(const int2*)(w + L.tiles), &hdr->n_tiles, g1.offsets, kBM};
-            std::lock_guard<std::mutex> lock(g_side_mu);
             e = hipEventRecord(ss->fork, stream);
             if (e == hipSuccess) e = hipStreamWaitEvent(ss->s, ss->fork, 0);
             if (e != hipSuccess) return hip_fail(e, "moe_forward: fork");

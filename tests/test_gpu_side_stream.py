@@ -125,3 +125,46 @@ def test_two_caller_streams_share_one_handle():
     torch.cuda.synchronize()
     for which, o in outs:
         assert np.array_equal(o.cpu().numpy().view(np.uint32), refs[which]), which
+
+
+@pytest.mark.parametrize("precision", ["bf16", "int8"])
+def test_eager_forward_beside_a_capture(precision):
+    """A captured forward leaves the side stream in the capture until it ends: an eager forward
+    on another stream meanwhile, before and after another captured one, stays out of the graph;
+    the replays and later eager forwards give the same bits."""
+    from swiglu_expert_mlp_amd import MoE
+    w = Workload("beside", 1400, 1500, 256, 288 if precision == "int8" else 192, 8, 2, precision)
+    c = _skewed(Case(w, seed=23))
+    m = MoE(w.E, w.H, w.F, w.k, w.precision)
+    m.load_weights(*c.weights_dev())
+    x = c.dev()[0]
+    x2 = torch.flip(x[: w.T], dims=[0]).contiguous()
+    x2 = torch.cat([x2, x[w.T:]])
+    ids, probs = torch.from_numpy(c.ids).cuda(), torch.from_numpy(c.probs).cuda()
+    live = live_tensor(w.T)
+    refs = [_run(m, v, ids, probs, w.T, w.T_cap, w.H, m.new_workspace(w.T_cap), live=live) for v in (x, x2)]
+    wss = [m.new_workspace(w.T_cap) for _ in range(3)]
+    outs = [sentinel_out(w.T_cap, w.H) for _ in range(4)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    refs = [r.cpu().numpy().view(np.uint32) for r in refs]
+    same = lambda o, i: np.array_equal(o.cpu().numpy().view(np.uint32), refs[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward(x, ids, probs, live, out=outs[0], ws=wss[0])
+        m.forward(x2, ids, probs, live, out=outs[1], ws=wss[1], stream=other)      # not captured
+        m.forward(x2, ids, probs, live, out=outs[2], ws=wss[0])
+        m.forward(x, ids, probs, live, out=outs[3], ws=wss[1], stream=other)       # not captured
+    torch.cuda.synchronize()
+    assert same(outs[1], 1) and same(outs[3], 0)
+    for n in range(3):
+        for o in (outs[0], outs[2]):
+            o.fill_(float("nan"))
+        outs[0][w.T:] = outs[1][w.T:]
+        outs[2][w.T:] = outs[1][w.T:]
+        eager = outs[3].clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        m.forward(x2, ids, probs, live, out=eager, ws=wss[2], stream=other)        # beside the replay
+        torch.cuda.synchronize()
+        assert same(outs[0], 0) and same(outs[2], 1) and same(eager, 1), n
