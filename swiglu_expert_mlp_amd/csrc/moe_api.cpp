@@ -908,11 +908,12 @@ moe_status moe_check(moe_handle h, void* ws, hipStream_t stream, uint32_t* err_b
     if (e != hipSuccess) return hip_fail(e, "moe_check: clear");
     if (*err_bits) {
         const uint32_t b = *err_bits;
-        return fail(MOE_ERR_DEVICE_CONTRACT, "moe_check: contract violations 0x%x:%s%s%s%s%s%s", b,
+        return fail(MOE_ERR_DEVICE_CONTRACT, "moe_check: contract violations 0x%x:%s%s%s%s%s%s%s", b,
                     (b & kErrBadId) ? " expert id outside [0, E) (route dropped);" : "",
                     (b & kErrDupId) ? " expert id repeated within a token (repeat dropped);" : "",
                     (b & kErrLiveHigh) ? " live count above capacity (clamped);" : "",
                     (b & kErrLiveNeg) ? " negative live count (taken as 0);" : "",
+                    (b & kErrFusedWait) ? " single-launch wait ran out (outputs invalid);" : "",
                     (b & kErrNoRows) ? " probabilities' gradient without the forward's rows (not written);" : "",
                     (b & kErrWeightedRows) ? " probabilities' gradient of rows weighted inside FC1 (not written);" : "");
     }

@@ -277,3 +277,19 @@ def test_bits_of_earlier_calls_stay_beside_it():
     ids = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
     big.balance(zz, ids, live_tensor(T), ws=ws)
     assert big.check(ws) == 0
+
+
+def test_check_names_every_bit():
+    """moe_last_error has a text for each bit of the word."""
+    import swiglu_expert_mlp_amd as m
+    moe, ws = moe_of(4, 2), moe_of(4, 2).new_workspace(8)
+    bits = {getattr(m, n) for n in m.__all__ if n.startswith("DEVERR_")}
+    seen = set()
+    for b in sorted(bits):
+        ws[:4] = torch.tensor([b], dtype=torch.int32, device="cuda").view(torch.uint8)
+        assert moe.check(ws) == b and moe.check(ws) == 0
+        ws[:4] = torch.tensor([b], dtype=torch.int32, device="cuda").view(torch.uint8)
+        moe.check(ws)
+        text = m.lib().moe_last_error().decode().split(":", 2)[2].strip()
+        assert text and text not in seen, (b, text)
+        seen.add(text)
