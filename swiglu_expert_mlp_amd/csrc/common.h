@@ -37,10 +37,12 @@ __host__ __device__ inline int64_t wblock_step(int64_t n16, int64_t nt16)
     return nt16 - 32 * g < 32 ? nt16 - 32 * g : 32;
 }
 
-// Codes per row of an int8 operand with K elements: padded with zero codes to a
-// multiple of 128 (the 256-row tiles' stage), or of 64 (the 64-row tiles' step)
-// below 256, where the 256-row tiles are not used.  FFN 1856 becomes 1920, 3 %
-// more FC2 bytes, for the 256-row tiles on such a K.
+// Codes per row of an int8 operand with K elements (its pitch): padded with zero
+// codes to a multiple of 128, the 256-row tiles' stage, or of 64, the 64-row
+// tiles' step, for K below 256.  The 256-row tiles take a pitch that is a multiple
+// of 128 and at least 256, their two stages: every K from 224 on (224 codes are
+// padded to 256), no smaller one.  FFN 1856 becomes 1920, 3 % more FC2 bytes, for
+// the 256-row tiles on such a K.
 __host__ __device__ inline int int8_pitch(int K)
 {
     return K < 256 ? (K + 63) / 64 * 64 : (K + 127) / 128 * 128;

@@ -11,7 +11,7 @@
 // The tiles are the bf16 ones (gemm_bf16_big.h, gemm_bf16_small.h) with a pair
 // of codes in place of a bf16 element: the same 16 bytes a lane and cycles per
 // MFMA, half the bytes and MFMAs per row.  Rows are padded with zero codes to a
-// multiple of 128 (64 below 256; common.h), so that every K from 256 on takes
+// multiple of 128 (64 below 256; common.h), so that every K from 224 on takes
 // the 256-row design's 128-byte stages.
 //
 // What bounds it (one MI355X).  16,384 tokens, 128 experts, top-8, hidden 2048, FFN
