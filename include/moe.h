@@ -297,8 +297,9 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
  * looked up once per GPU (hipGetSymbolAddress) at the first call there.  The
  * call allocates nothing and enqueues the same kernels as moe_forward_ex.
  *   Arguments as moe_forward_ex, minus ws / ws_bytes.
- *   Limit: T_cap with moe_workspace_bytes(h, T_cap) <= 64 MiB (about 600
- *   tokens at hidden 2048, FFN 1024, top-6); a larger T_cap returns
+ *   Limit: T_cap with moe_workspace_bytes(h, T_cap) <= 64 MiB (at hidden
+ *   2048, FFN 1024, 64 experts, top-6 about 1,090 tokens in bf16 and 960 in
+ *   int8); a larger T_cap returns
  *   MOE_ERR_INVALID_ARG with nothing enqueued.
  *   Every call on one GPU shares that GPU's array, from any handle or stream:
  *   calls that overlap in time on one GPU race and must be ordered by the
@@ -314,8 +315,9 @@ moe_status moe_forward_noalloc(moe_handle h, const void* x, const int32_t* exper
 /* Workspace bytes of moe_balance for a token capacity T_cap (0 for a NULL
  * handle or a negative T_cap): caller-owned, no required initial contents, not
  * shared with a call that may overlap in time.  A moe_workspace_bytes workspace
- * of that size may serve, but a forward's rows, indices and error bits there
- * are lost by it (moe_probs_backward then flags MOE_DEVERR_NO_ROWS). */
+ * of that size may serve; a forward's rows, indices and error bits there are
+ * lost where the call writes to it (it does not for the few tokens that one
+ * workgroup takes), and moe_probs_backward then flags MOE_DEVERR_NO_ROWS. */
 size_t moe_balance_workspace_bytes(moe_handle h, int64_t T_cap);
 
 /* Balance loss, z loss and per-expert counts of the router (training).  Over

@@ -328,8 +328,9 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
         // int8: lane l holds the activation row of tile row l and its scale, and the scales
         // of its two columns.  They are fetched here, older than the ring's loads, so that
         // the epilogue waits for nothing and the rows' loads need no lookup of their own
-        // (against the rows' lookup alone here, scales in the epilogue: 64 tokens, hidden
-        // 128, 23.65 -> 23.36 us a forward; 256 tokens, hidden 2048, 86.4 / 86.7)
+        // (no faster than the rows' lookup alone here and the scales in the epilogue: 64
+        // tokens, hidden 128, 23.4 us a forward against 23.65; 256 tokens, hidden 2048,
+        // 86.7 against 86.4, both within what two runs differ by)
         int srow = row0 + min(lane, rows - 1);
         float rs = 1.0f, cs[2] = {1.0f, 1.0f};
         if constexpr (Op::kScaled) {

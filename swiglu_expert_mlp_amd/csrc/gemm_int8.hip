@@ -15,14 +15,15 @@
 // the 256-row design's 128-byte stages.
 //
 // What bounds it (one MI355X).  16,384 tokens, 128 experts, top-8, hidden 2048, FFN
-// 1024: FC1 600 us, FC2 430 us.  The MFMAs and epilogues alone take 430 / 260 us and
-// the loads alone 450 / 270 (FC2's 1.07 GB of fp32 rows another 130), but the shader
-// clock falls to 1.6-1.9 GHz in FC1 and 1.7-2.1 GHz in FC2 (2.4 nominal): the
-// launches run at the power limit, where neither a deeper weight ring (1.3 % of the
-// forward), nor operands resident in the L2 (6 %), nor fewer tiles of mostly empty
-// rows (none) gains much.  With the rows that pad each expert to whole tiles the rate
-// is 2.1 PetaOPS, a library's dense int8 product of 16384 x 8192 x 8192 2.2.  256
-// tokens, 64 experts: FC1 45 us, 5.9 TB/s of weights, FC2 27 us (4.9, a third of it the
+// 1024: FC1 605 us, FC2 430 us.  With the rows that pad each expert to whole tiles
+// (12 %) FC1 runs at 2.03 PetaOPS, a library's dense int8 product of 16384 x 8192 x
+// 8192 at 2.19; its MFMAs and epilogues alone take 430 us and its loads alone 450, but
+// the shader clock falls to 1.86 GHz (2.4 nominal): it is at the power limit, where
+// neither a deeper weight ring (1.3 % of the forward), nor operands resident in the
+// L2 (6 %), nor fewer tiles of mostly empty rows (none) gains much.  FC2 runs at 1.43
+// PetaOPS, its MFMAs busy for 36 % of the CUs' cycles (FC1 55 %), the clock at 2.05
+// GHz: what bounds it is its 1.07 GB of fp32 rows.  Without their stores it takes 307
+// us, without MFMAs still 395, with operands resident in the L2 no less.  256 tokens, 64 experts: FC1 45 us, 5.9 TB/s of weights, FC2 27 us (4.9, a third of it the
 // first loads' and last stores' latency): the HBM rate of contiguous 32 KB reads (6.1).
 #include <hip/hip_ext.h>
 

@@ -657,8 +657,14 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
         g1.topk = h->k;
         g1.n_tiles_n = ((2 * F / 64) + 3) / 4;
         g1.max_tiles = (int)L.max_tiles;
-        // the 256-row design as for bf16: capacities above 1024, whole stages of
-        // 128 codes, two at least, and offsets that fit its 32-bit descriptors
+        // the 256-row design as for bf16: whole stages of 128 codes, two at least,
+        // offsets that fit its 32-bit descriptors, and capacities above 1024.  The two
+        // designs cross between 1,024 and 2,048 tokens (a forward of hidden 2048, FFN
+        // 1024, 64-row tiles alone against both): 512 tokens x top-2 of 8 experts 65
+        // us / 100, 1,024 x 2 of 8 67 / 82, 1,024 x 6 of 64 145 / 166, 1,100 x 2 of 8
+        // 66 / 83, 1,500 x 4 of 32 131 / 125, 2,048 x 2 of 8 109 / 82, 2,048 x 6 of 64
+        // 237 / 202.  Around the boundary the rows and columns decide too: 1,024 x 4 of
+        // 8 106 / 81, 1,024 x 2 of 8 with hidden 4096, FFN 2048 181 / 138
         g1.small_takes_big = T_cap <= 1024 || Kp1 % 128 != 0 || Kp1 < 256 ||
                              T_cap * Kp1 >= ((int64_t)1 << 31) || (int64_t)2 * F * Kp1 >= ((int64_t)1 << 31);
         g1.row_prob = fc1_topk ? (const float*)(w + L.sorted_probs) : nullptr;
