@@ -141,23 +141,27 @@ def _on_current(stream, inputs):
         raise ValueError(f"stream must be of the current device cuda:{dev}, got {stream.device}")
     for t in inputs:
         d = getattr(t, "device", None)      # (_dev refuses what is no GPU tensor)
-        if isinstance(d, torch.device) and d.type == "cuda" and d.index != dev:
+        if d is not None and d.index != dev and isinstance(d, torch.device) and d.type == "cuda":
             raise ValueError(f"tensors must be on the current device cuda:{dev}, got {d}")
 
 
-def _empty(stream, shape, dtype, device, returned=True):
-    """A tensor that a call on `stream` makes itself.  With another stream than the current
-    one it comes from that stream's memory: a block freed on the current stream may have work
-    pending there, which `stream` does not wait for.  One that is `returned` for use on the
-    current stream is not reused before that stream is done with it."""
+def _fill(stream, device, *wanted):
+    """The tensors that a call on `stream` was given, and those that it makes itself for a
+    None: wanted holds (tensor or None, shape, dtype, returned).  With another stream than the
+    current one they come from that stream's memory: a block freed on the current stream may
+    have work pending there, which `stream` does not wait for.  One that is `returned` for use
+    on the current stream is not reused before that stream is done with it."""
     torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    make = lambda: [torch.empty(shape, dtype=dtype, device=device) if t is None else t
+                    for t, shape, dtype, _ in wanted]
+    if stream is None or all(w[0] is not None for w in wanted):
+        return make()
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned and t.is_cuda:
-        t.record_stream(torch.cuda.current_stream())
-    return t
+        got = make()
+    for t, (given, _, _, returned) in zip(got, wanted):
+        if given is None and returned and t.is_cuda:
+            t.record_stream(torch.cuda.current_stream())
+    return got
 
 
 class MoE:
@@ -175,7 +179,7 @@ class MoE:
         self._destroy = lib().moe_destroy
         self.E, self.H, self.F, self.topk, self.precision = E, H, F, topk, precision
         self.kbuf = None
-        self._bound_streams = {}
+        self._kbuf_streams, self._bound_streams = set(), {}
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -210,8 +214,7 @@ class MoE:
         bf = (torch.bfloat16, torch.int16, torch.uint16)
         p1 = _dev(w1, "w1", bf, (self.E, 2 * self.F, self.H))
         p2 = _dev(w2, "w2", bf, (self.E, self.H, self.F))
-        if kbuf is None:
-            kbuf = _empty(stream, self.weight_bytes, torch.uint8, w1.device)
+        kbuf, = _fill(stream, w1.device, (kbuf, self.weight_bytes, torch.uint8, True))
         pk = _dev(kbuf, "kbuf", (torch.uint8,))
         _check(lib().moe_load_weights(self._h, p1, p2, pk, kbuf.numel(), _stream(stream)),
                "moe_load_weights")
@@ -227,30 +230,33 @@ class MoE:
         q1 = _dev(w1_scale, "w1_scale", (torch.float32,), (self.E, 2 * self.F))
         p2 = _dev(w2, "w2", (torch.int8,), (self.E, self.H, self.F))
         q2 = _dev(w2_scale, "w2_scale", (torch.float32,), (self.E, self.H))
-        if kbuf is None:
-            kbuf = _empty(stream, self.weight_bytes, torch.uint8, w1.device)
+        kbuf, = _fill(stream, w1.device, (kbuf, self.weight_bytes, torch.uint8, True))
         pk = _dev(kbuf, "kbuf", (torch.uint8,))
         _check(lib().moe_load_quantized(self._h, p1, q1, p2, q2, pk, kbuf.numel(), _stream(stream)),
                "moe_load_quantized")
         return self._set_kbuf(kbuf)
 
-    def _kbuf_used_on(self, stream, bound=False):
-        """The weights' memory, once the handle drops it, is not reused before `stream` (the
-        current one if None) is done with it; bound: nor is that of later weights.  An
-        external stream may be gone by then: its owner orders the refit."""
+    def _reading_stream(self, stream, bound=False) -> int:
+        """The stream (the current one if None) of a call that reads the weights: their memory,
+        once the handle drops it, is not reused before that stream is done with it; bound: nor
+        is that of later weights.  An external stream may be gone by then: its owner orders
+        the refit."""
         torch = _torch()
-        if isinstance(stream, torch.cuda.ExternalStream):
-            return
         s = stream if stream is not None else torch.cuda.current_stream()
-        if bound:
-            self._bound_streams[s.cuda_stream] = s
-        if self.kbuf is not None:
-            self.kbuf.record_stream(s)
+        n = s.cuda_stream
+        if n not in self._kbuf_streams and not isinstance(stream, torch.cuda.ExternalStream):
+            if self.kbuf is not None:
+                self.kbuf.record_stream(s)
+                self._kbuf_streams.add(n)
+        if bound and not isinstance(stream, torch.cuda.ExternalStream):
+            self._bound_streams[n] = s
+        return n
 
     def _set_kbuf(self, kbuf):
         self.kbuf = kbuf          # keep the buffer alive as long as the handle reads it
         for s in self._bound_streams.values():
             kbuf.record_stream(s)
+        self._kbuf_streams = set(self._bound_streams)
         return kbuf
 
     def route(self, logits, live, ids=None, probs=None, ws=None, stream=None):
@@ -259,12 +265,9 @@ class MoE:
         T_cap = logits.shape[0]
         pl = _dev(logits, "logits", (torch.float32,), (T_cap, self.E))
         plive = _dev(live, "live", (torch.int32,))
-        if ids is None:
-            ids = _empty(stream, (T_cap, self.topk), torch.int32, logits.device)
-        if probs is None:
-            probs = _empty(stream, (T_cap, self.topk), torch.float32, logits.device)
-        if ws is None:
-            ws = _empty(stream, self.workspace_bytes(T_cap), torch.uint8, logits.device, returned=False)
+        n_ws = self.workspace_bytes(T_cap) if ws is None else 0
+        ids, probs, ws = _fill(stream, logits.device, (ids, (T_cap, self.topk), torch.int32, True),
+                               (probs, (T_cap, self.topk), torch.float32, True), (ws, n_ws, torch.uint8, False))
         pi = _dev(ids, "ids", (torch.int32,), (T_cap, self.topk))
         pp = _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         pw = _dev(ws, "ws", (torch.uint8,))
@@ -306,16 +309,13 @@ class MoE:
         pi = _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk))
         pp = None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         plive = _dev(live, "live", (torch.int32,))
-        if out is None:
-            out = _empty(stream, shape, alloc, x.device)
+        n_ws = self.workspace_bytes(T_cap) if ws is None else 0
+        out, ws = _fill(stream, x.device, (out, shape, alloc, True), (ws, n_ws, torch.uint8, False))
         po = _dev(out, "out", dts, shape)
-        if ws is None:
-            ws = _empty(stream, self.workspace_bytes(T_cap), torch.uint8, x.device, returned=False)
         pw = _dev(ws, "ws", (torch.uint8,))
-        self._kbuf_used_on(stream)
         _check(lib().moe_forward_ex(self._h, px, pi, pp, T_cap, plive,
                                     self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize), po, pw,
-                                    ws.numel(), _stream(stream)), "moe_forward")
+                                    ws.numel(), self._reading_stream(stream)), "moe_forward")
         return out
 
     def forward_noalloc(self, x, ids, probs, live, out=None, stream=None, combine="fp32",
@@ -331,13 +331,11 @@ class MoE:
         pi = _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk))
         pp = None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk))
         plive = _dev(live, "live", (torch.int32,))
-        if out is None:
-            out = _empty(stream, shape, alloc, x.device)
+        out, = _fill(stream, x.device, (out, shape, alloc, True))
         po = _dev(out, "out", dts, shape)
-        self._kbuf_used_on(stream)
         _check(lib().moe_forward_noalloc(self._h, px, pi, pp, T_cap, plive,
                                          self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize), po,
-                                         _stream(stream)), "moe_forward_noalloc")
+                                         self._reading_stream(stream)), "moe_forward_noalloc")
         return out
 
     # ------------------------------------------------------------- training the router
@@ -371,15 +369,10 @@ class MoE:
         mask: bool or uint8 [T_cap], tokens with 0 are left out."""
         torch = _torch()
         dev = logits.device
-        if losses is None:
-            losses = _empty(stream, 2, torch.float32, dev)
-        if counts is None:
-            counts = _empty(stream, self.E + 1, torch.int32, dev)
-        if prob_sums is None:
-            prob_sums = _empty(stream, self.E, torch.float32, dev)
-        if ws is None:
-            ws = _empty(stream, int(lib().moe_balance_workspace_bytes(self._h, logits.shape[0])), torch.uint8, dev,
-                        returned=False)
+        n_ws = int(lib().moe_balance_workspace_bytes(self._h, logits.shape[0])) if ws is None else 0
+        losses, counts, prob_sums, ws = _fill(
+            stream, dev, (losses, 2, torch.float32, True), (counts, self.E + 1, torch.int32, True),
+            (prob_sums, self.E, torch.float32, True), (ws, n_ws, torch.uint8, False))
         _check(lib().moe_balance(*self._balance_args(logits, ids, live, losses, counts, prob_sums, ws, mask,
                                                      stream)), "moe_balance")
         return losses, counts, prob_sums
@@ -402,8 +395,7 @@ class MoE:
         """Gradient of the logits (moe_route_backward), fp32 [T_cap, E]: of the probabilities
         (probs with d_probs), of balance's losses (counts with d_losses, fp32 [2]), or of both."""
         torch = _torch()
-        if d_logits is None:
-            d_logits = _empty(stream, logits.shape, torch.float32, logits.device)
+        d_logits, = _fill(stream, logits.device, (d_logits, logits.shape, torch.float32, True))
         _check(lib().moe_route_backward(*self._route_backward_args(logits, ids, live, d_logits, probs, d_probs,
                                                                    counts, d_losses, mask, stream)),
                "moe_route_backward")
@@ -423,8 +415,7 @@ class MoE:
         """Gradient of the probabilities of the last forward on ws (moe_probs_backward), fp32
         [T_cap, topk], from d_out [T_cap, H] (fp32 or bf16) and that forward's expert ids."""
         torch = _torch()
-        if d_probs is None:
-            d_probs = _empty(stream, (d_out.shape[0], self.topk), torch.float32, d_out.device)
+        d_probs, = _fill(stream, d_out.device, (d_probs, (d_out.shape[0], self.topk), torch.float32, True))
         _check(lib().moe_probs_backward(*self._probs_backward_args(d_out, ids, d_probs, ws, stream)),
                "moe_probs_backward")
         return d_probs
@@ -522,8 +513,7 @@ class MoE:
                 T_cap, _dev(live, "live", (torch.int32,)),
                 self._combine_code(combine, topk_in_fc1, fused_ffn, fused_finalize),
                 _dev(out, "out", dts, shape),
-                _dev(ws, "ws", (torch.uint8,)), ws.numel(), _stream(stream))
-        self._kbuf_used_on(stream, bound=True)
+                _dev(ws, "ws", (torch.uint8,)), ws.numel(), self._reading_stream(stream, bound=True))
         fn = lib().moe_forward_ex
         keep = (self, x, ids, probs, live, out, ws)
 
