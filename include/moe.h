@@ -364,7 +364,7 @@ moe_status moe_balance(moe_handle h, const float* logits, const int32_t* expert_
  *   tokens are written whole, rows >= live not at all.  Every row's bits are
  *   independent of the other rows, given the counts.
  * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer, half a pair, neither
- * pair, T_cap outside [0, 2^26]), MOE_ERR_HIP. */
+ * pair, d_logits in an input's memory, T_cap outside [0, 2^26]), MOE_ERR_HIP. */
 moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* expert_ids,
                               const float* probs, const float* d_probs, int64_t T_cap,
                               const int32_t* live_rows_dev, const uint8_t* token_mask,

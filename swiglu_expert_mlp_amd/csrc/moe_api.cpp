@@ -111,6 +111,11 @@ static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+static bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
 static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
 {
     WsLayout L;
@@ -432,12 +437,17 @@ moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* 
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_losses needs counts, and counts d_losses");
     if (!d_probs && !d_losses)
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: neither d_probs nor d_losses");
-    if (logits == d_logits)
-        return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_logits must not be the logits");
     for (const void* p : {(const void*)logits, (const void*)expert_ids, (const void*)probs, (const void*)d_probs,
                           (const void*)token_mask, (const void*)counts, (const void*)d_losses, (const void*)d_logits})
         if (!aligned16(p))
             return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: pointers must be 16-byte aligned");
+    const size_t rows = 4 * (size_t)T_cap * h->E, routes = 4 * (size_t)T_cap * h->k;
+    const struct { const void* p; size_t n; } in[] = {
+        {logits, rows}, {expert_ids, routes}, {probs, routes}, {d_probs, routes}, {live_rows_dev, 4},
+        {token_mask, (size_t)T_cap}, {counts, 4 * (size_t)(h->E + 1)}, {d_losses, 8}};
+    for (const auto& i : in)
+        if (i.p && overlap(d_logits, rows, i.p, i.n))
+            return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_logits must not be in an input's memory");
     moe_status st = ensure_device(h);
     if (st != MOE_OK) return st;
     if (T_cap == 0) return MOE_OK;

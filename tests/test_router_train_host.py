@@ -156,3 +156,22 @@ def test_every_call_refuses_tensors_of_another_device(call, monkeypatch):
          "bind_route": 5}[call]
     with pytest.raises(ValueError, match="current device"):
         getattr(moe, call)(*[Fake()] * n)
+
+
+@pytest.mark.parametrize("name,size", [("logits", 64 * 8 * 4), ("ids", 64 * 2 * 4), ("probs", 64 * 2 * 4),
+                                       ("d_probs", 64 * 2 * 4), ("live", 4), ("mask", 64), ("counts", 9 * 4),
+                                       ("d_losses", 8)])
+def test_route_backward_refuses_outputs_inside_an_input(L, handle, name, size):
+    """Partly over an input's last bytes, and an input inside the output's rows."""
+    rows, out = 64 * 8 * 4, 1 << 26
+
+    def call(p):
+        where = dict(logits=1 << 20, ids=2 << 20, probs=3 << 20, d_probs=4 << 20, live=5 << 20, mask=6 << 20,
+                      counts=7 << 20, d_losses=8 << 20)
+        where[name] = p
+        a = {n: P(v) for n, v in where.items()}
+        return L.moe_route_backward(handle, a["logits"], a["ids"], a["probs"], a["d_probs"], 64, a["live"], a["mask"],
+                                    a["counts"], a["d_losses"], P(out), None)
+
+    for p in (out - (size - 1) // 16 * 16, out, out + rows - 16):
+        assert call(p) == -1 and b"must not be" in L.moe_last_error(), p
