@@ -502,7 +502,7 @@ class MoE:
                      topk_in_fc1=False, fused_ffn=False, fused_finalize=False):
         """Check the arguments once and return a no-argument callable that
         enqueues this forward (for launch loops where per-call checks would
-        cost more host time than the GPU work)."""
+        cost more host time than the GPU work), on the device current here."""
         torch = _torch()
         _on_current(stream, (x, ids, probs, live, out, ws))
         T_cap = x.shape[0]
