@@ -393,6 +393,121 @@ moe_status moe_probs_backward(moe_handle h, const void* d_out, int combine,
                               const int32_t* expert_ids, int64_t T_cap, float* d_probs, void* ws,
                               size_t ws_bytes, hipStream_t stream);
 
+/* Element types of the rows and gradients below. */
+typedef enum { MOE_TYPE_FP32 = 0, MOE_TYPE_BF16 = 1 } moe_type;
+
+/* The forward of a training step (bf16 handles): moe_forward_ex with one of its
+ * three combines and no option, bit for bit, that also keeps the gate and up
+ * values of every grouped row (the inputs of the SwiGLU) in 8 bits for
+ * moe_backward.
+ *   codes: int8 [T_cap * topk][2F]; scales: uint8 [T_cap * topk][F / 16].  Row r
+ *   is grouped row r (experts ascending, tokens ascending within an expert);
+ *   its columns are in blocks of 32, gate and up by turns (column 64 b + i is
+ *   gate 32 b + i for i < 32, else up 32 b + i - 32).  The block of columns
+ *   32 c .. 32 c + 31 has the scale 2^(scales[r][c] - 127), the smallest power of
+ *   two, at least 2^-126, whose 127-fold reaches the block's largest magnitude;
+ *   a code is the value over its scale rounded to the nearest integer (ties to
+ *   even), so a value is kept within half a scale.  A block with an infinity or
+ *   a NaN has byte 255 and codes of 0, and its values read back as NaN.
+ *   Rows past the last grouped row are not written.
+ * Errors: as moe_forward_ex; MOE_ERR_INVALID_ARG for a handle of another
+ * precision, a combine with options, codes or scales NULL, misaligned or in the
+ * memory of another argument. */
+moe_status moe_forward_checkpoint(moe_handle h, const void* x, const int32_t* expert_ids,
+                                  const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
+                                  int combine, void* out, int8_t* codes, uint8_t* scales, void* ws,
+                                  size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of moe_backward for a token capacity T_cap (0 for a NULL handle
+ * or a negative T_cap): caller-owned, no required initial contents. */
+size_t moe_backward_workspace_bytes(moe_handle h, int64_t T_cap);
+
+/* Backward pass of the experts (training, bf16 handles): the gradients of x, of
+ * both weights and of the probabilities, from the gradient of the output of a
+ * forward whose combine was MOE_COMBINE_FP32 or MOE_COMBINE_BF16.
+ * With g, u the kept gate and up of route (t, j) on expert e, p its probability,
+ * s = 1 / (1 + exp(-g)) and h = g s u:
+ *   raw      = W2_e^T d_out[t]                     (fp32)
+ *   d_gate   = p raw u s (1 + g (1 - s)),  d_up = p raw g s      (rounded to bf16)
+ *   d_x[t]   = sum over j of W1_e^T [d_gate; d_up]  (each route's rounded to bf16,
+ *              the sum over ascending experts fp32)
+ *   d_w1[e]  = sum over rows of [d_gate; d_up] x[t]^T
+ *   d_w2[e]  = sum over rows of d_out[t] (p h)^T    (p h rounded to bf16)
+ *   d_probs[t][j] = sum over the FFN of raw h       (fp32)
+ * A route whose id is outside [0, E) or repeats an earlier one of its token has
+ * no row: it adds nothing and its d_probs is 0.
+ *   d_out: [T_cap][H] of d_out_type (fp32 is rounded to bf16 first, for d_probs
+ *   too); x, expert_ids, probs, live_rows_dev: as given to that forward; codes,
+ *   scales: what moe_forward_checkpoint kept, or any in its layout.  The weights
+ *   are those of the last moe_load_weights.
+ *   d_x: bf16 [T_cap][H]; d_w1: [E][2F][H] (gate rows first) and d_w2: [E][H][F]
+ *   of d_w_type, written whole (zeros for an expert without rows); d_probs: fp32
+ *   [T_cap][topk], in the order of expert_ids.  Rows of d_x and d_probs past the
+ *   live count are not written.  ws_bytes >= moe_backward_workspace_bytes(h, T_cap).
+ * The forward's workspace is not used, so it may serve other layers in between.
+ * Every sum has a fixed order: repeated calls give the same bits.  moe_check on
+ * ws reports the ids and the live count as a forward's.
+ * Errors: MOE_ERR_INVALID_ARG (another precision or type, NULL or misaligned
+ * pointer, an output or the workspace in the memory of another argument, T_cap
+ * outside [0, 2^26], ws_bytes too small), MOE_ERR_NOT_LOADED, MOE_ERR_HIP. */
+moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const void* x,
+                        const int32_t* expert_ids, const float* probs, int64_t T_cap,
+                        const int32_t* live_rows_dev, const int8_t* codes, const uint8_t* scales,
+                        void* d_x, void* d_w1, void* d_w2, int d_w_type, float* d_probs, void* ws,
+                        size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of moe_dispatch for a token capacity T_cap (0 for a NULL handle
+ * or a negative T_cap): caller-owned, no required initial contents. */
+size_t moe_dispatch_workspace_bytes(moe_handle h, int64_t T_cap);
+
+/* Tokens sorted by expert, for experts of the caller's own (any handle; no weights
+ * are needed): the forward's permutation and a copy of each token to its rows.
+ *   x: [T_cap][H] of `type`; expert_ids: int32 [T_cap][topk].
+ *   rows: [T_cap * topk][H] of `type`, rows grouped by expert ascending, tokens
+ *   ascending within an expert; row_of: int32 [T_cap][topk], the row of each
+ *   route in the order of expert_ids, -1 for a route without one (an id outside
+ *   [0, E), or one that its token lists before); offsets: int32 [E + 1], expert
+ *   e's rows are offsets[e] .. offsets[e + 1] - 1.  Rows past offsets[E], and
+ *   row_of of tokens past the live count, are not written.
+ * ws_bytes >= moe_dispatch_workspace_bytes(h, T_cap); moe_check on ws reports the
+ * ids and the live count as a forward's.  The gradient of x is moe_combine_rows
+ * of the rows' gradients without probabilities.
+ * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer, unknown type, an output
+ * or the workspace in the memory of another argument, T_cap outside [0, 2^26],
+ * ws_bytes too small), MOE_ERR_HIP. */
+moe_status moe_dispatch(moe_handle h, const void* x, int type, const int32_t* expert_ids,
+                        int64_t T_cap, const int32_t* live_rows_dev, void* rows, int32_t* row_of,
+                        int32_t* offsets, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Rows summed back into tokens, with the probabilities applied:
+ *   out[t] = sum over j of probs[t][j] rows[row_of[t][j]],
+ * an fp32 chain of fused multiply-adds from +0 in ascending row (so expert) order,
+ * rounded once.  probs may be NULL (every probability 1): then it is the gradient
+ * of moe_dispatch's x.  A row_of outside [0, T_cap * topk) adds nothing.
+ *   rows: [T_cap * topk][H] of `type`; row_of: int32 [T_cap][topk]; probs: fp32
+ *   [T_cap][topk] or NULL; out: [T_cap][H] of out_type; rows of out past the live
+ *   count are not written.
+ * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer, unknown type, out in the
+ * memory of an input, T_cap outside [0, 2^26]), MOE_ERR_HIP. */
+moe_status moe_combine_rows(moe_handle h, const void* rows, int type, const int32_t* row_of,
+                            const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
+                            void* out, int out_type, hipStream_t stream);
+
+/* Gradients of moe_combine_rows:
+ *   d_rows[row_of[t][j]] = probs[t][j] d_out[t],
+ *   d_probs[t][j] = sum over m of d_out[t][m] rows[row_of[t][j]][m]   (fp32),
+ * 0 for a route without a row.  rows and d_probs may both be NULL (d_rows alone).
+ *   d_out: [T_cap][H] of out_type; rows and d_rows: [T_cap * topk][H] of `type`;
+ *   row_of: as moe_dispatch writes it (no row twice).  Rows of d_rows that no live
+ *   route has, and d_probs past the live count, are not written.
+ * Errors: MOE_ERR_INVALID_ARG (NULL or misaligned pointer, rows or d_probs alone,
+ * unknown type, an output in the memory of another argument, T_cap outside
+ * [0, 2^26]), MOE_ERR_HIP. */
+moe_status moe_combine_backward(moe_handle h, const void* d_out, int out_type, const void* rows,
+                                int type, const int32_t* row_of, const float* probs, int64_t T_cap,
+                                const int32_t* live_rows_dev, void* d_rows, float* d_probs,
+                                hipStream_t stream);
+
 /* Copy the permutation of the last forward to host arrays (synchronizes the
  * stream).  The grouping is cudnn-frontend PR #448's route index (MoeEp class
  * docstring): rows grouped by local expert in ascending order, token-major

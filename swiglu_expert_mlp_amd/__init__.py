@@ -66,6 +66,16 @@ _SIGNATURES = {
     "moe_route_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int64] + [_P] * 6),
     "moe_probs_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int64, _P, _P,
                                           ctypes.c_size_t, _P]),
+    "moe_forward_checkpoint": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, _P, ctypes.c_int, _P, _P, _P, _P,
+                                              ctypes.c_size_t, _P]),
+    "moe_backward_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int64]),
+    "moe_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_int64] + [_P] * 6 +
+                     [ctypes.c_int, _P, _P, ctypes.c_size_t, _P]),
+    "moe_dispatch_workspace_bytes": (ctypes.c_size_t, [_P, ctypes.c_int64]),
+    "moe_dispatch": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int64] + [_P] * 5 + [ctypes.c_size_t, _P]),
+    "moe_combine_rows": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, ctypes.c_int64, _P, _P, ctypes.c_int, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, _P, _P, ctypes.c_int64,
+                                            _P, _P, _P, _P]),
     "moe_get_indices": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P]),
     "moe_get_rows": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P]),
     "moe_check": (ctypes.c_int, [_P, _P, _P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -110,6 +120,20 @@ def _check(status: int, what: str):
 def _torch():
     import torch
     return torch
+
+
+class _Types(dict):
+    """moe_type by torch dtype (filled at the first use: torch is imported late)"""
+
+    def __missing__(self, dtype):
+        torch = _torch()
+        self.update({torch.float32: 0, torch.bfloat16: 1})
+        if dtype not in self:
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        return self[dtype]
+
+
+_TYPES = _Types()
 
 
 def _stream(stream=None) -> int:
@@ -420,6 +444,191 @@ class MoE:
                "moe_probs_backward")
         return d_probs
 
+    # ------------------------------------------------------------- training the experts
+
+    def new_checkpoint(self, T_cap: int, device=None):
+        """Buffers for the gate and up values that forward_checkpoint keeps in 8 bits: codes
+        int8 [T_cap * topk, 2F] and scales uint8 [T_cap * topk, F // 16]."""
+        torch = _torch()
+        R, device = int(T_cap) * self.topk, device or "cuda"
+        return (torch.empty((R, 2 * self.F), dtype=torch.int8, device=device),
+                torch.empty((R, self.F // 16), dtype=torch.uint8, device=device))
+
+    def _checkpoint(self, codes, scales, T_cap: int):
+        torch = _torch()
+        R = T_cap * self.topk
+        return (_dev(codes, "codes", (torch.int8,), (R, 2 * self.F)),
+                _dev(scales, "scales", (torch.uint8,), (R, self.F // 16)))
+
+    def _forward_checkpoint_args(self, x, ids, probs, live, out, codes, scales, ws, combine, stream, bound=False):
+        torch = _torch()
+        _on_current(stream, (x, ids, probs, live, out, codes, scales, ws))
+        T_cap = x.shape[0]
+        dts, shape, _ = self._out_spec(T_cap, combine)
+        pc, ps = self._checkpoint(codes, scales, T_cap)
+        return (self._h, _dev(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (T_cap, self.H)),
+                _dev(ids, "expert_ids", (torch.int32,), (T_cap, self.topk)),
+                None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk)), T_cap,
+                _dev(live, "live", (torch.int32,)), COMBINES[combine], _dev(out, "out", dts, shape), pc, ps,
+                _dev(ws, "ws", (torch.uint8,)), ws.numel(), self._reading_stream(stream, bound=bound))
+
+    def forward_checkpoint(self, x, ids, probs, live, out=None, codes=None, scales=None, ws=None, stream=None,
+                           combine="fp32"):
+        """forward (bf16 handles, no options) that also keeps every row's gate and up values in
+        8 bits (moe_forward_checkpoint).  Gives out, codes and scales; the last two are what
+        backward takes, and all that it needs of this forward."""
+        torch = _torch()
+        T_cap, R = x.shape[0], x.shape[0] * self.topk
+        _, shape, alloc = self._out_spec(T_cap, combine)
+        n_ws = self.workspace_bytes(T_cap) if ws is None else 0
+        out, codes, scales, ws = _fill(stream, x.device, (out, shape, alloc, True),
+                                       (codes, (R, 2 * self.F), torch.int8, True),
+                                       (scales, (R, self.F // 16), torch.uint8, True), (ws, n_ws, torch.uint8, False))
+        _check(lib().moe_forward_checkpoint(*self._forward_checkpoint_args(x, ids, probs, live, out, codes, scales, ws,
+                                                                           combine, stream)), "moe_forward_checkpoint")
+        return out, codes, scales
+
+    def new_backward_workspace(self, T_cap: int, device=None):
+        """A workspace of backward for capacity T_cap (no initial contents are required)."""
+        torch = _torch()
+        return torch.empty(int(lib().moe_backward_workspace_bytes(self._h, int(T_cap))), dtype=torch.uint8,
+                           device=device or "cuda")
+
+    def _backward_args(self, d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2, d_probs, ws, stream,
+                       bound=False):
+        torch = _torch()
+        _on_current(stream, (d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2, d_probs, ws))
+        T_cap, E, H, F, k = x.shape[0], self.E, self.H, self.F, self.topk
+        bf = (torch.bfloat16, torch.int16, torch.uint16)
+        grads = (torch.float32, torch.bfloat16)
+        p = _dev(d_out, "d_out", grads, (T_cap, H))
+        pw1 = _dev(d_w1, "d_w1", grads, (E, 2 * F, H))
+        pw2 = _dev(d_w2, "d_w2", (d_w1.dtype,), (E, H, F))
+        pc, ps = self._checkpoint(codes, scales, T_cap)
+        return (self._h, p, _TYPES[d_out.dtype], _dev(x, "x", bf, (T_cap, H)),
+                _dev(ids, "expert_ids", (torch.int32,), (T_cap, k)), _dev(probs, "probs", (torch.float32,), (T_cap, k)),
+                T_cap, _dev(live, "live", (torch.int32,)), pc, ps, _dev(d_x, "d_x", bf, (T_cap, H)), pw1, pw2,
+                _TYPES[d_w1.dtype], _dev(d_probs, "d_probs", (torch.float32,), (T_cap, k)),
+                _dev(ws, "ws", (torch.uint8,)), ws.numel(), self._reading_stream(stream, bound=bound))
+
+    def backward(self, d_out, x, ids, probs, live, codes, scales, d_x=None, d_w1=None, d_w2=None, d_probs=None,
+                 ws=None, stream=None, grad_dtype="bf16"):
+        """Gradients of the experts (moe_backward): d_x bf16 [T_cap, H], d_w1 [E, 2F, H] (gate rows
+        first) and d_w2 [E, H, F] (bf16, or fp32 with grad_dtype="fp32" or tensors of that
+        type), d_probs fp32 [T_cap, topk].  d_out [T_cap, H] fp32 or bf16; the other inputs as
+        given to, and kept by, forward_checkpoint."""
+        torch = _torch()
+        if grad_dtype not in ("bf16", "fp32"):
+            raise ValueError("grad_dtype must be bf16 or fp32")
+        T_cap, E, H, F, k = x.shape[0], self.E, self.H, self.F, self.topk
+        w = torch.bfloat16 if grad_dtype == "bf16" else torch.float32
+        w = next((t.dtype for t in (d_w1, d_w2) if t is not None), w)
+        n_ws = int(lib().moe_backward_workspace_bytes(self._h, T_cap)) if ws is None else 0
+        d_x, d_w1, d_w2, d_probs, ws = _fill(
+            stream, x.device, (d_x, (T_cap, H), torch.bfloat16, True), (d_w1, (E, 2 * F, H), w, True),
+            (d_w2, (E, H, F), w, True), (d_probs, (T_cap, k), torch.float32, True), (ws, n_ws, torch.uint8, False))
+        _check(lib().moe_backward(*self._backward_args(d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2,
+                                                       d_probs, ws, stream)), "moe_backward")
+        return d_x, d_w1, d_w2, d_probs
+
+    # ------------------------------------------------------------- tokens by expert and back
+
+    def new_dispatch_workspace(self, T_cap: int, device=None):
+        """A workspace of dispatch for capacity T_cap (no initial contents are required)."""
+        torch = _torch()
+        return torch.empty(int(lib().moe_dispatch_workspace_bytes(self._h, int(T_cap))), dtype=torch.uint8,
+                           device=device or "cuda")
+
+    def _rows(self, t, name, T_cap: int):
+        torch = _torch()
+        return _dev(t, name, (torch.float32, torch.bfloat16), (T_cap * self.topk, self.H))
+
+    def _tokens(self, t, name, T_cap: int):
+        torch = _torch()
+        return _dev(t, name, (torch.float32, torch.bfloat16), (T_cap, self.H))
+
+    def _dispatch_args(self, x, ids, live, rows, row_of, offsets, ws, stream):
+        torch = _torch()
+        _on_current(stream, (x, ids, live, rows, row_of, offsets, ws))
+        T_cap, i32 = x.shape[0], (torch.int32,)
+        px, pr = self._tokens(x, "x", T_cap), self._rows(rows, "rows", T_cap)
+        if rows.dtype != x.dtype:
+            raise TypeError(f"rows must have x's dtype {x.dtype}, got {rows.dtype}")
+        return (self._h, px, _TYPES[x.dtype], _dev(ids, "expert_ids", i32, (T_cap, self.topk)), T_cap,
+                _dev(live, "live", i32), pr, _dev(row_of, "row_of", i32, (T_cap, self.topk)),
+                _dev(offsets, "offsets", i32, (self.E + 1,)), _dev(ws, "ws", (torch.uint8,)), ws.numel(),
+                _stream(stream))
+
+    def dispatch(self, x, ids, live, rows=None, row_of=None, offsets=None, ws=None, stream=None):
+        """Tokens sorted by expert (moe_dispatch): rows [T_cap * topk, H] of x's dtype (fp32 or
+        bf16), row_of int32 [T_cap, topk] (-1 for a route without a row) and offsets int32
+        [E + 1]."""
+        torch = _torch()
+        T_cap = x.shape[0]
+        n_ws = int(lib().moe_dispatch_workspace_bytes(self._h, T_cap)) if ws is None else 0
+        rows, row_of, offsets, ws = _fill(
+            stream, x.device, (rows, (T_cap * self.topk, self.H), x.dtype, True),
+            (row_of, (T_cap, self.topk), torch.int32, True), (offsets, self.E + 1, torch.int32, True),
+            (ws, n_ws, torch.uint8, False))
+        _check(lib().moe_dispatch(*self._dispatch_args(x, ids, live, rows, row_of, offsets, ws, stream)), "moe_dispatch")
+        return rows, row_of, offsets
+
+    def _combine_args(self, rows, row_of, probs, live, out, stream):
+        torch = _torch()
+        _on_current(stream, (rows, row_of, probs, live, out))
+        T_cap = row_of.shape[0]
+        pr, po = self._rows(rows, "rows", T_cap), self._tokens(out, "out", T_cap)
+        return (self._h, pr, _TYPES[rows.dtype], _dev(row_of, "row_of", (torch.int32,), (T_cap, self.topk)),
+                None if probs is None else _dev(probs, "probs", (torch.float32,), (T_cap, self.topk)), T_cap,
+                _dev(live, "live", (torch.int32,)), po, _TYPES[out.dtype], _stream(stream))
+
+    def combine(self, rows, row_of, probs, live, out=None, stream=None, combine="fp32"):
+        """Rows summed back into tokens with their probabilities (moe_combine_rows), rows fp32 or
+        bf16; combine: "fp32" or "bf16", the dtype of out [T_cap, H]."""
+        torch = _torch()
+        if combine not in ("fp32", "bf16"):
+            raise ValueError("combine must be fp32 or bf16")
+        if probs is None:
+            raise ValueError("probs is None (dispatch_backward sums rows without probabilities)")
+        dt = torch.float32 if combine == "fp32" else torch.bfloat16
+        out, = _fill(stream, rows.device, (out, (row_of.shape[0], self.H), dt, True))
+        _check(lib().moe_combine_rows(*self._combine_args(rows, row_of, probs, live, out, stream)), "moe_combine_rows")
+        return out
+
+    def dispatch_backward(self, d_rows, row_of, live, d_x=None, stream=None):
+        """Gradient of dispatch's x [T_cap, H] (moe_combine_rows without probabilities), of
+        d_rows' dtype unless d_x is given."""
+        d_x, = _fill(stream, d_rows.device, (d_x, (row_of.shape[0], self.H), d_rows.dtype, True))
+        _check(lib().moe_combine_rows(*self._combine_args(d_rows, row_of, None, live, d_x, stream)), "moe_combine_rows")
+        return d_x
+
+    def _combine_backward_args(self, d_out, rows, row_of, probs, live, d_rows, d_probs, stream):
+        torch = _torch()
+        _on_current(stream, (d_out, rows, row_of, probs, live, d_rows, d_probs))
+        T_cap = d_out.shape[0]
+        p, pd = self._tokens(d_out, "d_out", T_cap), self._rows(d_rows, "d_rows", T_cap)
+        pr = None if rows is None else self._rows(rows, "rows", T_cap)
+        if rows is not None and rows.dtype != d_rows.dtype:
+            raise TypeError(f"d_rows must have the rows' dtype {rows.dtype}, got {d_rows.dtype}")
+        f32 = (torch.float32,)
+        return (self._h, p, _TYPES[d_out.dtype], pr, _TYPES[d_rows.dtype],
+                _dev(row_of, "row_of", (torch.int32,), (T_cap, self.topk)), _dev(probs, "probs", f32, (T_cap, self.topk)),
+                T_cap, _dev(live, "live", (torch.int32,)), pd,
+                None if d_probs is None else _dev(d_probs, "d_probs", f32, (T_cap, self.topk)), _stream(stream))
+
+    def combine_backward(self, d_out, rows, row_of, probs, live, d_rows=None, d_probs=None, stream=None):
+        """Gradients of combine (moe_combine_backward): d_rows [T_cap * topk, H] of the rows' dtype
+        and d_probs fp32 [T_cap, topk].  rows=None: d_rows alone (of d_out's dtype unless given)."""
+        torch = _torch()
+        T_cap = d_out.shape[0]
+        dt = d_out.dtype if rows is None else rows.dtype
+        d_rows, = _fill(stream, d_out.device, (d_rows, (T_cap * self.topk, self.H), dt, True))
+        if rows is not None:
+            d_probs, = _fill(stream, d_out.device, (d_probs, (T_cap, self.topk), torch.float32, True))
+        _check(lib().moe_combine_backward(*self._combine_backward_args(d_out, rows, row_of, probs, live, d_rows, d_probs,
+                                                                       stream)), "moe_combine_backward")
+        return d_rows, d_probs
+
     # ------------------------------------------------------------- inspection
 
     def get_indices(self, ws, T_cap: int, stream=None) -> dict:
@@ -564,6 +773,42 @@ class MoE:
         """As bind_forward, for probs_backward."""
         args = self._probs_backward_args(d_out, ids, d_probs, ws, stream)
         return self._bound(lib().moe_probs_backward, "moe_probs_backward", args, (self, d_out, ids, d_probs, ws))
+
+    def bind_forward_checkpoint(self, x, ids, probs, live, out, codes, scales, ws, stream=None, combine="fp32"):
+        """As bind_forward, for forward_checkpoint."""
+        args = self._forward_checkpoint_args(x, ids, probs, live, out, codes, scales, ws, combine, stream, bound=True)
+        return self._bound(lib().moe_forward_checkpoint, "moe_forward_checkpoint", args,
+                           (self, x, ids, probs, live, out, codes, scales, ws))
+
+    def bind_backward(self, d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2, d_probs, ws, stream=None):
+        """As bind_forward, for backward."""
+        args = self._backward_args(d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2, d_probs, ws, stream,
+                                   bound=True)
+        return self._bound(lib().moe_backward, "moe_backward", args,
+                           (self, d_out, x, ids, probs, live, codes, scales, d_x, d_w1, d_w2, d_probs, ws))
+
+    def bind_dispatch(self, x, ids, live, rows, row_of, offsets, ws, stream=None):
+        """As bind_forward, for dispatch."""
+        args = self._dispatch_args(x, ids, live, rows, row_of, offsets, ws, stream)
+        return self._bound(lib().moe_dispatch, "moe_dispatch", args, (self, x, ids, live, rows, row_of, offsets, ws))
+
+    def bind_combine(self, rows, row_of, probs, live, out, stream=None):
+        """As bind_forward, for combine."""
+        if probs is None:
+            raise ValueError("probs is None (bind_dispatch_backward sums rows without probabilities)")
+        args = self._combine_args(rows, row_of, probs, live, out, stream)
+        return self._bound(lib().moe_combine_rows, "moe_combine_rows", args, (self, rows, row_of, probs, live, out))
+
+    def bind_dispatch_backward(self, d_rows, row_of, live, d_x, stream=None):
+        """As bind_forward, for dispatch_backward."""
+        args = self._combine_args(d_rows, row_of, None, live, d_x, stream)
+        return self._bound(lib().moe_combine_rows, "moe_combine_rows", args, (self, d_rows, row_of, live, d_x))
+
+    def bind_combine_backward(self, d_out, rows, row_of, probs, live, d_rows, d_probs, stream=None):
+        """As bind_forward, for combine_backward."""
+        args = self._combine_backward_args(d_out, rows, row_of, probs, live, d_rows, d_probs, stream)
+        return self._bound(lib().moe_combine_backward, "moe_combine_backward", args,
+                           (self, d_out, rows, row_of, probs, live, d_rows, d_probs))
 
     def check(self, ws, stream=None) -> int:
         """moe_check: the contract-violation bits (DEVERR_*) of the last route and

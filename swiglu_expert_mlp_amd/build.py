@@ -22,7 +22,7 @@ ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["moe_api.cpp", "route.hip", "prep.hip", "gemm_bf16.hip", "gemm_mxfp8.hip",
            "gemm_int8.hip", "quant_int8.hip", "route_train.hip",
-           "finalize.hip", "pack.hip"]
+           "finalize.hip", "pack.hip", "grad_gemm.hip", "rows.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include")]

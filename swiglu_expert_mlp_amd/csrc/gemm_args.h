@@ -95,6 +95,10 @@ struct GemmArgs {
     // the grouped row) and of each weight row [E][N] (FC1: in packed row order)
     const float* a_scale;
     const float* w_scale;
+    // FC1 of a forward that keeps its gate and up values (checkpoint.h), else null: codes
+    // [rows][2F] and scale bytes [rows][F / 16]
+    int8_t* ck_codes;
+    uint8_t* ck_scales;
 };
 
 // MXFP8 operands: E4M3 codes with one E8M0 scale byte per 32 elements of K.

@@ -19,7 +19,8 @@ namespace moe {
 
 // PROB: FC1 with the routes' probabilities applied to the SwiGLU rows (a
 // compile-time variant; the default epilogues carry no probability loads)
-template <bool FC1, bool PROB>
+// CKPT: FC1 that also keeps its gate and up values in 8 bits
+template <bool FC1, bool PROB, bool CKPT = false>
 __global__ void __launch_bounds__(512, 1) gemm_bf16_small_kernel(GemmArgs g)
 {
     __shared__ __attribute__((aligned(1024))) char smem[kSmallLds];
@@ -32,14 +33,14 @@ __global__ void __launch_bounds__(512, 1) gemm_bf16_small_kernel(GemmArgs g)
     const int* te0 = (const int*)(g.tiles + min(xcd_first_tile() / small_col_tiles(g), g.max_tiles - 1));
     const int e0 = ld_const(te0), row00 = ld_const(te0 + 1);
     asm volatile("" : : "s"(n_big), "s"(n_small), "s"(multi), "s"(e0), "s"(row00));   // one round trip
-    if (multi) small_tiles<OpBf16, FC1, PROB, 0, 0>(g, smem, n_small, n_big, e0, row00);
-    else small_tiles<OpBf16, FC1, PROB, 0, kNonTemporal>(g, smem, n_small, n_big, e0, row00);
+    if (multi) small_tiles<OpBf16, FC1, PROB, 0, 0, CKPT>(g, smem, n_small, n_big, e0, row00);
+    else small_tiles<OpBf16, FC1, PROB, 0, kNonTemporal, CKPT>(g, smem, n_small, n_big, e0, row00);
 }
 
-template <bool FC1, bool PROB>
+template <bool FC1, bool PROB, bool CKPT = false>
 __global__ void __launch_bounds__(512, 1) gemm_bf16_big_kernel(GemmArgs g)
 {
-    big_tiles<OpBf16, FC1, PROB>(g, ld_const(&g.hdr->n_tiles_big));
+    big_tiles<OpBf16, FC1, PROB, FC1 ? 0 : kNonTemporal, 0, CKPT>(g, ld_const(&g.hdr->n_tiles_big));
 }
 
 // The single-launch FFN: FC1 then FC2 in one persistent launch of the 64-row
@@ -115,16 +116,20 @@ hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t
             hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, g);
     };
     const bool prob = fc1 && g.row_prob != nullptr;
+    const bool ckpt = fc1 && g.ck_codes != nullptr;
+    if (ckpt && (prob || !g.ck_scales)) return hipErrorInvalidValue;
     hipEvent_t small_start = t0;
     hipStream_t ss = s;
     if (!g.small_takes_big) {
-        if (prob) go(gemm_bf16_big_kernel<true, true>, 512, t0, nullptr, s);
+        if (ckpt) go(gemm_bf16_big_kernel<true, false, true>, 512, t0, nullptr, s);
+        else if (prob) go(gemm_bf16_big_kernel<true, true>, 512, t0, nullptr, s);
         else if (fc1) go(gemm_bf16_big_kernel<true, false>, 512, t0, nullptr, s);
         else go(gemm_bf16_big_kernel<false, false>, 512, t0, nullptr, s);
         small_start = nullptr;
         if (s_small) ss = s_small;
     }
-    if (prob) go(gemm_bf16_small_kernel<true, true>, 512, small_start, t1, ss);
+    if (ckpt) go(gemm_bf16_small_kernel<true, false, true>, 512, small_start, t1, ss);
+    else if (prob) go(gemm_bf16_small_kernel<true, true>, 512, small_start, t1, ss);
     else if (fc1) go(gemm_bf16_small_kernel<true, false>, 512, small_start, t1, ss);
     else go(gemm_bf16_small_kernel<false, false>, 512, small_start, t1, ss);
     return hipGetLastError();

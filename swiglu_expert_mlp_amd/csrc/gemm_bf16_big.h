@@ -46,6 +46,7 @@
 
 #include <type_traits>
 
+#include "checkpoint.h"
 #include "gemm_args.h"
 
 namespace moe {
@@ -308,11 +309,36 @@ __device__ __forceinline__ void big_kloop(const BigSrc& t, char* s0, char* s1, c
     big_mma<Op>(acc, y);                               // the last sub-step
 }
 
+// 16 x 64 of a wave's results (row block i, half hv) as fp32 through its LDS region, for
+// lanes that read runs of a row.  16-byte chunk c of row lr lies at chunk
+// c ^ (lr % 4 + 8 ((lr / 4) % 2)): the writes of two rows fall in different halves, and the
+// 16 lanes of 4 rows that read every fourth chunk fall on distinct ones.
+__device__ __forceinline__ int half_swz(int lr) { return 16 * ((lr & 3) | (((lr >> 2) & 1) << 3)); }
+
+template <typename Acc>
+__device__ __forceinline__ void big_half_to_lds(const Acc (&acc)[2], int hv, char* ep, int lane)
+{
+    const int hi = lane >> 5, c32 = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const int lr = 8 * (w >> 2) + 4 * hi + (w & 3);
+            *(float*)(ep + lr * 256 + ((128 * j + 4 * c32) ^ half_swz(lr))) = acc[j][8 * hv + w];
+        }
+}
+
+// FC1 with a checkpoint: 16-byte stores and scale bytes beyond big_stores
+constexpr int kCkptStores = 16;
+
 // The 256-row tile loop of one 8-wave workgroup (one workgroup per CU).
 // n_mt: the number of 256-row M tiles.  Requires K % 64 == 0 and K >= 128
 // (the launch sends other shapes to the 64-row kernel).
 // WPOL, RPOL: the cache policies of the weights' loads and of FC2's row stores.
-template <typename Op, bool FC1, bool PROB, int WPOL = FC1 ? 0 : kNonTemporal, int RPOL = 0>
+// CKPT: FC1 also stores its gate and up values in 8 bits (checkpoint.h): through the wave's
+// LDS region 16 rows at a time, so that a lane holds 16 neighbouring columns of a row (half
+// a block; the block's other half is the next lane's), quantizes them and stores 16 bytes.
+template <typename Op, bool FC1, bool PROB, int WPOL = FC1 ? 0 : kNonTemporal, int RPOL = 0, bool CKPT = false>
 __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
 {
     __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
@@ -396,7 +422,7 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
     // its first stages; before the first tile the same number of stores go to
     // an empty descriptor (the range check drops them all; distinct offsets, so
     // that none is merged away)
-    constexpr int kStores = big_stores<FC1>();
+    constexpr int kStores = big_stores<FC1>() + (CKPT ? kCkptStores : 0);
     {
         const __amdgpu_buffer_rsrc_t none =
             __builtin_amdgcn_make_buffer_rsrc(g.out, (short)0, 0, kBigRsrcWord3);
@@ -511,6 +537,43 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
                     const u32x4_t val = *(const u32x4_t*)(ep + ((rr * 64 + 16 * c) ^ (((rr >> 2) & 1) << 6)));
                     const int off = cols ? ((128 * wm + 32 * i + rr) * F + ib * 32 + 8 * c) * 2 : 0x7ffffff0;
                     __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
+                }
+                if constexpr (CKPT) {
+                    const __amdgpu_buffer_rsrc_t cr = __builtin_amdgcn_make_buffer_rsrc(
+                        (void*)(g.ck_codes + (int64_t)row0 * 2 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
+                    const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+                        (void*)(g.ck_scales + (int64_t)row0 * (F / 16)), (short)0, rows * (F / 16), kBigRsrcWord3);
+                    const int prow = elane >> 2, quarter = elane & 3;
+                    static_assert(kCkptStores == 4 * 2 * 2, "4 row blocks x 2 halves x (codes, scales)");
+#pragma unroll
+                    for (int hv = 0; hv < 2; ++hv) {
+                        big_half_to_lds(acc[i], hv, ep, elane);
+                        float v16[16];
+                        uint32_t amax = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x4 v = *(const f32x4*)(ep + prow * 256 + ((64 * quarter + 16 * q) ^ half_swz(prow)));
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                v16[4 * q + n] = v[n];
+                                amax = max(amax, __float_as_uint(v[n]) & 0x7fffffffu);
+                            }
+                        }
+                        const uint32_t byte = ckpt_byte(pair_max_u32(amax));
+                        const float f = ckpt_factor(byte);
+                        const uint32_t mask = byte == 255u ? 0u : 0xffu;
+                        u32x4_t w;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = (ckpt_code(v16[4 * q], f) & mask) | (ckpt_code(v16[4 * q + 1], f) & mask) << 8 |
+                                   (ckpt_code(v16[4 * q + 2], f) & mask) << 16 |
+                                   (ckpt_code(v16[4 * q + 3], f) & mask) << 24;
+                        const int tr = 128 * wm + 32 * i + 16 * hv + prow;
+                        const int off = cols ? tr * 2 * F + 64 * ib + 16 * quarter : 0x7ffffff0;
+                        __builtin_amdgcn_raw_buffer_store_b128(w, cr, off, 0, 0);
+                        const int soff = cols && !(quarter & 1) ? tr * (F / 16) + 2 * ib + (quarter >> 1) : 0x7ffffff0;
+                        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, sr, soff, 0, 0);
+                    }
                 }
             }
         } else {

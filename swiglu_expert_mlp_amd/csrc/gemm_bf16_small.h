@@ -246,7 +246,9 @@ __device__ __forceinline__ void small_finalize(const GemmArgs& g, SmallFinLds* f
 // WPOL: the cache policy of the weight stream (kNonTemporal when every
 // expert's rows fit one 64-row tile, else the default; the caller reads which
 // from the header).
-template <typename Op, bool FC1, bool PROB, int FUSE, int WPOL>
+// CKPT: FC1 also stores its gate and up values in 8 bits (checkpoint.h); the 32 lanes of a
+// half wave hold one row's block.
+template <typename Op, bool FC1, bool PROB, int FUSE, int WPOL, bool CKPT = false>
 __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n_small, int n_big,
                                             int e0, int row00, int need = 0, SmallFinLds* fin_lds = nullptr)
 {
@@ -436,6 +438,19 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
                 for (int v = 0; v < 16; ++v) {
                     const int r = 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
                     const float rv = Op::kScaled ? lane_value(4 * r, rs) : 1.0f;
+                    if constexpr (CKPT) {
+                        const float val[2] = {acc[i][0][v], acc[i][1][v]};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            // (every lane takes part in the maximum, whatever its row)
+                            const uint32_t byte = ckpt_byte(half_max_u32(__float_as_uint(val[j]) & 0x7fffffffu));
+                            const uint32_t code = byte == 255u ? 0u : ckpt_code(val[j], ckpt_factor(byte));
+                            if (i < nb && r < rows) {
+                                g.ck_codes[(int64_t)(row0 + r) * 2 * F + 64 * cb + 32 * j + c32] = (int8_t)code;
+                                if (c32 == 0) g.ck_scales[(int64_t)(row0 + r) * (F / 16) + 2 * cb + j] = (uint8_t)byte;
+                            }
+                        }
+                    }
                     if (i < nb && r < rows) {
                         const float pr = PROB ? fc1_row_prob(g.row_prob, g.perm_src, row0 + r) : 1.0f;
                         hb[(int64_t)(row0 + r) * F + cb * 32 + c32] =

@@ -1,0 +1,664 @@
+// The experts' backward pass: grouped products on CDNA4 MFMA, bf16 operands, fp32
+// accumulate, 256 x 256 output tiles.
+//
+// With r a grouped row (expert e, token t, probability p) and the interleaved gate/up
+// order of the kernel weights for the columns of dgu and the rows of W1:
+//   rows, SWIGLU   raw[r][f] = sum_h d_out[t][h] W2_e[h][f], then per element, from the
+//                  8-bit gate g and up u:  s = 1 / (1 + exp(-g)),  h = g s u,
+//                    dgu[r] = p raw (u s (1 + g (1 - s)),  g s),   hp[r] = p h,
+//                    part[r][f / 64] = sum over 64 columns of raw h
+//   rows, plain    dx[r][h] = sum_n dgu[r][n] W1_e[n][h]
+//   weights        dW1_e[n][h] = sum_r dgu[r][n] x[t][h]
+//                  dW2_e[h][f] = sum_r d_out[t][h] hp[r][f]
+// dgu, hp and dx are rounded to bf16 (the operand type of the next product, and half
+// the bytes of fp32 rows); every sum is fp32.
+//
+// Every product but the rows' first operand runs over an index that is not contiguous in
+// memory: the rows products over the rows of the kernel weights, which hold 8
+// neighbouring columns together, the weight products over the grouped rows themselves.
+// ds_read_b64_tr_b16 turns 4 x 16 blocks of 16-bit elements on the way from LDS to
+// registers, so no operand is ever transposed in memory and the backward pass reads the
+// same packed weights as the forward.  Of each 16 lanes, lane j names 4 contiguous
+// elements of row j / 4 (columns 4 (j % 4) ..) and lane i receives column i of the 4 rows.
+//
+// The tile loop is the 256-row forward's (gemm_bf16_big.h): 8 waves of 128 x 64, two
+// LDS stages of 64 along the sum by direct global->LDS loads, one barrier a stage, the
+// next tile's first two stages issued before the epilogue, which has LDS of its own.
+#pragma once
+
+#include "gemm_bf16_big.h"
+#include "grad_args.h"
+
+namespace moe {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// 16 bytes of zeros, the source of loads that lie past the end of a sum
+__device__ const uint32_t grad_zeros[4] __attribute__((aligned(16))) = {};
+
+// 8 elements along the sum for one column of an MFMA operand: two transposing reads,
+// the second `step` bytes after the first
+__device__ __forceinline__ bf16x8 grad_tr(const char* p, int step)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + step));
+    const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// The tile range of this workgroup's XCD: 8 contiguous ranges, walked in steps of the
+// XCD's workgroups (gridDim.x / 8)
+struct GradRange { int first, end, step; };
+__device__ __forceinline__ GradRange grad_range(int total)
+{
+    const int xcd = blockIdx.x & 7, chunk = (total + 7) / 8;
+    return {xcd * chunk + (int)(blockIdx.x >> 3), min(total, (xcd + 1) * chunk), (int)(gridDim.x >> 3)};
+}
+
+template <int STORES>
+__device__ __forceinline__ void grad_dummy_stores(void* p, int lane)
+{
+    // the K loop counts the previous tile's stores; before the first tile the same number
+    // go to an empty descriptor, whose range check drops them (distinct offsets, so that
+    // none is merged away)
+    const __amdgpu_buffer_rsrc_t none = __builtin_amdgcn_make_buffer_rsrc(p, (short)0, 0, kBigRsrcWord3);
+#pragma unroll
+    for (int k = 0; k < STORES; ++k)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{0u, 0u, 0u, 0u}, none, 16 * lane + 1024 * k, 0, 0);
+}
+
+struct GradFrag {
+    bf16x8 a[4], b[2];
+};
+
+__device__ __forceinline__ void grad_mma(f32x16 (&acc)[4][2], const GradFrag& f)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+}
+
+// One sub-step of 16 along the sum: the MFMAs of `cur` with the READS fragment reads of
+// the next sub-step spread between them; nothing crosses its ends
+template <int READS, typename Read>
+__device__ __forceinline__ void grad_phase(f32x16 (&acc)[4][2], const GradFrag& cur, Read read, GradFrag& nxt)
+{
+    read(nxt);
+    grad_mma(acc, cur);
+    constexpr int two = READS > 8 ? READS - 8 : 0;       // MFMAs followed by two reads
+#pragma unroll
+    for (int k = 0; k < two; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+#pragma unroll
+    for (int k = two; k < 8; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The sum over nst stages (nst >= 1) of a tile.  On entry this wave's loads of stages 0
+// and 1 are in flight into s0 and s1, followed by AFTER stores.  read(Q, stage, frag)
+// reads the fragments of sub-step Q; issue(stage, s) loads stage s (unconditional, so that
+// no path differs in its loads in flight: past the last stage it loads that one again,
+// into the buffer that no later read of the tile uses).  One last grad_mma for every path:
+// with a copy of it on each, the compiler kept the accumulators twice and spilled.
+template <int READS, int AFTER, typename Read, typename Issue>
+__device__ __forceinline__ void grad_kloop(int nst, char* s0, char* s1, f32x16 (&acc)[4][2],
+                                           Read read, Issue issue)
+{
+    static_assert(AFTER + 9 <= 63, "vmcnt bound");
+    GradFrag x, y;
+    using Q0 = std::integral_constant<int, 0>;
+    using Q1 = std::integral_constant<int, 1>;
+    using Q2 = std::integral_constant<int, 2>;
+    using Q3 = std::integral_constant<int, 3>;
+    BIG_WAIT_VMCNT(AFTER);
+    __builtin_amdgcn_s_barrier();
+    read(Q0{}, s0, x);
+    auto body = [&](const char* cur) {
+        grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, cur, n); }, y);
+        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q2{}, cur, n); }, x);
+        grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q3{}, cur, n); }, y);
+    };
+    // this wave's loads of the next stage landed (N younger operations may be in flight)
+    // and its reads of the current one are done; after the barrier both hold for every
+    // wave, and the current buffer may be refilled
+    auto boundary = [&](auto NC) {
+        constexpr int N = decltype(NC)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        BIG_WAIT_VMCNT(N);
+        __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto into = [&](const char* nxt) {
+        __builtin_amdgcn_sched_barrier(0);
+        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, nxt, n); }, x);
+    };
+    using Now = std::integral_constant<int, 0>;
+    body(s0);
+    if (nst > 1) {
+        boundary(std::integral_constant<int, AFTER>{});
+        issue(s0, min(2, nst - 1));
+        into(s1);
+        int s = 1;
+        for (; s + 2 < nst; s += 2) {
+            body(s1);
+            boundary(Now{});
+            issue(s1, s + 2);
+            into(s0);
+            body(s0);
+            boundary(Now{});
+            issue(s0, min(s + 3, nst - 1));
+            into(s1);
+        }
+        body(s1);
+        if (s + 1 < nst) {
+            boundary(Now{});
+            into(s0);
+            body(s0);
+        }
+    }
+    grad_mma(acc, y);
+}
+
+// 32 x 64 of a wave's results (row block i) to bf16 rows through its LDS region: row rr
+// at 128 rr bytes, 64-byte halves swapped in rows 4 m .. 4 m + 3 with odd m (the two rows a
+// write instruction covers fall in different halves).  store(k, row, chunk, value): the
+// lane's 16 bytes of row `row` of 32, columns 8 chunk .. 8 chunk + 7 of 64, k = 0 .. 3.
+template <typename Store>
+__device__ __forceinline__ void grad_rows_bf16(const f32x16 (&acc)[2], char* ep, int lane, Store store)
+{
+    const int hi = lane >> 5, c32 = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int rr = 8 * (v >> 2) + 4 * hi + (v & 3);
+            int ea = (rr * 128 + 64 * j + 2 * c32) ^ (((rr >> 2) & 1) << 6);
+            asm volatile("" : "+v"(ea));
+            *(uint16_t*)(ep + ea) = f32_to_bf16_bits(acc[j][v]);
+        }
+    const int c = lane & 7;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int rr = (lane >> 3) + 8 * k;
+        store(k, rr, c, *(const u32x4_t*)(ep + ((rr * 128 + 16 * c) ^ (((rr >> 2) & 1) << 6))));
+    }
+}
+
+// ---------------------------------------------------------------- rows products
+
+constexpr int grad_rows_stores(bool swiglu) { return swiglu ? 48 : 16; }
+
+template <bool SWIGLU>
+__device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
+{
+    __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
+    __shared__ __attribute__((aligned(1024))) char lds1[kBigStage];
+    __shared__ __attribute__((aligned(1024))) char lds_x[8 * kBigEpi];
+
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wid >> 2, wn = wid & 3;
+    const int N = SWIGLU ? g.F : g.H;                    // output columns
+    const int Kc = SWIGLU ? g.H : 2 * g.F;               // the sum
+    const uint16_t* const A = SWIGLU ? g.d_out : g.dgu;
+    const uint16_t* const W = SWIGLU ? g.w2 : g.w1;
+    const int nt16 = Kc / 16, ks = N / 32;               // the packed section: rows / 16, columns / 32
+    const int NT = (N + kBigTN - 1) / kBigTN;
+    const int n_big = ld_const(&g.hdr->n_tiles_big), n_small = ld_const(&g.hdr->n_tiles);
+    const int total = (n_big + n_small) * NT;
+    const int nst = (Kc + kBigKS - 1) / kBigKS;
+
+    struct TilePos { int e, row0, rows, n0; };
+    auto locate = [&](int tile) {
+        const int mt = tile / NT;
+        if (mt >= n_big) {
+            const int e = ld_const(&g.tiles[mt - n_big].x), row0 = ld_const(&g.tiles[mt - n_big].y);
+            return TilePos{e, row0, min(kBM, ld_const(g.offsets + e + 1) - row0), (tile - mt * NT) * kBigTN};
+        }
+        // the tiles of one expert keep their index range, walked column tile by column tile
+        const int e = ld_const(&g.tiles_big[mt].x), first = ld_const(&g.tiles_big[mt].y);
+        const int base = ld_const(g.offsets + e), cnt = ld_const(g.offsets + e + 1) - base;
+        const int m_e = (cnt + kBigTM - 1) / kBigTM;
+        const int b_e = mt - (first - base) / kBigTM;
+        const int u = tile - b_e * NT;
+        const int nt = u / m_e, mi = u - nt * m_e;
+        return TilePos{e, base + mi * kBigTM, min(kBigTM, cnt - mi * kBigTM), nt * kBigTN};
+    };
+
+    // activations: lane -> row 32 wid + 8 i + lane / 8 (the last valid row past the tile's),
+    // 16-byte chunk (lane % 8) ^ (row % 8) at slot lane % 8.  Weights: this wave's 32-column
+    // block of the tile, whose 4 row blocks of a stage are 4 KB contiguous; inside a 1 KB
+    // block [chunk q of 8 columns][row n of 16] the 16-byte slot q 16 + n' holds row n' ^ 4 q,
+    // so that the 4 rows x 4 chunks that 32 lanes read together lie on distinct banks.
+    const char* arow[kBigALoads];
+    const char* wbase;
+    int s32;
+    const int wlane = 16 * ((lane & 48) | ((lane & 15) ^ (4 * (lane >> 4))));
+    auto sources = [&](const TilePos& p) {
+#pragma unroll
+        for (int i = 0; i < kBigALoads; ++i) {
+            const int rr = 32 * wid + 8 * i + (lane >> 3);
+            int64_t src = p.row0 + min(rr, p.rows - 1);
+            if constexpr (SWIGLU) src = g.perm_src[src] / g.topk;
+            arow[i] = (const char*)(A + src * Kc);
+        }
+        wbase = (const char*)(W + (int64_t)p.e * Kc * N) + wlane;
+        s32 = min(p.n0 / 32 + wid, ks - 1);
+    };
+    auto issue = [&](char* st, int s) {
+#pragma unroll
+        for (int i = 0; i < kBigALoads; ++i) {
+            const int rr = 32 * wid + 8 * i + (lane >> 3);
+            const int c = 8 * s + ((lane & 7) ^ (rr & 7));
+            big_load_block(c < Kc / 8 ? arow[i] + 16 * c : (const char*)grad_zeros, st + (4 * wid + i) * 1024);
+        }
+        // (the last stage of a sum that is an odd multiple of 32 holds zeros against the
+        // weights of its first half again: a NaN there is one of the same output column)
+        const int grp = s >> 3;
+        const int w = min(32, nt16 - 32 * grp);
+        const char* wp = wbase + ((int64_t)grp * 32 * ks + (int64_t)s32 * w + ((4 * s) & 31)) * 1024;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 4 * s + i < nt16 ? i : i - 2;
+            big_load_block(wp + n * 1024, st + kBigWOff + (4 * wid + i) * 1024);
+        }
+    };
+    // fragments of sub-step Q: A row l % 32, chunk 2 Q + l / 32 at its slot; B one 1 KB
+    // block (16 of the sum x 32 columns), rows 8 (l / 32) + {0, 4} + (l % 16) / 4
+    int a_off[4], b_off[2];
+    {
+        const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a_off[q] = (128 * wm + r) * 128 + 16 * ((2 * q + hi) ^ (r & 7));
+        const int j = lane & 15, q = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            b_off[t] = kBigWOff + 8 * wn * 1024 + q * 256 + 16 * ((8 * hi + 4 * t + (j >> 2)) ^ (4 * q)) + 8 * (j & 1);
+    }
+    auto read = [&](auto QC, const char* st, GradFrag& f) {
+        constexpr int Q = decltype(QC)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            f.b[j] = grad_tr(st + b_off[0] + (4 * j + Q) * 1024, b_off[1] - b_off[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.a[i] = big_frag<OpBf16>(st + a_off[Q] + 32 * 128 * i);
+    };
+
+    const GradRange range = grad_range(total);
+    int tile = range.first;
+    if (tile >= range.end) return;
+    TilePos pos = locate(tile);
+    sources(pos);
+    issue(lds0, 0);
+    issue(lds1, min(1, nst - 1));
+    constexpr int kStores = grad_rows_stores(SWIGLU);
+    grad_dummy_stores<kStores>(g.dgu, lane);
+    char* const ep = lds_x + wid * kBigEpi;
+    while (true) {
+        const int row0 = pos.row0, rows = pos.rows, n0 = pos.n0;
+        f32x16 acc[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        grad_kloop<8, kStores>(nst, lds0, lds1, acc, read, issue);
+
+        const int next = tile + range.step;
+        const bool more = next < range.end;
+        __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        int elane = lane;
+        asm volatile("" : "+v"(elane));
+
+        // SWIGLU: everything the epilogue reads from memory, before the next tile's loads:
+        // lane = row elane / 4 of 16 and 16 of 64 columns; pass (i, hv) covers rows
+        // 32 i + 16 hv .. + 15 of the wave's 128
+        // (the second half of the passes after the first two: all at once spilled)
+        u32x4_t cg[8], cu[8];
+        uint16_t sc[8];
+        float pr0 = 0.0f, pr1 = 0.0f;
+        const int quarter = elane & 3, prow = elane >> 2;
+        const int ib = n0 / 32 + 2 * wn + (quarter >> 1);        // interleave block of the lane's columns
+        const int ibc = min(ib, g.F / 32 - 1);
+        auto kept = [&](int q) {
+            const int64_t row = row0 + min(128 * wm + 16 * q + prow, rows - 1);
+            const int8_t* cp = g.codes + row * 2 * g.F + 64 * ibc + 16 * (quarter & 1);
+            cg[q] = *(const u32x4_t*)cp;
+            cu[q] = *(const u32x4_t*)(cp + 32);
+            sc[q] = *(const uint16_t*)(g.scales + row * (g.F / 16) + 2 * ibc);
+        };
+        if constexpr (SWIGLU) {
+            const int r0 = min(128 * wm + elane, rows - 1), r1 = min(128 * wm + elane + 64, rows - 1);
+            pr0 = g.prob[g.perm_src[row0 + r0]];
+            pr1 = g.prob[g.perm_src[row0 + r1]];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) kept(q);
+        }
+        TilePos npos = pos;
+        if (more) {
+            npos = locate(next);
+            sources(npos);
+        }
+        issue(lds0, 0);
+        issue(lds1, min(1, nst - 1));
+
+        if constexpr (SWIGLU) {
+            const int F = g.F;
+            const bool cols = ib * 32 < F;
+            const __amdgpu_buffer_rsrc_t gu = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(g.dgu + (int64_t)row0 * 2 * F), (short)0, rows * 4 * F, kBigRsrcWord3);
+            const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(g.hp + (int64_t)row0 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
+            const int n_part = (F + 63) / 64;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q == 2) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int n = 4; n < 8; ++n) kept(n);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                big_half_to_lds(acc[q >> 1], q & 1, ep, elane);
+                float raw[16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const f32x4 v = *(const f32x4*)(ep + prow * 256 + ((64 * quarter + 16 * c) ^ half_swz(prow)));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) raw[4 * c + m] = v[m];
+                }
+                const int wr = 128 * wm + 16 * q + prow;         // row of the tile
+                const float p = lane_value(4 * (16 * (q & 3) + prow), q < 4 ? pr0 : pr1);
+                const float sg = __uint_as_float((uint32_t)(sc[q] & 0xff) << 23);
+                const float su = __uint_as_float((uint32_t)(sc[q] >> 8) << 23);
+                float dot = 0.0f;
+                uint32_t og[8], ou[8], oh[8];
+#pragma unroll
+                for (int m = 0; m < 16; m += 2) {
+                    float vg[2], vu[2], vh[2];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int sh = 8 * ((m + n) & 3);
+                        const float gate = (float)((int)(cg[q][(m + n) >> 2] << (24 - sh)) >> 24) * sg;
+                        const float up = (float)((int)(cu[q][(m + n) >> 2] << (24 - sh)) >> 24) * su;
+                        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gate));
+                        const float silu = gate * s;
+                        const float h = silu * up;
+                        const float r = raw[m + n];
+                        dot = __builtin_fmaf(r, h, dot);
+                        const float dh = r * p;
+                        vu[n] = dh * silu;
+                        vg[n] = dh * up * __builtin_fmaf(silu, 1.0f - s, s);
+                        vh[n] = h * p;
+                    }
+                    og[m / 2] = (uint32_t)f32_to_bf16_bits(vg[0]) | ((uint32_t)f32_to_bf16_bits(vg[1]) << 16);
+                    ou[m / 2] = (uint32_t)f32_to_bf16_bits(vu[0]) | ((uint32_t)f32_to_bf16_bits(vu[1]) << 16);
+                    oh[m / 2] = (uint32_t)f32_to_bf16_bits(vh[0]) | ((uint32_t)f32_to_bf16_bits(vh[1]) << 16);
+                }
+                const int og0 = cols ? (wr * 2 * F + 64 * ib + 16 * (quarter & 1)) * 2 : 0x7ffffe00;
+                const int oh0 = cols ? (wr * F + 32 * ib + 16 * (quarter & 1)) * 2 : 0x7ffffe00;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const u32x4_t a = {og[4 * hf], og[4 * hf + 1], og[4 * hf + 2], og[4 * hf + 3]};
+                    const u32x4_t b = {ou[4 * hf], ou[4 * hf + 1], ou[4 * hf + 2], ou[4 * hf + 3]};
+                    const u32x4_t c = {oh[4 * hf], oh[4 * hf + 1], oh[4 * hf + 2], oh[4 * hf + 3]};
+                    __builtin_amdgcn_raw_buffer_store_b128(a, gu, og0 + 16 * hf, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(b, gu, og0 + 64 + 16 * hf, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(c, hr, oh0 + 16 * hf, 0, 0);
+                }
+                if (!cols) dot = 0.0f;
+                dot += __shfl_xor(dot, 1);
+                dot += __shfl_xor(dot, 2);
+                if (quarter == 0 && wr < rows && n0 / 64 + wn < n_part)
+                    g.part[(int64_t)(row0 + wr) * n_part + n0 / 64 + wn] = dot;
+            }
+        } else {
+            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 2, kBigRsrcWord3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                grad_rows_bf16(acc[i], ep, elane, [&](int, int rr, int c, u32x4_t val) {
+                    const int col = n0 + 64 * wn + 8 * c;
+                    const int off = col < N ? ((128 * wm + 32 * i + rr) * N + col) * 2 : 0x7ffffff0;
+                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
+                });
+        }
+        if (!more) {
+            BIG_WAIT_VMCNT(0);          // the repeated loads land before the LDS is released
+            break;
+        }
+        tile = next;
+        pos = npos;
+    }
+}
+
+// ---------------------------------------------------------------- weight products
+
+// The number of experts e < E whose work before them, offsets[e] + kGradTileRows e, is at
+// most `target` (it grows with e), counted by all lanes of a wave at once
+constexpr int kGradTileRows = 256;      // rows that a tile's fixed cost weighs as much as
+__device__ __forceinline__ int grad_experts_below(const int32_t* offsets, int E, int64_t target, int lane)
+{
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        const bool le = e < E && (int64_t)offsets[min(e, E - 1)] + (int64_t)kGradTileRows * e <= target;
+        n += __popcll(__ballot(le));
+    }
+    return n;
+}
+
+// The first of `per_e` E tiles of part x of 8: the parts are contiguous and hold about the
+// same work, a tile of expert e weighing its rows + kGradTileRows (with parts of equally
+// many tiles the XCD of the fullest experts ran on alone)
+__device__ __forceinline__ int grad_part(const int32_t* offsets, int E, int per_e, int x, int lane)
+{
+    if (x <= 0) return 0;
+    if (x >= 8) return E * per_e;
+    const int64_t target = ((int64_t)ld_const(offsets + E) + (int64_t)kGradTileRows * E) * x / 8;
+    const int e = __builtin_amdgcn_readfirstlane(grad_experts_below(offsets, E, target, lane) - 1);      // >= 0: expert 0 has none before it
+    const int64_t row0 = ld_const(offsets + e);
+    const int64_t before = row0 + (int64_t)kGradTileRows * e;
+    const int64_t own = ld_const(offsets + e + 1) - row0 + kGradTileRows;
+    return e * per_e + (int)((target - before) * per_e / own);
+}
+
+// FP32: gradients of the weights in fp32, else bf16
+template <bool FP32>
+__device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
+{
+    __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
+    __shared__ __attribute__((aligned(1024))) char lds1[kBigStage];
+    __shared__ __attribute__((aligned(1024))) char lds_x[8 * kBigEpi];
+
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wid >> 2, wn = wid & 3;
+    const int H = g.H, F = g.F;
+    const int mt1 = (2 * F + kBigTM - 1) / kBigTM, nt1 = (H + kBigTN - 1) / kBigTN;
+    const int mt2 = (H + kBigTM - 1) / kBigTM, nt2 = (F + kBigTN - 1) / kBigTN;
+    const int t1 = mt1 * nt1, per_e = t1 + mt2 * nt2;
+
+    // a tile: M columns of the row matrix P against N columns of Q, over the expert's rows.
+    // W1: P = dgu (its own rows), Q = x (gathered); W2: P = d_out (gathered), Q = hp.
+    struct TilePos { int e, row0, cnt, m0, n0, w2; };
+    auto locate = [&](int tile) {
+        const int e = tile / per_e;
+        int u = tile - e * per_e;
+        const int w2 = u >= t1;
+        if (w2) u -= t1;
+        const int nt = w2 ? nt2 : nt1;
+        const int mi = u / nt;
+        const int base = ld_const(g.offsets + e);
+        return TilePos{e, base, ld_const(g.offsets + e + 1) - base, mi * kBigTM, (u - mi * nt) * kBigTN, w2};
+    };
+
+    // A stage: 64 rows of P, then of Q, 512 bytes each; 16-byte chunk c of row r at slot
+    // c ^ 4 (r % 4), so that the 4 rows x 4 chunks that 32 lanes read together lie on
+    // distinct banks.  Wave w loads rows 8 w .. 8 w + 7 of both, two rows an instruction.
+    // Rows past the expert's last read zeros on the own side (so that they add nothing) and
+    // the last row on the gathered side (so that no value of another row comes in: 0 times
+    // a NaN of the expert's own last row is a NaN that this row gives anyway).  An expert
+    // without rows reads zeros on both sides, and its sum is left out.
+    const char *ob, *gb;                   // own and gathered matrix
+    int64_t opitch, gpitch;                // bytes a row
+    int ocol[2], gcol[2];                  // the lane's column, bytes: rows r % 4 = 0, 1 and 2, 3
+    int cnt = 0, oslot = 0, gslot = 0;     // rows; where own and gathered rows lie in a stage
+    int64_t orow0 = 0;
+    int idx = 0;                           // lane l: route of row 8 w + l % 8 of the next stage to issue
+    auto route = [&](const TilePos& p, int s) {
+        const int r = p.row0 + min(64 * s + 8 * wid + (lane & 7), p.cnt - 1);
+        return g.perm_src[p.cnt > 0 ? r : 0];
+    };
+    auto sources = [&](const TilePos& p) {
+        const int ow = p.w2 ? F : 2 * F;                         // columns of the own matrix
+        const int o0 = p.w2 ? p.n0 : p.m0, g0 = p.w2 ? p.m0 : p.n0;
+        const uint16_t* own = p.w2 ? g.hp : g.dgu;
+        cnt = p.cnt;
+        orow0 = p.row0;
+        oslot = p.w2 ? kBigWOff : 0;
+        gslot = p.w2 ? 0 : kBigWOff;
+        opitch = 2 * (int64_t)ow;
+        gpitch = 2 * (int64_t)H;
+        ob = (const char*)own;
+        gb = (const char*)(p.w2 ? g.d_out : g.x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // the slot's chunk; a column past the matrix reads its last chunk (never stored)
+            const int c = 8 * ((lane & 31) ^ (4 * (2 * h + (lane >> 5))));
+            ocol[h] = 2 * min(o0 + c, ow - 8);
+            gcol[h] = 2 * min(g0 + c, H - 8);
+        }
+        if (p.cnt == 0) {
+            gb = (const char*)grad_zeros;
+            gpitch = 0;
+            gcol[0] = gcol[1] = 0;
+        }
+    };
+    auto issue_rows = [&](char* st, int s, int rt) {
+        const int tok = cnt > 0 ? rt / g.topk : 0;       // (an expert without rows: any value was read)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 64 * s + 8 * wid + 2 * i + (lane >> 5);
+            const int t0 = __builtin_amdgcn_readlane(tok, 2 * i), t1r = __builtin_amdgcn_readlane(tok, 2 * i + 1);
+            const int64_t grow = lane < 32 ? t0 : t1r;
+            big_load_block(r < cnt ? ob + (orow0 + r) * opitch + ocol[i & 1] : (const char*)grad_zeros, st + oslot + (4 * wid + i) * 1024);
+            big_load_block(gb + grow * gpitch + gcol[i & 1], st + gslot + (4 * wid + i) * 1024);
+        }
+    };
+    TilePos pos, npos;
+    auto issue = [&](char* st, int s) {
+        issue_rows(st, s, idx);
+        idx = route(pos, s + 1);
+    };
+    // the first two stages of a tile and the routes of its third
+    auto start = [&](const TilePos& p) {
+        const int i0 = route(p, 0), i1 = route(p, 1);
+        sources(p);
+        issue_rows(lds0, 0, i0);
+        issue_rows(lds1, 1, i1);
+        idx = route(p, 2);
+    };
+    // fragments of sub-step Q: rows 16 Q + 8 (l / 32) + {0, 4} + (l % 16) / 4, the lane's 4
+    // columns of each 32-column block
+    int a_off[4], b_off[2];
+    {
+        const int j = lane & 15, jj = j >> 2;
+        const int base = (8 * (lane >> 5) + jj) * 512 + 16 * (2 * ((lane >> 4) & 1) + ((j & 3) >> 1)) + 8 * (j & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a_off[i] = base + 64 * ((4 * wm + i) ^ jj);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b_off[i] = kBigWOff + base + 64 * ((2 * wn + i) ^ jj);
+    }
+    auto read = [&](auto QC, const char* st, GradFrag& f) {
+        constexpr int Q = decltype(QC)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f.b[j] = grad_tr(st + b_off[j] + 8192 * Q, 2048);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.a[i] = grad_tr(st + a_off[i] + 8192 * Q, 2048);
+    };
+
+    const int xcd = blockIdx.x & 7;
+    const int end = grad_part(g.offsets, g.E, per_e, xcd + 1, lane);
+    int tile = grad_part(g.offsets, g.E, per_e, xcd, lane) + (int)(blockIdx.x >> 3);
+    if (tile >= end) return;
+    pos = locate(tile);
+    start(pos);
+    constexpr int kStores = FP32 ? 32 : 16;
+    grad_dummy_stores<kStores>(g.dgu, lane);
+    char* const ep = lds_x + wid * kBigEpi;
+    while (true) {
+        f32x16 acc[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        if (pos.cnt > 0) grad_kloop<12, kStores>((pos.cnt + 63) / 64, lds0, lds1, acc, read, issue);
+        else BIG_WAIT_VMCNT(kStores);               // its loads land before the next tile's go out
+
+        const int next = tile + (int)(gridDim.x >> 3);
+        const bool more = next < end;
+        __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        npos = pos;
+        if (more) npos = locate(next);
+        start(npos);
+
+        int elane = lane;
+        asm volatile("" : "+v"(elane));
+        const int M = pos.w2 ? H : 2 * F, N = pos.w2 ? F : H;
+        void* const out = pos.w2 ? g.d_w2 : g.d_w1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // a 32-row block: of the interleaved order of W1, gate and up by turns
+            const int blk = pos.m0 / 32 + 4 * wm + i;
+            const int row = pos.w2 ? 32 * blk : (blk & 1 ? F : 0) + 32 * (blk >> 1);
+            const int64_t at = ((int64_t)pos.e * M + row) * N;
+            const int recs = 32 * blk < M ? 32 * N * (FP32 ? 4 : 2) : 0;
+            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
+                FP32 ? (void*)((float*)out + at) : (void*)((uint16_t*)out + at), (short)0, recs, kBigRsrcWord3);
+            if constexpr (FP32) {
+#pragma unroll
+                for (int hv = 0; hv < 2; ++hv) {
+                    big_half_to_lds(acc[i], hv, ep, elane);
+                    const int c = elane & 15;
+                    const int col = pos.n0 + 64 * wn + 4 * c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int lr = (elane >> 4) + 4 * k;
+                        const u32x4_t val = *(const u32x4_t*)(ep + lr * 256 + ((16 * c) ^ half_swz(lr)));
+                        const int off = col < N ? ((16 * hv + lr) * N + col) * 4 : 0x7ffffff0;
+                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
+                    }
+                }
+            } else {
+                grad_rows_bf16(acc[i], ep, elane, [&](int, int rr, int c, u32x4_t val) {
+                    const int col = pos.n0 + 64 * wn + 8 * c;
+                    const int off = col < N ? (rr * N + col) * 2 : 0x7ffffff0;
+                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
+                });
+            }
+        }
+        if (!more) {
+            BIG_WAIT_VMCNT(0);          // the repeated loads land before the LDS is released
+            break;
+        }
+        tile = next;
+        pos = npos;
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,30 @@
+// Launches of the experts' backward products (grad_gemm.h): the rows' gradients before and
+// after the SwiGLU, then both weights' gradients in one launch.
+#include "grad_gemm.h"
+
+namespace moe {
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(512, 1) grad_rows_kernel(GradArgs g)
+{
+    grad_rows_tiles<SWIGLU>(g);
+}
+
+template <bool FP32>
+__global__ void __launch_bounds__(512, 1) grad_weight_kernel(GradArgs g)
+{
+    grad_weight_tiles<FP32>(g);
+}
+
+hipError_t launch_grad_gemms(const GradArgs& g, bool fp32, int num_cu, hipStream_t s)
+{
+    // a multiple of 8 workgroups: the tiles are split over the 8 XCDs
+    const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
+    hipLaunchKernelGGL(grad_rows_kernel<true>, grid, block, 0, s, g);
+    hipLaunchKernelGGL(grad_rows_kernel<false>, grid, block, 0, s, g);
+    if (fp32) hipLaunchKernelGGL(grad_weight_kernel<true>, grid, block, 0, s, g);
+    else hipLaunchKernelGGL(grad_weight_kernel<false>, grid, block, 0, s, g);
+    return hipGetLastError();
+}
+
+}  // namespace moe

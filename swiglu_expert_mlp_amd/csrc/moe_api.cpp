@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -43,13 +44,28 @@ hipError_t launch_quant_rows_int8(const QuantRows& a, const QuantTiles* tiles, i
 hipError_t launch_pack_int8(const void* w1, const float* ws1, const void* w2, const float* ws2, int codes,
                             uint8_t* kbuf, int E, int H, int F, int num_cu, hipStream_t s);
 void int8_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
+hipError_t launch_dispatch(const void* x, int bf16, const int32_t* ids, const int32_t* dst, const int32_t* offsets,
+                           const int32_t* live, int64_t T_cap, int E, int k, int H, void* rows, int32_t* row_of,
+                           int32_t* offsets_out, int num_cu, hipStream_t s);
+hipError_t launch_combine(const void* rows, int in_bf16, const int32_t* row_of, const float* probs,
+                          const int32_t* live, int64_t T_cap, int k, int H, void* out, int out_bf16, int num_cu,
+                          hipStream_t s);
+hipError_t launch_combine_backward(const void* d_out, int out_bf16, const void* rows, int rows_bf16,
+                                   const int32_t* row_of, const float* probs, const int32_t* live, int64_t T_cap,
+                                   int k, int H, void* d_rows, float* d_probs, int num_cu, hipStream_t s);
+hipError_t launch_grad_probs(const float* part, int n_part, const int32_t* ids, const int32_t* dst,
+                             const int32_t* live, int64_t T_cap, int k, float* d_probs, int num_cu, hipStream_t s);
+hipError_t launch_cast_rows(const float* in, const int32_t* live, int64_t T_cap, int H, uint16_t* out, int num_cu,
+                            hipStream_t s);
 hipError_t launch_quant_x(const uint16_t* x, int64_t T_cap, const int32_t* live, int H,
                           uint8_t* codes, uint8_t* scales, int num_cu, hipStream_t s);
 }  // namespace moe
 
 #include "gemm_args.h"
+#include "grad_args.h"
 
 namespace moe {
+hipError_t launch_grad_gemms(const GradArgs& g, bool fp32, int num_cu, hipStream_t s);
 hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
                             hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
@@ -116,11 +132,13 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb)
     return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
 }
 
-static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
+// The regions of the permutation, at the start of every workspace that it runs on;
+// returns their end
+static size_t prep_layout(const moe_ctx* h, int64_t T_cap, WsLayout& L)
 {
-    WsLayout L;
-    const int64_t E = h->E, H = h->H, F = h->F, k = h->k;
+    const int64_t E = h->E, H = h->H, k = h->k;
     const int64_t R = T_cap * k;
+    L = WsLayout{};
     L.nchunks = (T_cap + kChunkTok - 1) / kChunkTok;
     if (L.nchunks < 1) L.nchunks = 1;
     L.max_tiles = E + (R + kBM - 1) / kBM + 1;
@@ -141,6 +159,16 @@ static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
     L.tiles_big = take(8 * L.max_tiles_big);
     L.ready = take(4 * (L.max_tiles + 4 * L.max_tiles_big));
     L.fin_cnt = take(4 * T_cap * ((H + kFinCols - 1) / kFinCols));
+    return o;
+}
+
+static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
+{
+    WsLayout L;
+    const int64_t H = h->H, F = h->F;
+    const int64_t R = T_cap * h->k;
+    size_t o = prep_layout(h, T_cap, L);
+    auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes > 0 ? bytes : 1); return at; };
     if (h->precision == MOE_BF16) {
         L.hbuf = take(2 * R * F);
         L.hscale = 0;
@@ -162,6 +190,32 @@ static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
     L.obuf = take(4 * R * H);
     L.total = o;
     return L;
+}
+
+// Workspace of the experts' backward pass: the permutation, then rows between its products
+struct BackwardLayout {
+    WsLayout prep;
+    size_t dgu;            // bf16 [R][2F]: gradient of gate and up
+    size_t hp;             // bf16 [R][F]: SwiGLU rows times their probability
+    size_t dx;             // bf16 [R][H]: gradient of the grouped rows of x
+    size_t part;           // fp32 [R][ceil(F / 64)]: partial sums of the probabilities' gradient
+    size_t d_out;          // bf16 [T_cap][H]: d_out rounded, where it is given in fp32
+    size_t total;
+};
+
+static BackwardLayout backward_layout(const moe_ctx* h, int64_t T_cap)
+{
+    BackwardLayout B;
+    const int64_t H = h->H, F = h->F, R = T_cap * h->k;
+    size_t o = prep_layout(h, T_cap, B.prep);
+    auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes > 0 ? bytes : 1); return at; };
+    B.dgu = take(4 * R * F);
+    B.hp = take(2 * R * F);
+    B.dx = take(2 * R * H);
+    B.part = take(4 * R * ((F + 63) / 64));
+    B.d_out = take(2 * T_cap * H);
+    B.total = o;
+    return B;
 }
 
 static moe_status ensure_device(moe_ctx* h)
@@ -493,9 +547,10 @@ moe_status moe_forward(moe_handle h, const void* x, const int32_t* expert_ids,
                           ws_bytes, stream);
 }
 
-moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids,
-                          const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
-                          int combine, void* out, void* ws, size_t ws_bytes, hipStream_t stream)
+// moe_forward_ex; with codes and scales, FC1 also keeps its gate and up values there
+static moe_status forward_impl(moe_handle h, const void* x, const int32_t* expert_ids, const float* probs,
+                               int64_t T_cap, const int32_t* live_rows_dev, int combine, void* out, int8_t* codes,
+                               uint8_t* scales, void* ws, size_t ws_bytes, hipStream_t stream)
 {
     if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_forward: NULL handle");
     if (!h->kbuf) return fail(MOE_ERR_NOT_LOADED, "moe_forward: no weights loaded (moe_load_weights)");
@@ -543,9 +598,11 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
     if ((e = mark(h, 1, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     const int E = h->E, H = h->H, F = h->F;
     if (h->precision == MOE_BF16) {
-        GemmArgs g1;
+        GemmArgs g1{};
         g1.A = (const uint16_t*)x;
         g1.W = (const uint16_t*)h->kbuf;
+        g1.ck_codes = codes;
+        g1.ck_scales = scales;
         g1.perm_src = (const int32_t*)(w + L.perm_src);
         g1.tiles = (const int2*)(w + L.tiles);
         g1.tiles_big = (const int2*)(w + L.tiles_big);
@@ -801,6 +858,233 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
                         live_rows_dev, h->k, H, combine, out, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: finalize launch");
     if ((e = mark(h, 5, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
+    return MOE_OK;
+}
+
+moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids,
+                          const float* probs, int64_t T_cap, const int32_t* live_rows_dev,
+                          int combine, void* out, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    return forward_impl(h, x, expert_ids, probs, T_cap, live_rows_dev, combine, out, nullptr, nullptr, ws, ws_bytes,
+                        stream);
+}
+
+// Pointers of a call: none may be null or unaligned
+static moe_status check_ptrs(const char* what, std::initializer_list<const void*> ptrs)
+{
+    for (const void* p : ptrs)
+        if (!p) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+    return MOE_OK;
+}
+
+static moe_status check_tokens(const char* what, moe_handle h, int64_t T_cap)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "%s: NULL handle", what);
+    if (T_cap < 0 || T_cap > (int64_t)1 << 26)
+        return fail(MOE_ERR_INVALID_ARG, "%s: T_cap=%lld out of range", what, (long long)T_cap);
+    return MOE_OK;
+}
+
+static moe_status check_type(const char* what, int type)
+{
+    if (type != MOE_TYPE_FP32 && type != MOE_TYPE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "%s: type %d (fp32=0, bf16=1)", what, type);
+    return MOE_OK;
+}
+
+static size_t type_bytes(int type) { return type == MOE_TYPE_BF16 ? 2 : 4; }
+
+struct Span { const void* p; size_t n; };
+
+// An output may overlap neither an input nor another output
+static moe_status check_overlap(const char* what, std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p || !o->n) continue;
+        for (const Span& i : ins)
+            if (i.p && i.n && overlap(o->p, o->n, i.p, i.n))
+                return fail(MOE_ERR_INVALID_ARG, "%s: an output must not be in an input's memory", what);
+        for (const Span* q = outs.begin(); q != o; ++q)
+            if (q->p && q->n && overlap(o->p, o->n, q->p, q->n))
+                return fail(MOE_ERR_INVALID_ARG, "%s: two outputs share memory", what);
+    }
+    return MOE_OK;
+}
+
+moe_status moe_forward_checkpoint(moe_handle h, const void* x, const int32_t* expert_ids, const float* probs,
+                                  int64_t T_cap, const int32_t* live_rows_dev, int combine, void* out, int8_t* codes,
+                                  uint8_t* scales, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_forward_checkpoint: NULL handle");
+    if (h->precision != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "moe_forward_checkpoint: the handle's precision is not bf16");
+    if (combine != MOE_COMBINE_FP32 && combine != MOE_COMBINE_BF16 && combine != MOE_COMBINE_ROWS)
+        return fail(MOE_ERR_INVALID_ARG, "moe_forward_checkpoint: combine %d (no options are taken)", combine);
+    moe_status st = check_tokens("moe_forward_checkpoint", h, T_cap);
+    if (st != MOE_OK || (st = check_ptrs("moe_forward_checkpoint", {codes, scales})) != MOE_OK) return st;
+    const size_t T = T_cap, R = T * h->k, H = h->H;
+    const size_t out_bytes = combine == MOE_COMBINE_ROWS ? 4 * R * H : combine == MOE_COMBINE_BF16 ? 2 * T * H : 4 * T * H;
+    st = check_overlap("moe_forward_checkpoint", {{codes, R * 2 * h->F}, {scales, R * (h->F / 16)}},
+                       {{x, 2 * T * H}, {expert_ids, 4 * R}, {probs, 4 * R}, {live_rows_dev, 4}, {out, out_bytes},
+                        {ws, layout_of(h, T_cap).total}, {h->kbuf, moe_weight_bytes(h)}});
+    if (st != MOE_OK) return st;
+    return forward_impl(h, x, expert_ids, probs, T_cap, live_rows_dev, combine, out, codes, scales, ws, ws_bytes,
+                        stream);
+}
+
+size_t moe_backward_workspace_bytes(moe_handle h, int64_t T_cap)
+{
+    if (!h || T_cap < 0) return 0;
+    return backward_layout(h, T_cap).total;
+}
+
+moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const void* x, const int32_t* expert_ids,
+                        const float* probs, int64_t T_cap, const int32_t* live_rows_dev, const int8_t* codes,
+                        const uint8_t* scales, void* d_x, void* d_w1, void* d_w2, int d_w_type, float* d_probs,
+                        void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const char* what = "moe_backward";
+    moe_status st = check_tokens(what, h, T_cap);
+    if (st != MOE_OK) return st;
+    if (h->precision != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "%s: the handle's precision is not bf16", what);
+    if (!h->kbuf) return fail(MOE_ERR_NOT_LOADED, "%s: no weights loaded (moe_load_weights)", what);
+    if ((st = check_type(what, d_out_type)) != MOE_OK || (st = check_type(what, d_w_type)) != MOE_OK) return st;
+    if ((st = check_ptrs(what, {d_out, x, expert_ids, probs, live_rows_dev, codes, scales, d_x, d_w1, d_w2, d_probs, ws})) !=
+        MOE_OK)
+        return st;
+    const BackwardLayout B = backward_layout(h, T_cap);
+    if (ws_bytes < B.total)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu for T_cap=%lld", what, ws_bytes, B.total,
+                    (long long)T_cap);
+    const size_t E = h->E, H = h->H, F = h->F, T = T_cap, R = T * h->k;
+    st = check_overlap(what,
+                       {{d_x, 2 * T * H}, {d_w1, E * 2 * F * H * type_bytes(d_w_type)},
+                        {d_w2, E * H * F * type_bytes(d_w_type)}, {d_probs, 4 * R}, {ws, B.total}},
+                       {{d_out, T * H * type_bytes(d_out_type)}, {x, 2 * T * H}, {expert_ids, 4 * R}, {probs, 4 * R},
+                        {live_rows_dev, 4}, {codes, R * 2 * F}, {scales, R * (F / 16)}, {h->kbuf, moe_weight_bytes(h)}});
+    if (st != MOE_OK || (st = ensure_device(h)) != MOE_OK) return st;
+    char* w = (char*)ws;
+    const WsLayout& L = B.prep;
+    hipError_t e = launch_prep(expert_ids, probs, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
+                               MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr);
+    if (e != hipSuccess) return hip_fail(e, "moe_backward: prep launch");
+    const uint16_t* g_out = (const uint16_t*)d_out;
+    if (d_out_type == MOE_TYPE_FP32) {
+        e = launch_cast_rows((const float*)d_out, live_rows_dev, T_cap, h->H, (uint16_t*)(w + B.d_out), h->num_cu, stream);
+        if (e != hipSuccess) return hip_fail(e, "moe_backward: d_out launch");
+        g_out = (const uint16_t*)(w + B.d_out);
+    }
+    GradArgs g{};
+    g.tiles = (const int2*)(w + L.tiles);
+    g.tiles_big = (const int2*)(w + L.tiles_big);
+    g.offsets = (const int32_t*)(w + L.offsets);
+    g.hdr = (const WsHeader*)(w + L.hdr);
+    g.perm_src = (const int32_t*)(w + L.perm_src);
+    g.prob = (const float*)(w + L.sorted_probs);
+    g.E = h->E; g.H = h->H; g.F = h->F; g.topk = h->k;
+    g.x = (const uint16_t*)x;
+    g.d_out = g_out;
+    g.w1 = (const uint16_t*)h->kbuf;
+    g.w2 = (const uint16_t*)h->kbuf + E * 2 * F * H;
+    g.codes = codes;
+    g.scales = scales;
+    g.dgu = (uint16_t*)(w + B.dgu);
+    g.hp = (uint16_t*)(w + B.hp);
+    g.dx = (uint16_t*)(w + B.dx);
+    g.part = (float*)(w + B.part);
+    g.d_w1 = d_w1;
+    g.d_w2 = d_w2;
+    e = launch_grad_gemms(g, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_backward: product launch");
+    if (T_cap == 0) return MOE_OK;
+    e = launch_combine(g.dx, 1, (const int32_t*)(w + L.dst), nullptr, live_rows_dev, T_cap, h->k, h->H, d_x, 1,
+                       h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_backward: d_x launch");
+    e = launch_grad_probs(g.part, (h->F + 63) / 64, expert_ids, (const int32_t*)(w + L.dst), live_rows_dev, T_cap,
+                          h->k, d_probs, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_backward: d_probs launch");
+    return MOE_OK;
+}
+
+size_t moe_dispatch_workspace_bytes(moe_handle h, int64_t T_cap)
+{
+    if (!h || T_cap < 0) return 0;
+    WsLayout L;
+    return prep_layout(h, T_cap, L);
+}
+
+moe_status moe_dispatch(moe_handle h, const void* x, int type, const int32_t* expert_ids, int64_t T_cap,
+                        const int32_t* live_rows_dev, void* rows, int32_t* row_of, int32_t* offsets, void* ws,
+                        size_t ws_bytes, hipStream_t stream)
+{
+    const char* what = "moe_dispatch";
+    moe_status st = check_tokens(what, h, T_cap);
+    if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK ||
+        (st = check_ptrs(what, {x, expert_ids, live_rows_dev, rows, row_of, offsets, ws})) != MOE_OK)
+        return st;
+    WsLayout L;
+    const size_t need = prep_layout(h, T_cap, L);
+    if (ws_bytes < need)
+        return fail(MOE_ERR_INVALID_ARG, "%s: ws_bytes %zu < %zu for T_cap=%lld", what, ws_bytes, need, (long long)T_cap);
+    const size_t T = T_cap, R = T * h->k, row = h->H * type_bytes(type);
+    st = check_overlap(what, {{rows, R * row}, {row_of, 4 * R}, {offsets, 4 * (size_t)(h->E + 1)}, {ws, need}},
+                       {{x, T * row}, {expert_ids, 4 * R}, {live_rows_dev, 4}});
+    if (st != MOE_OK || (st = ensure_device(h)) != MOE_OK) return st;
+    char* w = (char*)ws;
+    hipError_t e = launch_prep(expert_ids, nullptr, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
+                               MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr);
+    if (e != hipSuccess) return hip_fail(e, "moe_dispatch: prep launch");
+    e = launch_dispatch(x, type == MOE_TYPE_BF16, expert_ids, (const int32_t*)(w + L.dst),
+                        (const int32_t*)(w + L.offsets), live_rows_dev, T_cap, h->E, h->k, h->H, rows, row_of, offsets,
+                        h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_dispatch: launch");
+    return MOE_OK;
+}
+
+moe_status moe_combine_rows(moe_handle h, const void* rows, int type, const int32_t* row_of, const float* probs,
+                            int64_t T_cap, const int32_t* live_rows_dev, void* out, int out_type, hipStream_t stream)
+{
+    const char* what = "moe_combine_rows";
+    moe_status st = check_tokens(what, h, T_cap);
+    if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK || (st = check_type(what, out_type)) != MOE_OK ||
+        (st = check_ptrs(what, {rows, row_of, live_rows_dev, out})) != MOE_OK)
+        return st;
+    if (!aligned16(probs)) return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+    const size_t T = T_cap, R = T * h->k, H = h->H;
+    st = check_overlap(what, {{out, T * H * type_bytes(out_type)}},
+                       {{rows, R * H * type_bytes(type)}, {row_of, 4 * R}, {probs, 4 * R}, {live_rows_dev, 4}});
+    if (st != MOE_OK || (st = ensure_device(h)) != MOE_OK) return st;
+    if (T_cap == 0) return MOE_OK;
+    const hipError_t e = launch_combine(rows, type == MOE_TYPE_BF16, row_of, probs, live_rows_dev, T_cap, h->k, h->H,
+                                        out, out_type == MOE_TYPE_BF16, h->num_cu, stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_combine_rows: launch");
+    return MOE_OK;
+}
+
+moe_status moe_combine_backward(moe_handle h, const void* d_out, int out_type, const void* rows, int type,
+                                const int32_t* row_of, const float* probs, int64_t T_cap,
+                                const int32_t* live_rows_dev, void* d_rows, float* d_probs, hipStream_t stream)
+{
+    const char* what = "moe_combine_backward";
+    moe_status st = check_tokens(what, h, T_cap);
+    if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK || (st = check_type(what, out_type)) != MOE_OK ||
+        (st = check_ptrs(what, {d_out, row_of, probs, live_rows_dev, d_rows})) != MOE_OK)
+        return st;
+    if (!rows != !d_probs) return fail(MOE_ERR_INVALID_ARG, "%s: d_probs needs rows, and rows d_probs", what);
+    if (!aligned16(rows) || !aligned16(d_probs))
+        return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+    const size_t T = T_cap, R = T * h->k, H = h->H;
+    st = check_overlap(what, {{d_rows, R * H * type_bytes(type)}, {d_probs, 4 * R}},
+                       {{d_out, T * H * type_bytes(out_type)}, {rows, rows ? R * H * type_bytes(type) : 0},
+                        {row_of, 4 * R}, {probs, 4 * R}, {live_rows_dev, 4}});
+    if (st != MOE_OK || (st = ensure_device(h)) != MOE_OK) return st;
+    if (T_cap == 0) return MOE_OK;
+    const hipError_t e = launch_combine_backward(d_out, out_type == MOE_TYPE_BF16, rows, type == MOE_TYPE_BF16, row_of,
+                                                 probs, live_rows_dev, T_cap, h->k, h->H, d_rows, d_probs, h->num_cu,
+                                                 stream);
+    if (e != hipSuccess) return hip_fail(e, "moe_combine_backward: launch");
     return MOE_OK;
 }
 
