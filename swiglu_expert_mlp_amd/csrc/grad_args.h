@@ -21,8 +21,9 @@ struct GradArgs {
     const uint8_t* scales;     // [rows][F / 16]
     uint16_t* dgu;             // bf16 [rows][2F]
     uint16_t* hp;              // bf16 [rows][F]
-    uint16_t* dx;              // bf16 [rows][H]
-    float* part;               // fp32 [rows][ceil(F / 64)]
+    float* dx;                 // fp32 [rows][H]
+    float* part;               // fp32 [rows][F / 32]
+    int32_t* row_tok;          // int32 [rows]: token of each grouped row
     void* d_w1;                // [E][2F][H], gate rows first
     void* d_w2;                // [E][H][F]
 };

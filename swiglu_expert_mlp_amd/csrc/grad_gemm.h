@@ -196,7 +196,71 @@ __device__ __forceinline__ void grad_rows_bf16(const f32x16 (&acc)[2], char* ep,
 
 // ---------------------------------------------------------------- rows products
 
-constexpr int grad_rows_stores(bool swiglu) { return swiglu ? 48 : 16; }
+// What 16 neighbouring columns of a row need from memory: kept gate and up codes and the
+// two scale bytes of their block
+struct GradKept {
+    u32x4_t cg, cu;
+    uint16_t sc;
+};
+__device__ __forceinline__ GradKept grad_kept(const GradArgs& g, int64_t row, int block, int half)
+{
+    const int8_t* c = g.codes + row * 2 * g.F + 64 * block + 16 * half;
+    return {*(const u32x4_t*)c, *(const u32x4_t*)(c + 32), *(const uint16_t*)(g.scales + row * (g.F / 16) + 2 * block)};
+}
+
+// The SwiGLU's backward of 16 columns: bf16 pairs of the gate's and up's gradients and of
+// p h; returns the sum of raw h
+__device__ __forceinline__ float grad_swiglu16(const float (&raw)[16], const GradKept& k, float p, uint32_t (&og)[8],
+                                               uint32_t (&ou)[8], uint32_t (&oh)[8])
+{
+    const float sg = ckpt_scale(k.sc & 0xff), su = ckpt_scale(k.sc >> 8);
+    float dot = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 16; m += 2) {
+        float vg[2], vu[2], vh[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int sh = 24 - 8 * ((m + n) & 3);
+            const float gate = (float)((int)(k.cg[(m + n) >> 2] << sh) >> 24) * sg;
+            const float up = (float)((int)(k.cu[(m + n) >> 2] << sh) >> 24) * su;
+            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gate));
+            const float silu = gate * s;
+            const float h = silu * up;
+            dot = __builtin_fmaf(raw[m + n], h, dot);
+            const float dh = raw[m + n] * p;
+            vu[n] = dh * silu;
+            vg[n] = dh * up * __builtin_fmaf(silu, 1.0f - s, s);
+            vh[n] = h * p;
+        }
+        og[m / 2] = (uint32_t)f32_to_bf16_bits(vg[0]) | ((uint32_t)f32_to_bf16_bits(vg[1]) << 16);
+        ou[m / 2] = (uint32_t)f32_to_bf16_bits(vu[0]) | ((uint32_t)f32_to_bf16_bits(vu[1]) << 16);
+        oh[m / 2] = (uint32_t)f32_to_bf16_bits(vh[0]) | ((uint32_t)f32_to_bf16_bits(vh[1]) << 16);
+    }
+    return dot;
+}
+
+// Stores of grad_swiglu16's results: row `row` of the tile, columns 16 half .. of `block`
+// (past the last block: outside the descriptors, which drop them)
+__device__ __forceinline__ void grad_swiglu_store(__amdgpu_buffer_rsrc_t gu, __amdgpu_buffer_rsrc_t hr, int F, int row,
+                                                  int block, int half, const uint32_t (&og)[8], const uint32_t (&ou)[8],
+                                                  const uint32_t (&oh)[8])
+{
+    const bool cols = block * 32 < F;
+    const int og0 = cols ? (row * 2 * F + 64 * block + 16 * half) * 2 : 0x7ffffe00;
+    const int oh0 = cols ? (row * F + 32 * block + 16 * half) * 2 : 0x7ffffe00;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const u32x4_t a = {og[4 * hf], og[4 * hf + 1], og[4 * hf + 2], og[4 * hf + 3]};
+        const u32x4_t b = {ou[4 * hf], ou[4 * hf + 1], ou[4 * hf + 2], ou[4 * hf + 3]};
+        const u32x4_t c = {oh[4 * hf], oh[4 * hf + 1], oh[4 * hf + 2], oh[4 * hf + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(a, gu, og0 + 16 * hf, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(b, gu, og0 + 64 + 16 * hf, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(c, hr, oh0 + 16 * hf, 0, 0);
+    }
+}
+
+// dx: fp32 rows (rounded to bf16 they would add a third rounding to d_x's two)
+constexpr int grad_rows_stores(bool swiglu) { return swiglu ? 48 : 32; }
 
 template <bool SWIGLU>
 __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
@@ -214,17 +278,12 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     const uint16_t* const W = SWIGLU ? g.w2 : g.w1;
     const int nt16 = Kc / 16, ks = N / 32;               // the packed section: rows / 16, columns / 32
     const int NT = (N + kBigTN - 1) / kBigTN;
-    const int n_big = ld_const(&g.hdr->n_tiles_big), n_small = ld_const(&g.hdr->n_tiles);
-    const int total = (n_big + n_small) * NT;
+    const int total = ld_const(&g.hdr->n_tiles_big) * NT;
     const int nst = (Kc + kBigKS - 1) / kBigKS;
 
     struct TilePos { int e, row0, rows, n0; };
     auto locate = [&](int tile) {
         const int mt = tile / NT;
-        if (mt >= n_big) {
-            const int e = ld_const(&g.tiles[mt - n_big].x), row0 = ld_const(&g.tiles[mt - n_big].y);
-            return TilePos{e, row0, min(kBM, ld_const(g.offsets + e + 1) - row0), (tile - mt * NT) * kBigTN};
-        }
         // the tiles of one expert keep their index range, walked column tile by column tile
         const int e = ld_const(&g.tiles_big[mt].x), first = ld_const(&g.tiles_big[mt].y);
         const int base = ld_const(g.offsets + e), cnt = ld_const(g.offsets + e + 1) - base;
@@ -244,12 +303,24 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     const char* wbase;
     int s32;
     const int wlane = 16 * ((lane & 48) | ((lane & 15) ^ (4 * (lane >> 4))));
+    // the routes of a tile's rows: loaded before the K loop of the tile before it
+    int look[kBigALoads] = {};
+    auto lookup = [&](const TilePos& p) {
+        if constexpr (SWIGLU)
+#pragma unroll
+            for (int i = 0; i < kBigALoads; ++i)
+                look[i] = g.perm_src[p.row0 + min(32 * wid + 8 * i + (lane >> 3), p.rows - 1)];
+    };
     auto sources = [&](const TilePos& p) {
 #pragma unroll
         for (int i = 0; i < kBigALoads; ++i) {
-            const int rr = 32 * wid + 8 * i + (lane >> 3);
-            int64_t src = p.row0 + min(rr, p.rows - 1);
-            if constexpr (SWIGLU) src = g.perm_src[src] / g.topk;
+            int64_t src = p.row0 + min(32 * wid + 8 * i + (lane >> 3), p.rows - 1);
+            if constexpr (SWIGLU) {
+                // the first column tile leaves the token of every row for the weight products
+                const int tok = look[i] / g.topk;
+                if (p.n0 == 0 && (lane & 7) == 0) g.row_tok[src] = tok;
+                src = tok;
+            }
             arow[i] = (const char*)(A + src * Kc);
         }
         wbase = (const char*)(W + (int64_t)p.e * Kc * N) + wlane;
@@ -297,11 +368,13 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     const GradRange range = grad_range(total);
     int tile = range.first;
     if (tile >= range.end) return;
-    TilePos pos = locate(tile);
+    TilePos pos = locate(tile), npos = pos;
+    lookup(pos);
     sources(pos);
     issue(lds0, 0);
     issue(lds1, min(1, nst - 1));
     constexpr int kStores = grad_rows_stores(SWIGLU);
+    constexpr int kLook = SWIGLU ? kBigALoads : 0;
     grad_dummy_stores<kStores>(g.dgu, lane);
     char* const ep = lds_x + wid * kBigEpi;
     while (true) {
@@ -313,10 +386,11 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        grad_kloop<8, kStores>(nst, lds0, lds1, acc, read, issue);
-
         const int next = tile + range.step;
         const bool more = next < range.end;
+        if (more) npos = locate(next);
+        lookup(npos);
+        grad_kloop<8, kStores + kLook>(nst, lds0, lds1, acc, read, issue);
         __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         int elane = lane;
@@ -326,48 +400,36 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
         // lane = row elane / 4 of 16 and 16 of 64 columns; pass (i, hv) covers rows
         // 32 i + 16 hv .. + 15 of the wave's 128
         // (the second half of the passes after the first two: all at once spilled)
-        u32x4_t cg[8], cu[8];
-        uint16_t sc[8];
+        GradKept kept[8];
         float pr0 = 0.0f, pr1 = 0.0f;
         const int quarter = elane & 3, prow = elane >> 2;
         const int ib = n0 / 32 + 2 * wn + (quarter >> 1);        // interleave block of the lane's columns
-        const int ibc = min(ib, g.F / 32 - 1);
-        auto kept = [&](int q) {
-            const int64_t row = row0 + min(128 * wm + 16 * q + prow, rows - 1);
-            const int8_t* cp = g.codes + row * 2 * g.F + 64 * ibc + 16 * (quarter & 1);
-            cg[q] = *(const u32x4_t*)cp;
-            cu[q] = *(const u32x4_t*)(cp + 32);
-            sc[q] = *(const uint16_t*)(g.scales + row * (g.F / 16) + 2 * ibc);
+        auto load_kept = [&](int q) {
+            kept[q] = grad_kept(g, row0 + min(128 * wm + 16 * q + prow, rows - 1), min(ib, g.F / 32 - 1), quarter & 1);
         };
         if constexpr (SWIGLU) {
             const int r0 = min(128 * wm + elane, rows - 1), r1 = min(128 * wm + elane + 64, rows - 1);
             pr0 = g.prob[g.perm_src[row0 + r0]];
             pr1 = g.prob[g.perm_src[row0 + r1]];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) kept(q);
+            for (int q = 0; q < 4; ++q) load_kept(q);
         }
-        TilePos npos = pos;
-        if (more) {
-            npos = locate(next);
-            sources(npos);
-        }
+        sources(npos);
         issue(lds0, 0);
         issue(lds1, min(1, nst - 1));
 
         if constexpr (SWIGLU) {
             const int F = g.F;
-            const bool cols = ib * 32 < F;
             const __amdgpu_buffer_rsrc_t gu = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)(g.dgu + (int64_t)row0 * 2 * F), (short)0, rows * 4 * F, kBigRsrcWord3);
             const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)(g.hp + (int64_t)row0 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
-            const int n_part = (F + 63) / 64;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 if (q == 2) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int n = 4; n < 8; ++n) kept(n);
+                    for (int n = 4; n < 8; ++n) load_kept(n);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 big_half_to_lds(acc[q >> 1], q & 1, ep, elane);
@@ -380,59 +442,253 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
                 }
                 const int wr = 128 * wm + 16 * q + prow;         // row of the tile
                 const float p = lane_value(4 * (16 * (q & 3) + prow), q < 4 ? pr0 : pr1);
-                const float sg = __uint_as_float((uint32_t)(sc[q] & 0xff) << 23);
-                const float su = __uint_as_float((uint32_t)(sc[q] >> 8) << 23);
-                float dot = 0.0f;
                 uint32_t og[8], ou[8], oh[8];
-#pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    float vg[2], vu[2], vh[2];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int sh = 8 * ((m + n) & 3);
-                        const float gate = (float)((int)(cg[q][(m + n) >> 2] << (24 - sh)) >> 24) * sg;
-                        const float up = (float)((int)(cu[q][(m + n) >> 2] << (24 - sh)) >> 24) * su;
-                        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-gate));
-                        const float silu = gate * s;
-                        const float h = silu * up;
-                        const float r = raw[m + n];
-                        dot = __builtin_fmaf(r, h, dot);
-                        const float dh = r * p;
-                        vu[n] = dh * silu;
-                        vg[n] = dh * up * __builtin_fmaf(silu, 1.0f - s, s);
-                        vh[n] = h * p;
-                    }
-                    og[m / 2] = (uint32_t)f32_to_bf16_bits(vg[0]) | ((uint32_t)f32_to_bf16_bits(vg[1]) << 16);
-                    ou[m / 2] = (uint32_t)f32_to_bf16_bits(vu[0]) | ((uint32_t)f32_to_bf16_bits(vu[1]) << 16);
-                    oh[m / 2] = (uint32_t)f32_to_bf16_bits(vh[0]) | ((uint32_t)f32_to_bf16_bits(vh[1]) << 16);
-                }
-                const int og0 = cols ? (wr * 2 * F + 64 * ib + 16 * (quarter & 1)) * 2 : 0x7ffffe00;
-                const int oh0 = cols ? (wr * F + 32 * ib + 16 * (quarter & 1)) * 2 : 0x7ffffe00;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const u32x4_t a = {og[4 * hf], og[4 * hf + 1], og[4 * hf + 2], og[4 * hf + 3]};
-                    const u32x4_t b = {ou[4 * hf], ou[4 * hf + 1], ou[4 * hf + 2], ou[4 * hf + 3]};
-                    const u32x4_t c = {oh[4 * hf], oh[4 * hf + 1], oh[4 * hf + 2], oh[4 * hf + 3]};
-                    __builtin_amdgcn_raw_buffer_store_b128(a, gu, og0 + 16 * hf, 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(b, gu, og0 + 64 + 16 * hf, 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(c, hr, oh0 + 16 * hf, 0, 0);
-                }
-                if (!cols) dot = 0.0f;
+                float dot = grad_swiglu16(raw, kept[q], p, og, ou, oh);
+                grad_swiglu_store(gu, hr, F, wr, ib, quarter & 1, og, ou, oh);
                 dot += __shfl_xor(dot, 1);
-                dot += __shfl_xor(dot, 2);
-                if (quarter == 0 && wr < rows && n0 / 64 + wn < n_part)
-                    g.part[(int64_t)(row0 + wr) * n_part + n0 / 64 + wn] = dot;
+                if (!(quarter & 1) && wr < rows && 32 * ib < F) g.part[(int64_t)(row0 + wr) * (F / 32) + ib] = dot;
             }
         } else {
             const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 2, kBigRsrcWord3);
+                (void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 4, kBigRsrcWord3);
+            const int c = elane & 15;
+            const int col = n0 + 64 * wn + 4 * c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                grad_rows_bf16(acc[i], ep, elane, [&](int, int rr, int c, u32x4_t val) {
-                    const int col = n0 + 64 * wn + 8 * c;
-                    const int off = col < N ? ((128 * wm + 32 * i + rr) * N + col) * 2 : 0x7ffffff0;
+            for (int q = 0; q < 8; ++q) {
+                big_half_to_lds(acc[q >> 1], q & 1, ep, elane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int lr = (elane >> 4) + 4 * k;
+                    const u32x4_t val = *(const u32x4_t*)(ep + lr * 256 + ((16 * c) ^ half_swz(lr)));
+                    const int off = col < N ? ((128 * wm + 16 * q + lr) * N + col) * 4 : 0x7ffffff0;
                     __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
-                });
+                }
+            }
+        }
+        if (!more) {
+            BIG_WAIT_VMCNT(0);          // the repeated loads land before the LDS is released
+            break;
+        }
+        tile = next;
+        pos = npos;
+    }
+}
+
+// The 64-row tiles (experts with at most 128 rows): 64 x 256, 8 waves of 64 x 32, the
+// arithmetic of the 256-row tiles (the same MFMAs in the same order, so a row's results do
+// not depend on the tile that computes them).  The weights stream from memory, each byte for
+// at most 64 rows, so what counts is loads in flight: three LDS stages of 64 along the sum
+// (8 KB of rows, 32 KB of weights), two of them in flight, a barrier a stage.  With the
+// 256-row tiles in their place (three quarters and more of every tile empty) 4,096 tokens on
+// 128 unevenly loaded experts took 858 us for both products instead of GRAD_SMALL_4K.
+// take_big: this launch also takes the 256-row tiles, as four of 64 rows each.
+constexpr int kGradSmallStage = 40 * 1024;
+constexpr int kGradSmallW = 8 * 1024;           // weight part of a stage
+constexpr int kGradSmallLoads = 5;              // direct loads per wave per stage
+
+template <bool SWIGLU>
+__device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_big)
+{
+    __shared__ __attribute__((aligned(1024))) char lds0[kGradSmallStage];
+    __shared__ __attribute__((aligned(1024))) char lds1[kGradSmallStage];
+    __shared__ __attribute__((aligned(1024))) char lds2[kGradSmallStage];
+    __shared__ __attribute__((aligned(1024))) char lds_x[8 * kBigEpi];
+
+    const int lane = threadIdx.x & 63;
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int N = SWIGLU ? g.F : g.H;                    // output columns
+    const int Kc = SWIGLU ? g.H : 2 * g.F;               // the sum
+    const uint16_t* const A = SWIGLU ? g.d_out : g.dgu;
+    const uint16_t* const W = SWIGLU ? g.w2 : g.w1;
+    const int nt16 = Kc / 16, ks = N / 32;
+    const int NT = (N + kBigTN - 1) / kBigTN;
+    const int n_small = ld_const(&g.hdr->n_tiles), n_big = take_big ? ld_const(&g.hdr->n_tiles_big) : 0;
+    const int total = (n_small + 4 * n_big) * NT;
+    const int nst = (Kc + kBigKS - 1) / kBigKS;
+
+    struct TilePos { int e, row0, rows, n0; };
+    auto locate = [&](int tile) {
+        const int mt = tile / NT;
+        const bool big = mt >= n_small;
+        const int2* te = big ? g.tiles_big + ((mt - n_small) >> 2) : g.tiles + mt;
+        const int e = ld_const(&te->x), row0 = ld_const(&te->y) + (big ? kBM * ((mt - n_small) & 3) : 0);
+        return TilePos{e, row0, min(kBM, ld_const(g.offsets + e + 1) - row0), (tile - mt * NT) * kBigTN};
+    };
+    // the next tile with rows (the last quarters of a 256-row tile may have none)
+    auto advance = [&](int tile, TilePos& p) {
+        for (; tile < total; tile += (int)gridDim.x) {
+            p = locate(tile);
+            if (p.rows > 0) break;
+        }
+        return tile;
+    };
+
+    // as in the 256-row tiles: rows 8 wid + lane / 8, the wave's 32-column weight block
+    const char* arow;
+    const char* wbase;
+    int s32, look = 0;
+    const int myrow = 8 * wid + (lane >> 3), achunk = (lane & 7) ^ (lane >> 3);
+    const int wlane = 16 * ((lane & 48) | ((lane & 15) ^ (4 * (lane >> 4))));
+    auto lookup = [&](const TilePos& p) {
+        if constexpr (SWIGLU) look = g.perm_src[p.row0 + min(myrow, p.rows - 1)];
+    };
+    auto sources = [&](const TilePos& p) {
+        int64_t src = p.row0 + min(myrow, p.rows - 1);
+        if constexpr (SWIGLU) {
+            const int tok = look / g.topk;
+            if (p.n0 == 0 && (lane & 7) == 0) g.row_tok[src] = tok;
+            src = tok;
+        }
+        arow = (const char*)(A + src * Kc);
+        wbase = (const char*)(W + (int64_t)p.e * Kc * N) + wlane;
+        s32 = min(p.n0 / 32 + wid, ks - 1);
+    };
+    auto issue = [&](char* st, int s) {
+        const int c = 8 * s + achunk;
+        big_load_block(c < Kc / 8 ? arow + 16 * c : (const char*)grad_zeros, st + wid * 1024);
+        const int grp = s >> 3;
+        const int w = min(32, nt16 - 32 * grp);
+        const char* wp = wbase + ((int64_t)grp * 32 * ks + (int64_t)s32 * w + ((4 * s) & 31)) * 1024;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 4 * s + i < nt16 ? i : i - 2;
+            big_load_block(wp + n * 1024, st + kGradSmallW + (4 * wid + i) * 1024);
+        }
+    };
+    int a_off[4], b_off[2];
+    {
+        const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a_off[q] = r * 128 + 16 * ((2 * q + hi) ^ (r & 7));
+        const int j = lane & 15, q = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            b_off[t] = kGradSmallW + 4 * wid * 1024 + q * 256 + 16 * ((8 * hi + 4 * t + (j >> 2)) ^ (4 * q)) + 8 * (j & 1);
+    }
+
+    TilePos pos{}, npos{};
+    int tile = advance(xcd_first_tile(), pos);
+    if (tile >= total) return;
+    // SWIGLU: 12 stores of the rows (and 2 of partial sums), else 8
+    constexpr int kStores = SWIGLU ? 12 : 8;
+    constexpr int kLook = SWIGLU ? 1 : 0;
+    lookup(pos);
+    sources(pos);
+    issue(lds0, 0);
+    issue(lds1, min(1, nst - 1));
+    grad_dummy_stores<kStores>(g.dgu, lane);
+    char* const ep = lds_x + wid * kBigEpi;
+    while (true) {
+        const int row0 = pos.row0, rows = pos.rows, n0 = pos.n0;
+        npos = pos;
+        const int next = advance(tile + (int)gridDim.x, npos);
+        const bool more = next < total;
+        if (!more) npos = pos;
+        lookup(npos);
+        f32x16 acc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][v] = 0.0f;
+        // stage s is in cur, stage s + 1 in flight; stage s + 2 goes where stage s - 1 was
+        // (past the last stage that one again, which no later read of the tile uses).  AFTER:
+        // what is younger than stage s + 1 and may still be in flight, at stage 0 the stores of
+        // the tile before and this tile's lookup.
+        auto step = [&](auto AC, int s, const char* cur, char* refill) {
+            BIG_WAIT_VMCNT(kGradSmallLoads + decltype(AC)::value);
+            __builtin_amdgcn_s_waitcnt(0xC07F);     // lgkmcnt(0): this wave's reads of stage s - 1 are done
+            __builtin_amdgcn_s_barrier();
+            issue(refill, min(s + 2, nst - 1));
+            bf16x8 a[4][2], b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                b[q] = grad_tr(cur + b_off[0] + q * 1024, b_off[1] - b_off[0]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) a[q][i] = big_frag<OpBf16>(cur + a_off[q] + 4096 * i);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q], acc[i], 0, 0, 0);
+        };
+        using Now = std::integral_constant<int, 0>;
+        step(std::integral_constant<int, kStores + kLook>{}, 0, lds0, lds2);
+        int s = 1;
+        for (; s + 3 <= nst; s += 3) {
+            step(Now{}, s, lds1, lds0);
+            step(Now{}, s + 1, lds2, lds1);
+            step(Now{}, s + 2, lds0, lds2);
+        }
+        if (s < nst) {
+            step(Now{}, s, lds1, lds0);
+            if (s + 1 < nst) step(Now{}, s + 1, lds2, lds1);
+        }
+        // lane = row lane / 2 of 32 and 16 of the wave's 32 columns
+        int elane = lane;
+        asm volatile("" : "+v"(elane));
+        const int half = elane & 1, prow = elane >> 1;
+        const int ib = n0 / 32 + wid;
+        GradKept kept[2];
+        float p[2];
+        if constexpr (SWIGLU) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t row = row0 + min(32 * i + prow, rows - 1);
+                p[i] = g.prob[g.perm_src[row]];
+                kept[i] = grad_kept(g, row, min(ib, g.F / 32 - 1), half);
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();               // every wave has read its last stage
+        sources(npos);
+        issue(lds0, 0);
+        issue(lds1, min(1, nst - 1));
+        __amdgpu_buffer_rsrc_t o0, o1;
+        if constexpr (SWIGLU) {
+            o0 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.dgu + (int64_t)row0 * 2 * g.F), (short)0, rows * 4 * g.F,
+                                                   kBigRsrcWord3);
+            o1 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.hp + (int64_t)row0 * g.F), (short)0, rows * 2 * g.F,
+                                                   kBigRsrcWord3);
+        } else {
+            o0 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 4,
+                                                   kBigRsrcWord3);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // 32 rows x 32 fp32 through the wave's region: row r in slot r ^ ((r / 4) % 2), its
+            // 16-byte chunk c at c ^ ((r / 2) % 4), so that a write's two rows fall in different
+            // halves of the banks and so do the 8 rows that 16 lanes read
+            const int hi = elane >> 5, c32 = elane & 31;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int r = 8 * (v >> 2) + 4 * hi + (v & 3);
+                *(float*)(ep + (r ^ ((r >> 2) & 1)) * 128 + ((4 * c32) ^ (16 * ((r >> 1) & 3)))) = acc[i][v];
+            }
+            float raw[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const f32x4 v = *(const f32x4*)(ep + (prow ^ ((prow >> 2) & 1)) * 128 +
+                                                ((64 * half + 16 * c) ^ (16 * ((prow >> 1) & 3))));
+#pragma unroll
+                for (int m = 0; m < 4; ++m) raw[4 * c + m] = v[m];
+            }
+            const int wr = 32 * i + prow;
+            if constexpr (SWIGLU) {
+                uint32_t og[8], ou[8], oh[8];
+                float dot = grad_swiglu16(raw, kept[i], p[i], og, ou, oh);
+                grad_swiglu_store(o0, o1, g.F, wr, ib, half, og, ou, oh);
+                dot += __shfl_xor(dot, 1);
+                if (half == 0 && wr < rows && 32 * ib < g.F) g.part[(int64_t)(row0 + wr) * (g.F / 32) + ib] = dot;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const u32x4_t val = {__float_as_uint(raw[4 * c]), __float_as_uint(raw[4 * c + 1]),
+                                         __float_as_uint(raw[4 * c + 2]), __float_as_uint(raw[4 * c + 3])};
+                    const int off = 32 * ib < N ? (wr * N + 32 * ib + 16 * half + 4 * c) * 4 : 0x7ffffff0;
+                    __builtin_amdgcn_raw_buffer_store_b128(val, o0, off, 0, 0);
+                }
+            }
         }
         if (!more) {
             BIG_WAIT_VMCNT(0);          // the repeated loads land before the LDS is released
@@ -511,64 +767,77 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     // the last row on the gathered side (so that no value of another row comes in: 0 times
     // a NaN of the expert's own last row is a NaN that this row gives anyway).  An expert
     // without rows reads zeros on both sides, and its sum is left out.
-    const char *ob, *gb;                   // own and gathered matrix
-    int64_t opitch, gpitch;                // bytes a row
-    int ocol[2], gcol[2];                  // the lane's column, bytes: rows r % 4 = 0, 1 and 2, 3
+    // The addresses are kept so that a stage costs few instructions (computed anew from the
+    // row and its token each stage they were 4.6 vector instructions per MFMA): the own
+    // rows' pointers advance by 64 rows, a gathered row is one multiply-add of its token,
+    // read a stage ahead from the table that the first product left.
     int cnt = 0, oslot = 0, gslot = 0;     // rows; where own and gathered rows lie in a stage
-    int64_t orow0 = 0;
-    int idx = 0;                           // lane l: route of row 8 w + l % 8 of the next stage to issue
-    auto route = [&](const TilePos& p, int s) {
-        const int r = p.row0 + min(64 * s + 8 * wid + (lane & 7), p.cnt - 1);
-        return g.perm_src[p.cnt > 0 ? r : 0];
+    const int half = lane >> 5;
+    const int row8 = 8 * wid + half;       // load i: row row8 + 2 i of the stage
+    const char* own[4];                    // own rows of the next stage to issue, at the lane's column
+    const char* gcol[2];                   // gathered matrix at the lane's column: rows r % 4 = 0, 1 and 2, 3
+    uint32_t ostep = 0, gpitch = 0;        // bytes of 64 own rows, of a gathered row
+    const int32_t* toks = nullptr;         // the expert's part of the token table
+    int tok[4];                            // tokens of the next stage to issue
+    auto tokens = [&](const int32_t* table, int n, int s, int (&t)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = table[max(0, min(64 * s + row8 + 2 * i, n - 1))];
     };
+    // (an expert without rows: entry 0 of the table, whatever it holds, with a pitch of 0)
+    auto table_of = [&](const TilePos& p) { return g.row_tok + (p.cnt > 0 ? p.row0 : 0); };
     auto sources = [&](const TilePos& p) {
         const int ow = p.w2 ? F : 2 * F;                         // columns of the own matrix
         const int o0 = p.w2 ? p.n0 : p.m0, g0 = p.w2 ? p.m0 : p.n0;
-        const uint16_t* own = p.w2 ? g.hp : g.dgu;
+        const uint16_t* ob = p.w2 ? g.hp : g.dgu;
+        const uint16_t* gb = p.w2 ? g.d_out : g.x;
         cnt = p.cnt;
-        orow0 = p.row0;
         oslot = p.w2 ? kBigWOff : 0;
         gslot = p.w2 ? 0 : kBigWOff;
-        opitch = 2 * (int64_t)ow;
-        gpitch = 2 * (int64_t)H;
-        ob = (const char*)own;
-        gb = (const char*)(p.w2 ? g.d_out : g.x);
+        ostep = 128u * (uint32_t)ow;
+        gpitch = p.cnt > 0 ? 2u * (uint32_t)H : 0u;
+        toks = table_of(p);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             // the slot's chunk; a column past the matrix reads its last chunk (never stored)
-            const int c = 8 * ((lane & 31) ^ (4 * (2 * h + (lane >> 5))));
-            ocol[h] = 2 * min(o0 + c, ow - 8);
-            gcol[h] = 2 * min(g0 + c, H - 8);
-        }
-        if (p.cnt == 0) {
-            gb = (const char*)grad_zeros;
-            gpitch = 0;
-            gcol[0] = gcol[1] = 0;
+            const int c = 8 * ((lane & 31) ^ (4 * (2 * h + half)));
+            gcol[h] = p.cnt > 0 ? (const char*)(gb + min(g0 + c, H - 8)) : (const char*)grad_zeros;
+            const uint16_t* o = ob + min(o0 + c, ow - 8);
+#pragma unroll
+            for (int i = h; i < 4; i += 2) own[i] = (const char*)(o + ((int64_t)p.row0 + row8 + 2 * i) * ow);
         }
     };
-    auto issue_rows = [&](char* st, int s, int rt) {
-        const int tok = cnt > 0 ? rt / g.topk : 0;       // (an expert without rows: any value was read)
+    auto issue_rows = [&](char* st, int s, const int (&t)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 64 * s + 8 * wid + 2 * i + (lane >> 5);
-            const int t0 = __builtin_amdgcn_readlane(tok, 2 * i), t1r = __builtin_amdgcn_readlane(tok, 2 * i + 1);
-            const int64_t grow = lane < 32 ? t0 : t1r;
-            big_load_block(r < cnt ? ob + (orow0 + r) * opitch + ocol[i & 1] : (const char*)grad_zeros, st + oslot + (4 * wid + i) * 1024);
-            big_load_block(gb + grow * gpitch + gcol[i & 1], st + gslot + (4 * wid + i) * 1024);
+            big_load_block(64 * s + row8 + 2 * i < cnt ? own[i] : (const char*)grad_zeros,
+                           st + oslot + (4 * wid + i) * 1024);
+            own[i] += ostep;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            big_load_block(gcol[i & 1] + (uint64_t)(uint32_t)t[i] * gpitch, st + gslot + (4 * wid + i) * 1024);
     };
     TilePos pos, npos;
-    auto issue = [&](char* st, int s) {
-        issue_rows(st, s, idx);
-        idx = route(pos, s + 1);
+    // (past the last stage: rows past the expert's last, so zeros and the last row again)
+    int next_stage = 0;
+    auto issue = [&](char* st, int) {
+        issue_rows(st, next_stage, tok);
+        tokens(toks, cnt, ++next_stage, tok);
     };
-    // the first two stages of a tile and the routes of its third
+    // the tokens of a tile's first two stages, loaded before the K loop of the tile before it,
+    // then those stages and the tokens of the third
+    int tok0[4], tok1[4];
+    auto lookup = [&](const TilePos& p) {
+        const int32_t* table = table_of(p);
+        tokens(table, p.cnt, 0, tok0);
+        tokens(table, p.cnt, 1, tok1);
+    };
     auto start = [&](const TilePos& p) {
-        const int i0 = route(p, 0), i1 = route(p, 1);
         sources(p);
-        issue_rows(lds0, 0, i0);
-        issue_rows(lds1, 1, i1);
-        idx = route(p, 2);
+        issue_rows(lds0, 0, tok0);
+        issue_rows(lds1, 1, tok1);
+        tokens(toks, cnt, 2, tok);
+        next_stage = 2;
     };
     // fragments of sub-step Q: rows 16 Q + 8 (l / 32) + {0, 4} + (l % 16) / 4, the lane's 4
     // columns of each 32-column block
@@ -593,9 +862,11 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     const int end = grad_part(g.offsets, g.E, per_e, xcd + 1, lane);
     int tile = grad_part(g.offsets, g.E, per_e, xcd, lane) + (int)(blockIdx.x >> 3);
     if (tile >= end) return;
-    pos = locate(tile);
+    pos = npos = locate(tile);
+    lookup(pos);
     start(pos);
     constexpr int kStores = FP32 ? 32 : 16;
+    constexpr int kLook = 8;                    // the next tile's lookup
     grad_dummy_stores<kStores>(g.dgu, lane);
     char* const ep = lds_x + wid * kBigEpi;
     while (true) {
@@ -606,15 +877,14 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-        if (pos.cnt > 0) grad_kloop<12, kStores>((pos.cnt + 63) / 64, lds0, lds1, acc, read, issue);
-        else BIG_WAIT_VMCNT(kStores);               // its loads land before the next tile's go out
-
         const int next = tile + (int)(gridDim.x >> 3);
         const bool more = next < end;
+        if (more) npos = locate(next);
+        lookup(npos);
+        if (pos.cnt > 0) grad_kloop<12, kStores + kLook>((pos.cnt + 63) / 64, lds0, lds1, acc, read, issue);
+        else BIG_WAIT_VMCNT(kStores + kLook);       // its loads land before the next tile's go out
         __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
-        npos = pos;
-        if (more) npos = locate(next);
         start(npos);
 
         int elane = lane;

@@ -10,18 +10,27 @@ __global__ void __launch_bounds__(512, 1) grad_rows_kernel(GradArgs g)
     grad_rows_tiles<SWIGLU>(g);
 }
 
+template <bool SWIGLU>
+__global__ void __launch_bounds__(512, 1) grad_small_kernel(GradArgs g, int take_big)
+{
+    grad_small_tiles<SWIGLU>(g, take_big != 0);
+}
+
 template <bool FP32>
 __global__ void __launch_bounds__(512, 1) grad_weight_kernel(GradArgs g)
 {
     grad_weight_tiles<FP32>(g);
 }
 
-hipError_t launch_grad_gemms(const GradArgs& g, bool fp32, int num_cu, hipStream_t s)
+hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int num_cu, hipStream_t s)
 {
     // a multiple of 8 workgroups: the tiles are split over the 8 XCDs
     const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
-    hipLaunchKernelGGL(grad_rows_kernel<true>, grid, block, 0, s, g);
-    hipLaunchKernelGGL(grad_rows_kernel<false>, grid, block, 0, s, g);
+    const int take_big = T_cap <= 1024;
+    if (!take_big) hipLaunchKernelGGL(grad_rows_kernel<true>, grid, block, 0, s, g);
+    hipLaunchKernelGGL(grad_small_kernel<true>, grid, block, 0, s, g, take_big);
+    if (!take_big) hipLaunchKernelGGL(grad_rows_kernel<false>, grid, block, 0, s, g);
+    hipLaunchKernelGGL(grad_small_kernel<false>, grid, block, 0, s, g, take_big);
     if (fp32) hipLaunchKernelGGL(grad_weight_kernel<true>, grid, block, 0, s, g);
     else hipLaunchKernelGGL(grad_weight_kernel<false>, grid, block, 0, s, g);
     return hipGetLastError();

@@ -65,7 +65,7 @@ hipError_t launch_quant_x(const uint16_t* x, int64_t T_cap, const int32_t* live,
 #include "grad_args.h"
 
 namespace moe {
-hipError_t launch_grad_gemms(const GradArgs& g, bool fp32, int num_cu, hipStream_t s);
+hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int num_cu, hipStream_t s);
 hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
                             hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
@@ -197,8 +197,9 @@ struct BackwardLayout {
     WsLayout prep;
     size_t dgu;            // bf16 [R][2F]: gradient of gate and up
     size_t hp;             // bf16 [R][F]: SwiGLU rows times their probability
-    size_t dx;             // bf16 [R][H]: gradient of the grouped rows of x
-    size_t part;           // fp32 [R][ceil(F / 64)]: partial sums of the probabilities' gradient
+    size_t dx;             // fp32 [R][H]: gradient of the grouped rows of x
+    size_t part;           // fp32 [R][F / 32]: partial sums of the probabilities' gradient
+    size_t row_tok;        // int32 [R]: token of each grouped row
     size_t d_out;          // bf16 [T_cap][H]: d_out rounded, where it is given in fp32
     size_t total;
 };
@@ -211,8 +212,9 @@ static BackwardLayout backward_layout(const moe_ctx* h, int64_t T_cap)
     auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes > 0 ? bytes : 1); return at; };
     B.dgu = take(4 * R * F);
     B.hp = take(2 * R * F);
-    B.dx = take(2 * R * H);
-    B.part = take(4 * R * ((F + 63) / 64));
+    B.dx = take(4 * R * H);
+    B.part = take(R * F / 8);
+    B.row_tok = take(4 * R);
     B.d_out = take(2 * T_cap * H);
     B.total = o;
     return B;
@@ -992,17 +994,18 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     g.scales = scales;
     g.dgu = (uint16_t*)(w + B.dgu);
     g.hp = (uint16_t*)(w + B.hp);
-    g.dx = (uint16_t*)(w + B.dx);
+    g.dx = (float*)(w + B.dx);
     g.part = (float*)(w + B.part);
+    g.row_tok = (int32_t*)(w + B.row_tok);
     g.d_w1 = d_w1;
     g.d_w2 = d_w2;
-    e = launch_grad_gemms(g, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
+    e = launch_grad_gemms(g, T_cap, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: product launch");
     if (T_cap == 0) return MOE_OK;
-    e = launch_combine(g.dx, 1, (const int32_t*)(w + L.dst), nullptr, live_rows_dev, T_cap, h->k, h->H, d_x, 1,
+    e = launch_combine(g.dx, 0, (const int32_t*)(w + L.dst), nullptr, live_rows_dev, T_cap, h->k, h->H, d_x, 1,
                        h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: d_x launch");
-    e = launch_grad_probs(g.part, (h->F + 63) / 64, expert_ids, (const int32_t*)(w + L.dst), live_rows_dev, T_cap,
+    e = launch_grad_probs(g.part, h->F / 32, expert_ids, (const int32_t*)(w + L.dst), live_rows_dev, T_cap,
                           h->k, d_probs, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: d_probs launch");
     return MOE_OK;
