@@ -39,19 +39,6 @@ __device__ __forceinline__ uint32_t ckpt_code(float v, float factor)
     return __float_as_uint(__builtin_fmaf(v, factor, 12582912.0f));
 }
 
-// Largest value over the 32 lanes of a half wave: rotations by 1, 2, 4, 8 inside rows of
-// 16 lanes, then the two rows of the half
-__device__ __forceinline__ uint32_t half_max_u32(uint32_t x)
-{
-#define CKPT_ROR(n) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + (n), 0xf, 0xf, false))
-    CKPT_ROR(1);
-    CKPT_ROR(2);
-    CKPT_ROR(4);
-    CKPT_ROR(8);
-#undef CKPT_ROR
-    return max(x, (uint32_t)__shfl_xor((int)x, 16));
-}
-
 // The larger of this lane's value and its neighbour's (lane ^ 1)
 __device__ __forceinline__ uint32_t pair_max_u32(uint32_t x)
 {

@@ -324,8 +324,47 @@ __device__ __forceinline__ void big_half_to_lds(const Acc (&acc)[2], int hv, cha
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             const int lr = 8 * (w >> 2) + 4 * hi + (w & 3);
-            *(float*)(ep + lr * 256 + ((128 * j + 4 * c32) ^ half_swz(lr))) = acc[j][8 * hv + w];
+            // (an opaque offset, as in the FC1 epilogue: with its constant part folded into the
+            // instruction the compiler waited for the next tile's direct loads first)
+            int ea = lr * 256 + ((128 * j + 4 * c32) ^ half_swz(lr));
+            asm volatile("" : "+v"(ea));
+            *(float*)(ep + ea) = acc[j][8 * hv + w];
         }
+}
+
+// Quantizes and stores the 16 rows x 64 columns of interleave block ib that big_half_to_lds
+// left in ep: a lane takes 16 neighbouring columns (half a block of 32; the other half is
+// the next lane's) of row row0 + lane / 4 of the tile.  cr, sr: codes [rows][2F] and scales
+// [rows][F / 16] of the tile's rows; what lies past them is dropped.
+__device__ __forceinline__ void ckpt_store_half(const char* ep, int lane, __amdgpu_buffer_rsrc_t cr,
+                                                __amdgpu_buffer_rsrc_t sr, int row0, int F, int ib)
+{
+    const int prow = lane >> 2, quarter = lane & 3;
+    float v[16];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const f32x4 u = *(const f32x4*)(ep + prow * 256 + ((64 * quarter + 16 * q) ^ half_swz(prow)));
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            v[4 * q + n] = u[n];
+            amax = max(amax, __float_as_uint(u[n]) & 0x7fffffffu);
+        }
+    }
+    const uint32_t byte = ckpt_byte(pair_max_u32(amax));
+    const float f = ckpt_factor(byte);
+    const uint32_t mask = byte == 255u ? 0u : 0xffu;
+    u32x4_t w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        w[q] = (ckpt_code(v[4 * q], f) & mask) | (ckpt_code(v[4 * q + 1], f) & mask) << 8 |
+               (ckpt_code(v[4 * q + 2], f) & mask) << 16 | (ckpt_code(v[4 * q + 3], f) & mask) << 24;
+    const int row = row0 + prow;
+    const bool cols = 32 * ib < F;
+    __builtin_amdgcn_raw_buffer_store_b128(w, cr, cols ? row * 2 * F + 64 * ib + 16 * quarter : 0x7ffffff0, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, sr,
+                                         cols && !(quarter & 1) ? row * (F / 16) + 2 * ib + (quarter >> 1) : 0x7ffffff0,
+                                         0, 0);
 }
 
 // FC1 with a checkpoint: 16-byte stores and scale bytes beyond big_stores
@@ -543,36 +582,11 @@ __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
                         (void*)(g.ck_codes + (int64_t)row0 * 2 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
                     const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
                         (void*)(g.ck_scales + (int64_t)row0 * (F / 16)), (short)0, rows * (F / 16), kBigRsrcWord3);
-                    const int prow = elane >> 2, quarter = elane & 3;
                     static_assert(kCkptStores == 4 * 2 * 2, "4 row blocks x 2 halves x (codes, scales)");
 #pragma unroll
                     for (int hv = 0; hv < 2; ++hv) {
                         big_half_to_lds(acc[i], hv, ep, elane);
-                        float v16[16];
-                        uint32_t amax = 0;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const f32x4 v = *(const f32x4*)(ep + prow * 256 + ((64 * quarter + 16 * q) ^ half_swz(prow)));
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                v16[4 * q + n] = v[n];
-                                amax = max(amax, __float_as_uint(v[n]) & 0x7fffffffu);
-                            }
-                        }
-                        const uint32_t byte = ckpt_byte(pair_max_u32(amax));
-                        const float f = ckpt_factor(byte);
-                        const uint32_t mask = byte == 255u ? 0u : 0xffu;
-                        u32x4_t w;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = (ckpt_code(v16[4 * q], f) & mask) | (ckpt_code(v16[4 * q + 1], f) & mask) << 8 |
-                                   (ckpt_code(v16[4 * q + 2], f) & mask) << 16 |
-                                   (ckpt_code(v16[4 * q + 3], f) & mask) << 24;
-                        const int tr = 128 * wm + 32 * i + 16 * hv + prow;
-                        const int off = cols ? tr * 2 * F + 64 * ib + 16 * quarter : 0x7ffffff0;
-                        __builtin_amdgcn_raw_buffer_store_b128(w, cr, off, 0, 0);
-                        const int soff = cols && !(quarter & 1) ? tr * (F / 16) + 2 * ib + (quarter >> 1) : 0x7ffffff0;
-                        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, sr, soff, 0, 0);
+                        ckpt_store_half(ep, elane, cr, sr, 128 * wm + 32 * i + 16 * hv, F, ib);
                     }
                 }
             }

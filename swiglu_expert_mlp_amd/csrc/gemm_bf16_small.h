@@ -246,8 +246,11 @@ __device__ __forceinline__ void small_finalize(const GemmArgs& g, SmallFinLds* f
 // WPOL: the cache policy of the weight stream (kNonTemporal when every
 // expert's rows fit one 64-row tile, else the default; the caller reads which
 // from the header).
-// CKPT: FC1 also stores its gate and up values in 8 bits (checkpoint.h); the 32 lanes of a
-// half wave hold one row's block.
+// CKPT: FC1 also stores its gate and up values in 8 bits (ckpt_store_half), through the ring
+// stage after the last one: whoever is past the K loop has passed the last step's barrier,
+// so every wave's reads of that stage are done.  (Quantized in place instead, the 32 lanes of
+// a half wave reducing each row's block and storing a byte each, the 64-row FC1 of 4,096
+// tokens on 128 unevenly loaded experts took 480 us beside the 256-row one, 942 a forward.)
 template <typename Op, bool FC1, bool PROB, int FUSE, int WPOL, bool CKPT = false>
 __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n_small, int n_big,
                                             int e0, int row00, int need = 0, SmallFinLds* fin_lds = nullptr)
@@ -432,25 +435,27 @@ __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n
             // column block 0 is the gate half, 1 the up half of interleave block cb
             const int F = g.N / 2;
             uint16_t* hb = (uint16_t*)g.out;
+            if constexpr (CKPT) {
+                char* const ep = smem + (nsteps % kSmallRing) * kSmallStage + wid * kBigEpi;
+                static_assert(8 * kBigEpi <= kSmallStage, "the waves' regions fit one stage");
+                const __amdgpu_buffer_rsrc_t cr = __builtin_amdgcn_make_buffer_rsrc(
+                    (void*)(g.ck_codes + (int64_t)row0 * 2 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
+                const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+                    (void*)(g.ck_scales + (int64_t)row0 * (F / 16)), (short)0, rows * (F / 16), kBigRsrcWord3);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int hv = 0; hv < 2; ++hv) {
+                        big_half_to_lds(acc[i], hv, ep, lane);
+                        ckpt_store_half(ep, lane, cr, sr, 32 * i + 16 * hv, F, cb);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int r = 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
                     const float rv = Op::kScaled ? lane_value(4 * r, rs) : 1.0f;
-                    if constexpr (CKPT) {
-                        const float val[2] = {acc[i][0][v], acc[i][1][v]};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            // (every lane takes part in the maximum, whatever its row)
-                            const uint32_t byte = ckpt_byte(half_max_u32(__float_as_uint(val[j]) & 0x7fffffffu));
-                            const uint32_t code = byte == 255u ? 0u : ckpt_code(val[j], ckpt_factor(byte));
-                            if (i < nb && r < rows) {
-                                g.ck_codes[(int64_t)(row0 + r) * 2 * F + 64 * cb + 32 * j + c32] = (int8_t)code;
-                                if (c32 == 0) g.ck_scales[(int64_t)(row0 + r) * (F / 16) + 2 * cb + j] = (uint8_t)byte;
-                            }
-                        }
-                    }
                     if (i < nb && r < rows) {
                         const float pr = PROB ? fc1_row_prob(g.row_prob, g.perm_src, row0 + r) : 1.0f;
                         hb[(int64_t)(row0 + r) * F + cb * 32 + c32] =

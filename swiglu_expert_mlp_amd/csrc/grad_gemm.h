@@ -259,6 +259,16 @@ __device__ __forceinline__ void grad_swiglu_store(__amdgpu_buffer_rsrc_t gu, __a
     }
 }
 
+// The first column tile of the SWIGLU product leaves the token of every row for the weight
+// products: 8 lanes hold a row's, the first stores it (a store for all, which the descriptor
+// drops for the others and for rows past `rows`: no branch among the loads in flight)
+__device__ __forceinline__ void grad_leave_token(const GradArgs& g, int row0, int rows, int r, int tok, int lane)
+{
+    const __amdgpu_buffer_rsrc_t d =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(g.row_tok + row0), (short)0, 4 * rows, kBigRsrcWord3);
+    __builtin_amdgcn_raw_buffer_store_b32((uint32_t)tok, d, (lane & 7) == 0 ? 4 * r : 0x7ffffff0, 0, 0);
+}
+
 // dx: fp32 rows (rounded to bf16 they would add a third rounding to d_x's two)
 constexpr int grad_rows_stores(bool swiglu) { return swiglu ? 48 : 32; }
 
@@ -314,11 +324,11 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     auto sources = [&](const TilePos& p) {
 #pragma unroll
         for (int i = 0; i < kBigALoads; ++i) {
-            int64_t src = p.row0 + min(32 * wid + 8 * i + (lane >> 3), p.rows - 1);
+            const int rr = 32 * wid + 8 * i + (lane >> 3);
+            int64_t src = p.row0 + min(rr, p.rows - 1);
             if constexpr (SWIGLU) {
-                // the first column tile leaves the token of every row for the weight products
                 const int tok = look[i] / g.topk;
-                if (p.n0 == 0 && (lane & 7) == 0) g.row_tok[src] = tok;
+                grad_leave_token(g, p.row0, p.n0 == 0 ? p.rows : 0, rr, tok, lane);
                 src = tok;
             }
             arow[i] = (const char*)(A + src * Kc);
@@ -536,7 +546,7 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
         int64_t src = p.row0 + min(myrow, p.rows - 1);
         if constexpr (SWIGLU) {
             const int tok = look / g.topk;
-            if (p.n0 == 0 && (lane & 7) == 0) g.row_tok[src] = tok;
+            grad_leave_token(g, p.row0, p.n0 == 0 ? p.rows : 0, myrow, tok, lane);
             src = tok;
         }
         arow = (const char*)(A + src * Kc);

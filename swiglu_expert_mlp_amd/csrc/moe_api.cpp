@@ -53,8 +53,9 @@ hipError_t launch_combine(const void* rows, int in_bf16, const int32_t* row_of, 
 hipError_t launch_combine_backward(const void* d_out, int out_bf16, const void* rows, int rows_bf16,
                                    const int32_t* row_of, const float* probs, const int32_t* live, int64_t T_cap,
                                    int k, int H, void* d_rows, float* d_probs, int num_cu, hipStream_t s);
-hipError_t launch_grad_probs(const float* part, int n_part, const int32_t* ids, const int32_t* dst,
-                             const int32_t* live, int64_t T_cap, int k, float* d_probs, int num_cu, hipStream_t s);
+hipError_t launch_grad_ends(const float* rows, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
+                            const int32_t* live, int64_t T_cap, int k, int H, void* d_x, float* d_probs, int num_cu,
+                            hipStream_t s);
 hipError_t launch_cast_rows(const float* in, const int32_t* live, int64_t T_cap, int H, uint16_t* out, int num_cu,
                             hipStream_t s);
 hipError_t launch_quant_x(const uint16_t* x, int64_t T_cap, const int32_t* live, int H,
@@ -1002,12 +1003,9 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     e = launch_grad_gemms(g, T_cap, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: product launch");
     if (T_cap == 0) return MOE_OK;
-    e = launch_combine(g.dx, 0, (const int32_t*)(w + L.dst), nullptr, live_rows_dev, T_cap, h->k, h->H, d_x, 1,
-                       h->num_cu, stream);
+    e = launch_grad_ends(g.dx, (const int32_t*)(w + L.dst), g.part, h->F / 32, expert_ids, live_rows_dev, T_cap, h->k,
+                         h->H, d_x, d_probs, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: d_x launch");
-    e = launch_grad_probs(g.part, h->F / 32, expert_ids, (const int32_t*)(w + L.dst), live_rows_dev, T_cap,
-                          h->k, d_probs, h->num_cu, stream);
-    if (e != hipSuccess) return hip_fail(e, "moe_backward: d_probs launch");
     return MOE_OK;
 }
 

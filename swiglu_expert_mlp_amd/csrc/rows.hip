@@ -9,13 +9,12 @@
 //                      d_probs[t][j] = sum over columns of d_out[t] rows[row_of[t][j]]
 // row_of outside [0, T_cap k): a route without a row adds nothing and has a gradient of 0.
 //
-// Bound by memory: every row is touched once.  A thread takes 8 neighbouring columns of a
-// token (16 bytes of bf16) with all k rows' accesses in flight at once.
+// Bound by memory: every row is touched once.  A thread takes 16 bytes of neighbouring
+// columns of a token's rows, with all k rows' accesses in flight at once.
 #include "common.h"
 
 namespace moe {
 
-typedef float f4v __attribute__((ext_vector_type(4)));
 typedef unsigned u4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ int64_t rows_live(const int32_t* live_ptr, int64_t T_cap)
@@ -24,55 +23,71 @@ __device__ __forceinline__ int64_t rows_live(const int32_t* live_ptr, int64_t T_
     return live < 0 ? 0 : (live > T_cap ? T_cap : live);
 }
 
-// 8 neighbouring columns of a row, fp32 or bf16 in memory
-template <bool BF16>
-struct Row8;
-template <>
-struct Row8<true> {
-    u4v v;
-    __device__ __forceinline__ void load(const void* base, int64_t at) { v = __builtin_nontemporal_load((const u4v*)((const uint16_t*)base + at)); }
-    __device__ __forceinline__ void get(float (&f)[8]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(v[i] << 16);
-            f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-        }
-    }
-    __device__ __forceinline__ void zero() { v = u4v{0u, 0u, 0u, 0u}; }
-    __device__ __forceinline__ void set(const float (&f)[8])
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = (uint32_t)f32_to_bf16_bits(f[2 * i]) | ((uint32_t)f32_to_bf16_bits(f[2 * i + 1]) << 16);
-    }
-    __device__ __forceinline__ void store(void* base, int64_t at) const { __builtin_nontemporal_store(v, (u4v*)((uint16_t*)base + at)); }
-};
-template <>
-struct Row8<false> {
-    f4v a, b;
+// N neighbouring columns of a row, fp32 or bf16 in memory.  Each is touched once:
+// non-temporal accesses (as in the forward's combine).
+typedef unsigned u2v __attribute__((ext_vector_type(2)));
+template <bool BF16, int N>
+struct RowN {
+    static constexpr int kWords = BF16 ? N / 2 : N;              // 32-bit words
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const void* base, int64_t at)
     {
-        a = __builtin_nontemporal_load((const f4v*)((const float*)base + at));
-        b = __builtin_nontemporal_load((const f4v*)((const float*)base + at) + 1);
-    }
-    __device__ __forceinline__ void get(float (&f)[8]) const
-    {
+        const char* p = (const char*)base + at * (BF16 ? 2 : 4);
+        if constexpr (kWords >= 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { f[i] = a[i]; f[4 + i] = b[i]; }
-    }
-    __device__ __forceinline__ void zero() { a = b = f4v{0.f, 0.f, 0.f, 0.f}; }
-    __device__ __forceinline__ void set(const float (&f)[8])
-    {
+            for (int i = 0; i < kWords / 4; ++i) {
+                const u4v v = __builtin_nontemporal_load((const u4v*)p + i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { a[i] = f[i]; b[i] = f[4 + i]; }
+                for (int n = 0; n < 4; ++n) w[4 * i + n] = v[n];
+            }
+        } else {
+            const u2v v = __builtin_nontemporal_load((const u2v*)p);
+            w[0] = v[0];
+            w[1] = v[1];
+        }
     }
     __device__ __forceinline__ void store(void* base, int64_t at) const
     {
-        __builtin_nontemporal_store(a, (f4v*)((float*)base + at));
-        __builtin_nontemporal_store(b, (f4v*)((float*)base + at) + 1);
+        char* p = (char*)base + at * (BF16 ? 2 : 4);
+        if constexpr (kWords >= 4) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                __builtin_nontemporal_store(u4v{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]}, (u4v*)p + i);
+        } else {
+            __builtin_nontemporal_store(u2v{w[0], w[1]}, (u2v*)p);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if constexpr (BF16) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                f[i] = __uint_as_float(w[i]);
+            }
+    }
+    __device__ __forceinline__ void set(const float (&f)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if constexpr (BF16)
+                w[i] = (uint32_t)f32_to_bf16_bits(f[2 * i]) | ((uint32_t)f32_to_bf16_bits(f[2 * i + 1]) << 16);
+            else
+                w[i] = __float_as_uint(f[i]);
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
 };
+
+// Columns of a thread: 16 bytes of the rows (with 32 bytes of fp32 a wave's instruction
+// took every other 16 bytes: the 16K-token sum of fp32 rows 241 us instead of COMBINE_16K)
+template <bool BF16>
+constexpr int row_cols() { return BF16 ? 8 : 4; }
 
 // ---------------------------------------------------------------- dispatch
 
@@ -93,20 +108,21 @@ template <int K, bool BF16>
 __global__ void __launch_bounds__(256) dispatch_kernel(DispatchArgs a)
 {
     const int64_t T = rows_live(a.live, a.T_cap);
-    const int nc = a.H / 8;
+    constexpr int N = row_cols<BF16>();
+    const int nc = a.H / N;
     const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t e = i0; e <= a.E; e += step) a.offsets_out[e] = a.offsets[e];
     for (int64_t i = i0; i < T * nc; i += step) {
         const int64_t t = i / nc;
         const int c = (int)(i - t * nc);
-        Row8<BF16> v;
-        v.load(a.x, t * a.H + 8 * c);
+        RowN<BF16, N> v;
+        v.load(a.x, t * a.H + N * c);
         int d[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) d[j] = a.dst[t * K + j];
 #pragma unroll
         for (int j = 0; j < K; ++j)
-            if (d[j] >= 0) v.store(a.rows, (int64_t)d[j] * a.H + 8 * c);
+            if (d[j] >= 0) v.store(a.rows, (int64_t)d[j] * a.H + N * c);
         if (c == 0) {
             // the canonical order is a stable sort by id: a route's place is its id's rank
             int id[K];
@@ -153,12 +169,14 @@ __device__ __forceinline__ void rows_sort(uint32_t (&d)[K], float (&p)[K])
         }
 }
 
+// The tokens' columns of workgroup `block` of `blocks`
 template <int K, bool IN_BF16, bool OUT_BF16>
-__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a)
+__device__ __forceinline__ void combine_tokens(const CombineArgs& a, int block, int blocks)
 {
     const int64_t T = rows_live(a.live, a.T_cap);
-    const int nc = a.H / 8;
-    const int64_t i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    constexpr int N = row_cols<IN_BF16>();
+    const int nc = a.H / N;
+    const int64_t i0 = (int64_t)block * blockDim.x + threadIdx.x, step = (int64_t)blocks * blockDim.x;
     for (int64_t i = i0; i < T * nc; i += step) {
         const int64_t t = i / nc;
         const int c = (int)(i - t * nc);
@@ -171,24 +189,30 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a)
             p[j] = a.probs ? a.probs[t * K + j] : 1.0f;
         }
         rows_sort<K>(d, p);
-        Row8<IN_BF16> v[K];
+        RowN<IN_BF16, N> v[K];
 #pragma unroll
         for (int j = 0; j < K; ++j)
-            if (d[j] != 0xffffffffu) v[j].load(a.rows, (int64_t)d[j] * a.H + 8 * c);
+            if (d[j] != 0xffffffffu) v[j].load(a.rows, (int64_t)d[j] * a.H + N * c);
             else v[j].zero();
-        float acc[8] = {};
+        float acc[N] = {};
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             if (d[j] == 0xffffffffu) continue;
-            float f[8];
+            float f[N];
             v[j].get(f);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) acc[n] = __builtin_fmaf(p[j], f[n], acc[n]);
+            for (int n = 0; n < N; ++n) acc[n] = __builtin_fmaf(p[j], f[n], acc[n]);
         }
-        Row8<OUT_BF16> o;
+        RowN<OUT_BF16, N> o;
         o.set(acc);
-        o.store(a.out, t * a.H + 8 * c);
+        o.store(a.out, t * a.H + N * c);
     }
+}
+
+template <int K, bool IN_BF16, bool OUT_BF16>
+__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a)
+{
+    combine_tokens<K, IN_BF16, OUT_BF16>(a, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- combine backward
@@ -210,7 +234,8 @@ template <int K, bool ROWS_BF16, bool OUT_BF16, bool PROBS>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(CombineBwdArgs a)
 {
     const int64_t T = rows_live(a.live, a.T_cap);
-    const int nc = a.H / 8, lane = threadIdx.x & 63;
+    constexpr int N = row_cols<ROWS_BF16>();
+    const int nc = a.H / N, lane = threadIdx.x & 63;
     const int64_t waves = (int64_t)gridDim.x * (blockDim.x >> 6);
     for (int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6); t < T; t += waves) {
         int32_t d[K];
@@ -223,31 +248,31 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(CombineBwdArgs a)
             dot[j] = 0.0f;
         }
         for (int c = lane; c < nc; c += 64) {
-            Row8<OUT_BF16> g;
-            g.load(a.d_out, t * a.H + 8 * c);
-            Row8<ROWS_BF16> v[K];
+            RowN<OUT_BF16, N> g;
+            g.load(a.d_out, t * a.H + N * c);
+            RowN<ROWS_BF16, N> v[K];
             if constexpr (PROBS) {
 #pragma unroll
                 for (int j = 0; j < K; ++j)
-                    if (d[j] >= 0) v[j].load(a.rows, (int64_t)d[j] * a.H + 8 * c);
+                    if (d[j] >= 0) v[j].load(a.rows, (int64_t)d[j] * a.H + N * c);
                     else v[j].zero();
             }
-            float gf[8];
+            float gf[N];
             g.get(gf);
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 if (d[j] < 0) continue;
-                float f[8];
+                float f[N];
                 if constexpr (PROBS) {
                     v[j].get(f);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) dot[j] = __builtin_fmaf(gf[n], f[n], dot[j]);
+                    for (int n = 0; n < N; ++n) dot[j] = __builtin_fmaf(gf[n], f[n], dot[j]);
                 }
 #pragma unroll
-                for (int n = 0; n < 8; ++n) f[n] = p[j] * gf[n];
-                Row8<ROWS_BF16> o;
+                for (int n = 0; n < N; ++n) f[n] = p[j] * gf[n];
+                RowN<ROWS_BF16, N> o;
                 o.set(f);
-                o.store(a.d_rows, (int64_t)d[j] * a.H + 8 * c);
+                o.store(a.d_rows, (int64_t)d[j] * a.H + N * c);
             }
         }
         if constexpr (PROBS) {
@@ -263,26 +288,47 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(CombineBwdArgs a)
 
 // ---------------------------------------------------------------- experts' backward: ends
 
-// d_probs[t][j] of the caller's route j from the partial sums of its row
-__global__ void __launch_bounds__(256) grad_probs_kernel(const float* part, int n_part, const int32_t* ids,
-                                                         const int32_t* dst, const int32_t* live, int64_t T_cap, int k,
-                                                         float* d_probs)
+// d_x from the fp32 rows of its gradient, by the first `blocks_x` workgroups, and
+// d_probs[t][j] of the caller's route j from the n_part partial sums of its row, 8 lanes a
+// route (in the same launch: a launch of its own cost 3 us at 64 tokens, and a thread a route
+// 27 us at 16K tokens)
+struct GradEndsArgs {
+    CombineArgs x;
+    const float* part;
+    int n_part;
+    const int32_t* ids;
+    float* d_probs;
+    int blocks_x;
+};
+
+template <int K>
+__global__ void __launch_bounds__(256) grad_ends_kernel(GradEndsArgs a)
 {
-    const int64_t T = rows_live(live, T_cap);
-    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < T * k; r += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t t = r / k;
-        const int j = (int)(r - t * k);
-        const int id = ids[r];
-        int rank = 0;
-        for (int i = 0; i < k; ++i) {
-            const int o = ids[t * k + i];
+    if ((int)blockIdx.x < a.blocks_x) {
+        combine_tokens<K, false, true>(a.x, blockIdx.x, a.blocks_x);
+        return;
+    }
+    const int64_t T = rows_live(a.x.live, a.x.T_cap);
+    const int sub = threadIdx.x & 7;
+    const int64_t first = (int64_t)(blockIdx.x - a.blocks_x) * 32 + (threadIdx.x >> 3);
+    for (int64_t r = first; r < T * K; r += (int64_t)(gridDim.x - a.blocks_x) * 32) {
+        const int64_t t = r / K;
+        const int j = (int)(r - t * K);
+        const int id = a.ids[r];
+        int rank = 0;                                   // the route's place in the canonical order
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int o = a.ids[t * K + i];
             rank += (o < id || (o == id && i < j)) ? 1 : 0;
         }
-        const int d = dst[t * k + rank];
+        const int d = a.x.row_of[t * K + rank];
         float s = 0.0f;
         if (d >= 0)
-            for (int i = 0; i < n_part; ++i) s += part[(int64_t)d * n_part + i];
-        d_probs[r] = s;
+            for (int i = sub; i < a.n_part; i += 8) s += a.part[(int64_t)d * a.n_part + i];
+        s += __shfl_xor(s, 1);
+        s += __shfl_xor(s, 2);
+        s += __shfl_xor(s, 4);
+        if (sub == 0) a.d_probs[r] = s;
     }
 }
 
@@ -292,13 +338,13 @@ __global__ void __launch_bounds__(256) cast_rows_kernel(const float* in, const i
 {
     const int64_t n = rows_live(live, T_cap) * (H / 8);
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        Row8<false> v;
+        RowN<false, 8> v;
         v.load(in, 8 * i);
         float f[8];
         v.get(f);
-        Row8<true> o;
+        RowN<true, 8> o;
         o.set(f);
-        *(u4v*)(out + 8 * i) = o.v;
+        *(u4v*)(out + 8 * i) = u4v{o.w[0], o.w[1], o.w[2], o.w[3]};
     }
 }
 
@@ -323,7 +369,7 @@ hipError_t launch_dispatch(const void* x, int bf16, const int32_t* ids, const in
                            int32_t* row_of, int32_t* offsets_out, int num_cu, hipStream_t s)
 {
     const DispatchArgs a{x, ids, dst, offsets, live, T_cap, E, H, rows, row_of, offsets_out};
-    const dim3 g = rows_grid(T_cap * (H / 8), num_cu), b(256);
+    const dim3 g = rows_grid(T_cap * (H / (bf16 ? 8 : 4)), num_cu), b(256);
 #define M(K)                                                                                   \
     case K:                                                                                    \
         if (bf16) hipLaunchKernelGGL((dispatch_kernel<K, true>), g, b, 0, s, a);               \
@@ -339,7 +385,7 @@ hipError_t launch_combine(const void* rows, int in_bf16, const int32_t* row_of, 
                           hipStream_t s)
 {
     const CombineArgs a{rows, row_of, probs, live, T_cap, H, out};
-    const dim3 g = rows_grid(T_cap * (H / 8), num_cu), b(256);
+    const dim3 g = rows_grid(T_cap * (H / (in_bf16 ? 8 : 4)), num_cu), b(256);
 #define M(K)                                                                                   \
     case K:                                                                                    \
         if (in_bf16 && out_bf16) hipLaunchKernelGGL((combine_kernel<K, true, true>), g, b, 0, s, a);   \
@@ -374,11 +420,18 @@ hipError_t launch_combine_backward(const void* d_out, int out_bf16, const void* 
     return hipGetLastError();
 }
 
-hipError_t launch_grad_probs(const float* part, int n_part, const int32_t* ids, const int32_t* dst,
-                             const int32_t* live, int64_t T_cap, int k, float* d_probs, int num_cu, hipStream_t s)
+hipError_t launch_grad_ends(const float* rows, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
+                            const int32_t* live, int64_t T_cap, int k, int H, void* d_x, float* d_probs, int num_cu,
+                            hipStream_t s)
 {
-    hipLaunchKernelGGL(grad_probs_kernel, rows_grid(T_cap * k, num_cu), dim3(256), 0, s, part, n_part, ids, dst, live,
-                       T_cap, k, d_probs);
+    const dim3 gx = rows_grid(T_cap * (H / 4), num_cu), gp = rows_grid(T_cap * k * 8, num_cu), b(256);
+    const GradEndsArgs a{{rows, dst, nullptr, live, T_cap, H, d_x}, part, n_part, ids, d_probs, (int)gx.x};
+#define M(K)                                                                                   \
+    case K:                                                                                    \
+        hipLaunchKernelGGL(grad_ends_kernel<K>, dim3(gx.x + gp.x), b, 0, s, a);                \
+        break;
+    ROWS_K(M)
+#undef M
     return hipGetLastError();
 }
 
