@@ -18,7 +18,8 @@ hipError_t launch_route(const float* logits, int64_t T_cap, const int32_t* live,
                         int32_t* ids, float* probs, WsHeader* hdr, int num_cu, hipStream_t s);
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x);
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x,
+                       bool scatter = true);
 size_t balance_ws_bytes(int E, int64_t T_cap);
 hipError_t launch_balance(const float* logits, const int32_t* ids, int64_t T_cap, const int32_t* live,
                           const uint8_t* mask, int E, int k, float* losses, int32_t* counts, float* prob_sums,
@@ -44,7 +45,8 @@ hipError_t launch_quant_rows_int8(const QuantRows& a, const QuantTiles* tiles, i
 hipError_t launch_pack_int8(const void* w1, const float* ws1, const void* w2, const float* ws2, int codes,
                             uint8_t* kbuf, int E, int H, int F, int num_cu, hipStream_t s);
 void int8_section_bytes(int E, int H, int F, size_t* c1, size_t* c2, size_t* s1, size_t* s2);
-hipError_t launch_dispatch(const void* x, int bf16, const int32_t* ids, const int32_t* dst, const int32_t* offsets,
+bool dispatch_in_one(int64_t T_cap);
+hipError_t launch_dispatch(const void* x, int bf16, const int32_t* ids, char* ws, const WsLayout& L,
                            const int32_t* live, int64_t T_cap, int E, int k, int H, void* rows, int32_t* row_of,
                            int32_t* offsets_out, int num_cu, hipStream_t s);
 hipError_t launch_combine(const void* rows, int in_bf16, const int32_t* row_of, const float* probs,
@@ -1034,12 +1036,15 @@ moe_status moe_dispatch(moe_handle h, const void* x, int type, const int32_t* ex
                        {{x, T * row}, {expert_ids, 4 * R}, {live_rows_dev, 4}});
     if (st != MOE_OK || (st = ensure_device(h)) != MOE_OK) return st;
     char* w = (char*)ws;
-    hipError_t e = launch_prep(expert_ids, nullptr, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
-                               MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr);
-    if (e != hipSuccess) return hip_fail(e, "moe_dispatch: prep launch");
-    e = launch_dispatch(x, type == MOE_TYPE_BF16, expert_ids, (const int32_t*)(w + L.dst),
-                        (const int32_t*)(w + L.offsets), live_rows_dev, T_cap, h->E, h->k, h->H, rows, row_of, offsets,
-                        h->num_cu, stream);
+    hipError_t e = hipSuccess;
+    if (!dispatch_in_one(T_cap)) {
+        // (the rows of the routes come from the ranks and bases: no scatter)
+        e = launch_prep(expert_ids, nullptr, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
+                        MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr, false);
+        if (e != hipSuccess) return hip_fail(e, "moe_dispatch: prep launch");
+    }
+    e = launch_dispatch(x, type == MOE_TYPE_BF16, expert_ids, w, L, live_rows_dev, T_cap, h->E, h->k, h->H, rows,
+                        row_of, offsets, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_dispatch: launch");
     return MOE_OK;
 }

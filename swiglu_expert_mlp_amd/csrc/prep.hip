@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(256) prep_scatter_kernel(
 
 hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, const int32_t* live,
                        int E, int k, int num_cu, char* ws, const WsLayout& L, hipStream_t s,
-                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x)
+                       int fin_H, int fin_mode, void* fin_out, uint64_t tag, int weighted, const QuantRows* quant_x,
+                       bool scatter)
 {
     PrepArgs a;
     a.tag = tag;
@@ -521,6 +522,7 @@ hipError_t launch_prep(const int32_t* ids, const float* probs, int64_t T_cap, co
         hipLaunchKernelGGL(prep_finish_quant_kernel, gq, dim3(256), 0, s, a, *quant_x);
     else
         hipLaunchKernelGGL(prep_finish_kernel, dim3(1), dim3(256), 0, s, a);
+    if (!scatter) return hipGetLastError();         // the caller's own launch places the routes
     int64_t R = T_cap * k;
     int64_t blocks = (R + 255) / 256;
     if (blocks > (int64_t)num_cu * 4) blocks = (int64_t)num_cu * 4;
