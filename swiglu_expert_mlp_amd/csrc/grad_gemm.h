@@ -169,6 +169,64 @@ __device__ __forceinline__ void grad_kloop(int nst, char* s0, char* s1, f32x16 (
     grad_mma(acc, y);
 }
 
+// grad_kloop with the two stages in halves of 32 along the sum (h0, h1 the first stage's, h2,
+// h3 the second's) that are refilled one by one, so three halves instead of one stage are in
+// flight, for two barriers a stage.  LOADS: direct loads of a half per wave; on entry four
+// halves are in flight.  read(Q, half, frag): sub-step Q = 0, 1 of a half; issue(half): the
+// next half not issued yet (past the last stage: zeros).
+template <int READS, int AFTER, int LOADS, typename Read, typename Issue>
+__device__ __forceinline__ void grad_kloop_halves(int nst, char* h0, char* h1, char* h2, char* h3,
+                                                  f32x16 (&acc)[4][2], Read read, Issue issue)
+{
+    static_assert(AFTER + 3 * LOADS <= 63, "vmcnt bound");
+    GradFrag x, y;
+    using Q0 = std::integral_constant<int, 0>;
+    using Q1 = std::integral_constant<int, 1>;
+    using Now = std::integral_constant<int, 0>;
+    using Aft = std::integral_constant<int, AFTER>;
+    BIG_WAIT_VMCNT(AFTER + 3 * LOADS);
+    __builtin_amdgcn_s_barrier();
+    read(Q0{}, h0, x);
+    // the next half landed (the two halves after it, and N stores, may be in flight), every
+    // wave's reads of `cur` are done: `cur` is refilled
+    auto boundary = [&](auto NC, char* cur) {
+        __builtin_amdgcn_sched_barrier(0);
+        BIG_WAIT_VMCNT(2 * LOADS + decltype(NC)::value);
+        __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(cur);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto body = [&](auto NC, char* a, char* b) {
+        grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, a, n); }, y);
+        boundary(NC, a);
+        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, b, n); }, x);
+        grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, b, n); }, y);
+    };
+    auto into = [&](auto NC, char* b, char* c) {
+        boundary(NC, b);
+        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, c, n); }, x);
+    };
+    body(Aft{}, h0, h1);
+    if (nst > 1) {
+        into(Aft{}, h1, h2);
+        body(Aft{}, h2, h3);
+        int s = 2;
+        for (; s + 2 <= nst; s += 2) {
+            into(Now{}, h3, h0);
+            body(Now{}, h0, h1);
+            into(Now{}, h1, h2);
+            body(Now{}, h2, h3);
+        }
+        if (s < nst) {
+            into(Now{}, h3, h0);
+            body(Now{}, h0, h1);
+        }
+    }
+    grad_mma(acc, y);
+}
+
 // 32 x 64 of a wave's results (row block i) to bf16 rows through its LDS region: row rr
 // at 128 rr bytes, 64-byte halves swapped in rows 4 m .. 4 m + 3 with odd m (the two rows a
 // write instruction covers fall in different halves).  store(k, row, chunk, value): the
@@ -744,8 +802,12 @@ __device__ __forceinline__ int grad_part(const int32_t* offsets, int E, int per_
 template <bool FP32>
 __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
 {
-    __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
-    __shared__ __attribute__((aligned(1024))) char lds1[kBigStage];
+    constexpr int kHalf = kBigStage / 2;            // 32 rows of P, then of Q, 512 bytes each
+    constexpr int kHalfQ = kHalf / 2;
+    __shared__ __attribute__((aligned(1024))) char lds0[kHalf];
+    __shared__ __attribute__((aligned(1024))) char lds1[kHalf];
+    __shared__ __attribute__((aligned(1024))) char lds2[kHalf];
+    __shared__ __attribute__((aligned(1024))) char lds3[kHalf];
     __shared__ __attribute__((aligned(1024))) char lds_x[8 * kBigEpi];
 
     const int lane = threadIdx.x & 63;
@@ -770,87 +832,77 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
         return TilePos{e, base, ld_const(g.offsets + e + 1) - base, mi * kBigTM, (u - mi * nt) * kBigTN, w2};
     };
 
-    // A stage: 64 rows of P, then of Q, 512 bytes each; 16-byte chunk c of row r at slot
-    // c ^ 4 (r % 4), so that the 4 rows x 4 chunks that 32 lanes read together lie on
-    // distinct banks.  Wave w loads rows 8 w .. 8 w + 7 of both, two rows an instruction.
-    // Rows past the expert's last read zeros on the own side (so that they add nothing) and
-    // the last row on the gathered side (so that no value of another row comes in: 0 times
-    // a NaN of the expert's own last row is a NaN that this row gives anyway).  An expert
-    // without rows reads zeros on both sides, and its sum is left out.
-    // The addresses are kept so that a stage costs few instructions (computed anew from the
-    // row and its token each stage they were 4.6 vector instructions per MFMA): the own
-    // rows' pointers advance by 64 rows, a gathered row is one multiply-add of its token,
-    // read a stage ahead from the table that the first product left.
-    int cnt = 0, oslot = 0, gslot = 0;     // rows; where own and gathered rows lie in a stage
-    const int half = lane >> 5;
-    const int row8 = 8 * wid + half;       // load i: row row8 + 2 i of the stage
-    const char* own[4];                    // own rows of the next stage to issue, at the lane's column
-    const char* gcol[2];                   // gathered matrix at the lane's column: rows r % 4 = 0, 1 and 2, 3
-    uint32_t ostep = 0, gpitch = 0;        // bytes of 64 own rows, of a gathered row
-    const int32_t* toks = nullptr;         // the expert's part of the token table
-    int tok[4];                            // tokens of the next stage to issue
-    auto tokens = [&](const int32_t* table, int n, int s, int (&t)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = table[max(0, min(64 * s + row8 + 2 * i, n - 1))];
-    };
-    // (an expert without rows: entry 0 of the table, whatever it holds, with a pitch of 0)
-    auto table_of = [&](const TilePos& p) { return g.row_tok + (p.cnt > 0 ? p.row0 : 0); };
+    // 16-byte chunk c of row r lies at chunk c ^ 4 (r % 4), so that the 4 rows x 4 chunks that
+    // 32 lanes read together lie on distinct banks.  Wave w loads rows 4 w .. 4 w + 3 of both
+    // matrices, two rows an instruction.  Rows past the expert's last read zeros on both sides.
+    // The own rows' pointers advance by 32 rows a half; a gathered row is one multiply-add of
+    // its token, which comes by a scalar load a half ahead from the table that the first
+    // product left (with the row and its token worked out anew each stage these were 4.6
+    // vector instructions per MFMA).
+    int cnt = 0, oslot = 0, gslot = 0;     // rows; where own and gathered rows lie in a half
+    const int odd = lane >> 5;
+    const char* own[2];                    // own rows of the next half to issue, at the lane's column
+    const char* gcol[2];                   // gathered matrix at the lane's column
+    uint32_t ostep = 0;                    // bytes of 32 own rows
+    int row = 0;                           // the lane's first row of the next half to issue
+    struct Tok { int t[4]; };
+    const int32_t* toks = nullptr;         // the wave's first token of the next half to issue
+    Tok tok;
+    auto tokens = [&](const int32_t* p) { return Tok{{ld_const(p), ld_const(p + 1), ld_const(p + 2), ld_const(p + 3)}}; };
     auto sources = [&](const TilePos& p) {
         const int ow = p.w2 ? F : 2 * F;                         // columns of the own matrix
         const int o0 = p.w2 ? p.n0 : p.m0, g0 = p.w2 ? p.m0 : p.n0;
         const uint16_t* ob = p.w2 ? g.hp : g.dgu;
         const uint16_t* gb = p.w2 ? g.d_out : g.x;
         cnt = p.cnt;
-        oslot = p.w2 ? kBigWOff : 0;
-        gslot = p.w2 ? 0 : kBigWOff;
-        ostep = 128u * (uint32_t)ow;
-        gpitch = p.cnt > 0 ? 2u * (uint32_t)H : 0u;
-        toks = table_of(p);
+        oslot = p.w2 ? kHalfQ : 0;
+        gslot = p.w2 ? 0 : kHalfQ;
+        ostep = 64u * (uint32_t)ow;
+        row = 4 * wid + odd;
+        toks = g.row_tok + p.row0 + 4 * wid;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < 2; ++i) {
             // the slot's chunk; a column past the matrix reads its last chunk (never stored)
-            const int c = 8 * ((lane & 31) ^ (4 * (2 * h + half)));
-            gcol[h] = p.cnt > 0 ? (const char*)(gb + min(g0 + c, H - 8)) : (const char*)grad_zeros;
-            const uint16_t* o = ob + min(o0 + c, ow - 8);
-#pragma unroll
-            for (int i = h; i < 4; i += 2) own[i] = (const char*)(o + ((int64_t)p.row0 + row8 + 2 * i) * ow);
+            const int c = 8 * ((lane & 31) ^ (4 * (2 * i + odd)));
+            gcol[i] = (const char*)(gb + min(g0 + c, H - 8));
+            own[i] = (const char*)(ob + min(o0 + c, ow - 8) + ((int64_t)p.row0 + row + 2 * i) * ow);
         }
     };
-    auto issue_rows = [&](char* st, int s, const int (&t)[4]) {
+    auto issue_rows = [&](char* st, const Tok& t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            big_load_block(64 * s + row8 + 2 * i < cnt ? own[i] : (const char*)grad_zeros,
-                           st + oslot + (4 * wid + i) * 1024);
+        for (int i = 0; i < 2; ++i) {
+            const bool in = row + 2 * i < cnt;
+            const uint32_t tk = (uint32_t)(odd ? t.t[2 * i + 1] : t.t[2 * i]);
+            const char* gp = gcol[i] + (uint64_t)tk * (2u * (uint32_t)H);
+            big_load_block(in ? own[i] : (const char*)grad_zeros, st + oslot + (2 * wid + i) * 1024);
+            big_load_block(in ? gp : (const char*)grad_zeros, st + gslot + (2 * wid + i) * 1024);
             own[i] += ostep;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            big_load_block(gcol[i & 1] + (uint64_t)(uint32_t)t[i] * gpitch, st + gslot + (4 * wid + i) * 1024);
+        row += 32;
     };
-    TilePos pos, npos;
-    // (past the last stage: rows past the expert's last, so zeros and the last row again)
-    int next_stage = 0;
-    auto issue = [&](char* st, int) {
-        issue_rows(st, next_stage, tok);
-        tokens(toks, cnt, ++next_stage, tok);
+    auto issue = [&](char* st) {
+        issue_rows(st, tok);
+        toks += 32;
+        tok = tokens(toks);                // (the table is 256 entries longer than the rows)
     };
-    // the tokens of a tile's first two stages, loaded before the K loop of the tile before it,
-    // then those stages and the tokens of the third
-    int tok0[4], tok1[4];
+    // a tile's first four halves, and the tokens of its fifth; the tokens are loaded before the
+    // K loop of the tile before it
+    Tok ahead[4];
     auto lookup = [&](const TilePos& p) {
-        const int32_t* table = table_of(p);
-        tokens(table, p.cnt, 0, tok0);
-        tokens(table, p.cnt, 1, tok1);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) ahead[h] = tokens(g.row_tok + p.row0 + 32 * h + 4 * wid);
     };
     auto start = [&](const TilePos& p) {
         sources(p);
-        issue_rows(lds0, 0, tok0);
-        issue_rows(lds1, 1, tok1);
-        tokens(toks, cnt, 2, tok);
-        next_stage = 2;
+        issue_rows(lds0, ahead[0]);
+        issue_rows(lds1, ahead[1]);
+        issue_rows(lds2, ahead[2]);
+        issue_rows(lds3, ahead[3]);
+        toks += 128;
+        tok = tokens(toks);
     };
-    // fragments of sub-step Q: rows 16 Q + 8 (l / 32) + {0, 4} + (l % 16) / 4, the lane's 4
-    // columns of each 32-column block
+    // fragments of sub-step Q of a half: rows 16 Q + 8 (l / 32) + {0, 4} + (l % 16) / 4, the
+    // lane's 4 columns of each 32-column block
     int a_off[4], b_off[2];
     {
         const int j = lane & 15, jj = j >> 2;
@@ -858,7 +910,7 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
 #pragma unroll
         for (int i = 0; i < 4; ++i) a_off[i] = base + 64 * ((4 * wm + i) ^ jj);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) b_off[i] = kBigWOff + base + 64 * ((2 * wn + i) ^ jj);
+        for (int i = 0; i < 2; ++i) b_off[i] = kHalfQ + base + 64 * ((2 * wn + i) ^ jj);
     }
     auto read = [&](auto QC, const char* st, GradFrag& f) {
         constexpr int Q = decltype(QC)::value;
@@ -872,11 +924,10 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     const int end = grad_part(g.offsets, g.E, per_e, xcd + 1, lane);
     int tile = grad_part(g.offsets, g.E, per_e, xcd, lane) + (int)(blockIdx.x >> 3);
     if (tile >= end) return;
-    pos = npos = locate(tile);
+    TilePos pos = locate(tile), npos = pos;
     lookup(pos);
     start(pos);
     constexpr int kStores = FP32 ? 32 : 16;
-    constexpr int kLook = 8;                    // the next tile's lookup
     grad_dummy_stores<kStores>(g.dgu, lane);
     char* const ep = lds_x + wid * kBigEpi;
     while (true) {
@@ -891,8 +942,10 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
         const bool more = next < end;
         if (more) npos = locate(next);
         lookup(npos);
-        if (pos.cnt > 0) grad_kloop<12, kStores + kLook>((pos.cnt + 63) / 64, lds0, lds1, acc, read, issue);
-        else BIG_WAIT_VMCNT(kStores + kLook);       // its loads land before the next tile's go out
+        if (pos.cnt > 0)
+            grad_kloop_halves<12, kStores, 4>((pos.cnt + 63) / 64, lds0, lds1, lds2, lds3, acc, read, issue);
+        else
+            BIG_WAIT_VMCNT(kStores);                // its loads land before the next tile's go out
         __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         start(npos);

@@ -217,7 +217,7 @@ static BackwardLayout backward_layout(const moe_ctx* h, int64_t T_cap)
     B.hp = take(2 * R * F);
     B.dx = take(4 * R * H);
     B.part = take(R * F / 8);
-    B.row_tok = take(4 * R);
+    B.row_tok = take(4 * (R + 512));        // (read ahead of the rows, up to 256 entries)
     B.d_out = take(2 * T_cap * H);
     B.total = o;
     return B;

@@ -473,10 +473,13 @@ __global__ void __launch_bounds__(256) cast_rows_kernel(const float* in, const i
 
 // ---------------------------------------------------------------- launches
 
+// Up to 64 workgroups a CU, looping above that: at 16K tokens (hidden 2048, top-8) sums of
+// fp32 rows 206 us against 222 with 16 a CU, dispatch 117 against 126; workgroups past the
+// live tokens of a large capacity start and exit (6 us for 16,384 of them)
 static dim3 rows_grid(int64_t threads, int num_cu)
 {
     int64_t b = (threads + 255) / 256;
-    const int64_t most = (int64_t)num_cu * 16;
+    const int64_t most = (int64_t)num_cu * 64;
     if (b > most) b = most;
     return dim3((unsigned)(b < 1 ? 1 : b));
 }
