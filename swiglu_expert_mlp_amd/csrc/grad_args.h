@@ -21,7 +21,8 @@ struct GradArgs {
     const uint8_t* scales;     // [rows][F / 16]
     uint16_t* dgu;             // bf16 [rows][2F]
     uint16_t* hp;              // bf16 [rows][F]
-    float* dx;                 // fp32 [rows][H]
+    uint16_t* dx;              // [rows][H], 16-bit codes (grad_dx.h)
+    uint8_t* dx_scale;         // [rows][H / 16], their scale bytes
     float* part;               // fp32 [rows][F / 32]
     int32_t* row_tok;          // int32 [rows]: token of each grouped row
     void* d_w1;                // [E][2F][H], gate rows first

@@ -28,6 +28,7 @@
 
 #include "gemm_bf16_big.h"
 #include "grad_args.h"
+#include "grad_dx.h"
 
 namespace moe {
 
@@ -73,13 +74,20 @@ struct GradFrag {
     bf16x8 a[4], b[2];
 };
 
+// The operands go in swapped, so that a block's results come transposed: lane l holds row
+// l % 32 and columns 8 (v / 4) + 4 (l / 32) + v % 4, four neighbouring ones at a time, and
+// leaves them in LDS by 16-byte writes (one value a write otherwise)
+__device__ __forceinline__ f32x16 grad_mfma(bf16x8 a, bf16x8 b, f32x16 acc)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, acc, 0, 0, 0);
+}
+
 __device__ __forceinline__ void grad_mma(f32x16 (&acc)[4][2], const GradFrag& f)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j) acc[i][j] = grad_mfma(f.a[i], f.b[j], acc[i][j]);
 }
 
 // One sub-step of 16 along the sum: the MFMAs of `cur` with the READS fragment reads of
@@ -227,29 +235,53 @@ __device__ __forceinline__ void grad_kloop_halves(int nst, char* h0, char* h1, c
     grad_mma(acc, y);
 }
 
-// 32 x 64 of a wave's results (row block i) to bf16 rows through its LDS region: row rr
-// at 128 rr bytes, 64-byte halves swapped in rows 4 m .. 4 m + 3 with odd m (the two rows a
-// write instruction covers fall in different halves).  store(k, row, chunk, value): the
-// lane's 16 bytes of row `row` of 32, columns 8 chunk .. 8 chunk + 7 of 64, k = 0 .. 3.
-template <typename Store>
-__device__ __forceinline__ void grad_rows_bf16(const f32x16 (&acc)[2], char* ep, int lane, Store store)
+// A wave's results leave through its LDS region, a block at a time.  fp32: 32 rows of 128
+// bytes, 16-byte chunk c of row r at c ^ ((r / 2) % 8); bf16: 32 rows of 64 columns, also 128
+// bytes, placed the same way.  (Two rows span the banks, so 16 rows' writes of one chunk, and
+// the reads of 8 rows' halves, fall on distinct ones.)  The offsets are opaque: with a
+// constant part folded into the instruction the compiler waited for the next tile's direct
+// loads before the write.
+__device__ __forceinline__ int grad_at(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
+
+__device__ __forceinline__ void grad_block_to_lds(const f32x16& acc, char* ep, int lane)
 {
-    const int hi = lane >> 5, c32 = lane & 31;
+    const int r = lane & 31, hi = lane >> 5;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        int ea = grad_at(r, 2 * q + hi);
+        asm volatile("" : "+v"(ea));
+        *(f32x4*)(ep + ea) = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    }
+}
+
+// 16 neighbouring columns (half h) of a row of the block
+__device__ __forceinline__ void grad_read16(const char* ep, int row, int h, float (&v)[16])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const f32x4 u = *(const f32x4*)(ep + grad_at(row, 4 * h + c));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[4 * c + m] = u[m];
+    }
+}
+
+__device__ __forceinline__ uint32_t grad_pair(float a, float b)
+{
+    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+}
+
+__device__ __forceinline__ void grad_blocks_to_lds_bf16(const f32x16 (&acc)[2], char* ep, int lane)
+{
+    const int r = lane & 31, hi = lane >> 5;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            const int rr = 8 * (v >> 2) + 4 * hi + (v & 3);
-            int ea = (rr * 128 + 64 * j + 2 * c32) ^ (((rr >> 2) & 1) << 6);
+        for (int q = 0; q < 4; ++q) {
+            int ea = grad_at(r, 4 * j + q) + 8 * hi;
             asm volatile("" : "+v"(ea));
-            *(uint16_t*)(ep + ea) = f32_to_bf16_bits(acc[j][v]);
+            *(uint2*)(ep + ea) = make_uint2(grad_pair(acc[j][4 * q], acc[j][4 * q + 1]),
+                                            grad_pair(acc[j][4 * q + 2], acc[j][4 * q + 3]));
         }
-    const int c = lane & 7;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int rr = (lane >> 3) + 8 * k;
-        store(k, rr, c, *(const u32x4_t*)(ep + ((rr * 128 + 16 * c) ^ (((rr >> 2) & 1) << 6))));
-    }
 }
 
 // ---------------------------------------------------------------- rows products
@@ -290,9 +322,9 @@ __device__ __forceinline__ float grad_swiglu16(const float (&raw)[16], const Gra
             vg[n] = dh * up * __builtin_fmaf(silu, 1.0f - s, s);
             vh[n] = h * p;
         }
-        og[m / 2] = (uint32_t)f32_to_bf16_bits(vg[0]) | ((uint32_t)f32_to_bf16_bits(vg[1]) << 16);
-        ou[m / 2] = (uint32_t)f32_to_bf16_bits(vu[0]) | ((uint32_t)f32_to_bf16_bits(vu[1]) << 16);
-        oh[m / 2] = (uint32_t)f32_to_bf16_bits(vh[0]) | ((uint32_t)f32_to_bf16_bits(vh[1]) << 16);
+        og[m / 2] = grad_pair(vg[0], vg[1]);
+        ou[m / 2] = grad_pair(vu[0], vu[1]);
+        oh[m / 2] = grad_pair(vh[0], vh[1]);
     }
     return dot;
 }
@@ -327,8 +359,61 @@ __device__ __forceinline__ void grad_leave_token(const GradArgs& g, int row0, in
     __builtin_amdgcn_raw_buffer_store_b32((uint32_t)tok, d, (lane & 7) == 0 ? 4 * r : 0x7ffffff0, 0, 0);
 }
 
-// dx: fp32 rows (rounded to bf16 they would add a third rounding to d_x's two)
-constexpr int grad_rows_stores(bool swiglu) { return swiglu ? 48 : 32; }
+// The epilogue of one 32 x 32 block of either rows product, shared by the tile designs: lane
+// = row lane / 2 and 16 columns (half lane % 2).
+struct GradOut {
+    __amdgpu_buffer_rsrc_t o0, o1;     // SWIGLU: rows of dgu, of hp; else of dx, of its scales
+};
+template <bool SWIGLU>
+__device__ __forceinline__ GradOut grad_out(const GradArgs& g, int row0, int rows)
+{
+    if constexpr (SWIGLU)
+        return {__builtin_amdgcn_make_buffer_rsrc((void*)(g.dgu + (int64_t)row0 * 2 * g.F), (short)0, rows * 4 * g.F,
+                                                  kBigRsrcWord3),
+                __builtin_amdgcn_make_buffer_rsrc((void*)(g.hp + (int64_t)row0 * g.F), (short)0, rows * 2 * g.F,
+                                                  kBigRsrcWord3)};
+    else
+        return {__builtin_amdgcn_make_buffer_rsrc((void*)(g.dx + (int64_t)row0 * g.H), (short)0, rows * 2 * g.H,
+                                                  kBigRsrcWord3),
+                __builtin_amdgcn_make_buffer_rsrc((void*)(g.dx_scale + (int64_t)row0 * (g.H / 16)), (short)0,
+                                                  rows * (g.H / 16), kBigRsrcWord3)};
+}
+
+// SWIGLU: block `block` of the FFN, rows tr .. tr + 31 of the tile's `rows` from row0 on
+__device__ __forceinline__ void grad_swiglu_block(const GradArgs& g, const GradOut& o, const f32x16& acc, char* ep,
+                                                  int lane, const GradKept& kept, float p, int row0, int rows, int tr,
+                                                  int block)
+{
+    grad_block_to_lds(acc, ep, lane);
+    float raw[16];
+    const int row = tr + (lane >> 1), half = lane & 1;
+    grad_read16(ep, lane >> 1, half, raw);
+    uint32_t og[8], ou[8], oh[8];
+    float dot = grad_swiglu16(raw, kept, p, og, ou, oh);
+    grad_swiglu_store(o.o0, o.o1, g.F, row, block, half, og, ou, oh);
+    dot += __shfl_xor(dot, 1);
+    if (half == 0 && row < rows && 32 * block < g.F) g.part[(int64_t)(row0 + row) * (g.F / 32) + block] = dot;
+}
+
+// dx: columns 32 block .. of 32 rows, 16 bits a value (grad_dx.h)
+__device__ __forceinline__ void grad_dx_block(const GradArgs& g, const GradOut& o, const f32x16& acc, char* ep, int lane,
+                                              int tr, int block)
+{
+    grad_block_to_lds(acc, ep, lane);
+    float v[16];
+    const int row = tr + (lane >> 1), half = lane & 1;
+    grad_read16(ep, lane >> 1, half, v);
+    uint32_t w[8];
+    const uint32_t byte = dx_pack16(v, w);
+    const bool cols = 32 * block < g.H;
+    const int at = cols ? (row * g.H + 32 * block + 16 * half) * 2 : 0x7ffffe00;
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{w[0], w[1], w[2], w[3]}, o.o0, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{w[4], w[5], w[6], w[7]}, o.o0, at + 16, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, o.o1, cols ? row * (g.H / 16) + 2 * block + half : 0x7ffffe00, 0, 0);
+}
+
+// Stores of a 32 x 32 block that every lane issues (SWIGLU: and one of partial sums)
+constexpr int grad_block_stores(bool swiglu) { return swiglu ? 6 : 3; }
 
 template <bool SWIGLU>
 __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
@@ -441,7 +526,7 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     sources(pos);
     issue(lds0, 0);
     issue(lds1, min(1, nst - 1));
-    constexpr int kStores = grad_rows_stores(SWIGLU);
+    constexpr int kStores = 8 * grad_block_stores(SWIGLU);
     constexpr int kLook = SWIGLU ? kBigALoads : 0;
     grad_dummy_stores<kStores>(g.dgu, lane);
     char* const ep = lds_x + wid * kBigEpi;
@@ -464,16 +549,15 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
         int elane = lane;
         asm volatile("" : "+v"(elane));
 
-        // SWIGLU: everything the epilogue reads from memory, before the next tile's loads:
-        // lane = row elane / 4 of 16 and 16 of 64 columns; pass (i, hv) covers rows
-        // 32 i + 16 hv .. + 15 of the wave's 128
-        // (the second half of the passes after the first two: all at once spilled)
+        // SWIGLU: everything the epilogue reads from memory, before the next tile's loads, by 8
+        // blocks of 32 x 32 (row block q / 2, column block q % 2); the second half of them after
+        // the first two (all at once spilled)
         GradKept kept[8];
         float pr0 = 0.0f, pr1 = 0.0f;
-        const int quarter = elane & 3, prow = elane >> 2;
-        const int ib = n0 / 32 + 2 * wn + (quarter >> 1);        // interleave block of the lane's columns
+        const int prow = elane >> 1, ib = n0 / 32 + 2 * wn;
         auto load_kept = [&](int q) {
-            kept[q] = grad_kept(g, row0 + min(128 * wm + 16 * q + prow, rows - 1), min(ib, g.F / 32 - 1), quarter & 1);
+            kept[q] = grad_kept(g, row0 + min(128 * wm + 32 * (q >> 1) + prow, rows - 1),
+                                min(ib + (q & 1), g.F / 32 - 1), elane & 1);
         };
         if constexpr (SWIGLU) {
             const int r0 = min(128 * wm + elane, rows - 1), r1 = min(128 * wm + elane + 64, rows - 1);
@@ -486,51 +570,21 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
         issue(lds0, 0);
         issue(lds1, min(1, nst - 1));
 
-        if constexpr (SWIGLU) {
-            const int F = g.F;
-            const __amdgpu_buffer_rsrc_t gu = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(g.dgu + (int64_t)row0 * 2 * F), (short)0, rows * 4 * F, kBigRsrcWord3);
-            const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(g.hp + (int64_t)row0 * F), (short)0, rows * 2 * F, kBigRsrcWord3);
+        const GradOut out = grad_out<SWIGLU>(g, row0, rows);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 8; ++q) {
+            const int i = q >> 1, tr = 128 * wm + 32 * i;
+            if constexpr (SWIGLU) {
                 if (q == 2) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int n = 4; n < 8; ++n) load_kept(n);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                big_half_to_lds(acc[q >> 1], q & 1, ep, elane);
-                float raw[16];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const f32x4 v = *(const f32x4*)(ep + prow * 256 + ((64 * quarter + 16 * c) ^ half_swz(prow)));
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) raw[4 * c + m] = v[m];
-                }
-                const int wr = 128 * wm + 16 * q + prow;         // row of the tile
-                const float p = lane_value(4 * (16 * (q & 3) + prow), q < 4 ? pr0 : pr1);
-                uint32_t og[8], ou[8], oh[8];
-                float dot = grad_swiglu16(raw, kept[q], p, og, ou, oh);
-                grad_swiglu_store(gu, hr, F, wr, ib, quarter & 1, og, ou, oh);
-                dot += __shfl_xor(dot, 1);
-                if (!(quarter & 1) && wr < rows && 32 * ib < F) g.part[(int64_t)(row0 + wr) * (F / 32) + ib] = dot;
-            }
-        } else {
-            const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 4, kBigRsrcWord3);
-            const int c = elane & 15;
-            const int col = n0 + 64 * wn + 4 * c;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                big_half_to_lds(acc[q >> 1], q & 1, ep, elane);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int lr = (elane >> 4) + 4 * k;
-                    const u32x4_t val = *(const u32x4_t*)(ep + lr * 256 + ((16 * c) ^ half_swz(lr)));
-                    const int off = col < N ? ((128 * wm + 16 * q + lr) * N + col) * 4 : 0x7ffffff0;
-                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
-                }
+                const float p = lane_value(4 * (32 * (i & 1) + prow), i < 2 ? pr0 : pr1);
+                grad_swiglu_block(g, out, acc[i][q & 1], ep, elane, kept[q], p, row0, rows, tr, ib + (q & 1));
+            } else {
+                grad_dx_block(g, out, acc[i][q & 1], ep, elane, tr, ib + (q & 1));
             }
         }
         if (!more) {
@@ -637,8 +691,7 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
     TilePos pos{}, npos{};
     int tile = advance(xcd_first_tile(), pos);
     if (tile >= total) return;
-    // SWIGLU: 12 stores of the rows (and 2 of partial sums), else 8
-    constexpr int kStores = SWIGLU ? 12 : 8;
+    constexpr int kStores = 2 * grad_block_stores(SWIGLU);
     constexpr int kLook = SWIGLU ? 1 : 0;
     lookup(pos);
     sources(pos);
@@ -678,7 +731,7 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[q][i], b[q], acc[i], 0, 0, 0);
+                    acc[i] = grad_mfma(a[q][i], b[q], acc[i]);
         };
         using Now = std::integral_constant<int, 0>;
         step(std::integral_constant<int, kStores + kLook>{}, 0, lds0, lds2);
@@ -712,52 +765,13 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
         sources(npos);
         issue(lds0, 0);
         issue(lds1, min(1, nst - 1));
-        __amdgpu_buffer_rsrc_t o0, o1;
-        if constexpr (SWIGLU) {
-            o0 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.dgu + (int64_t)row0 * 2 * g.F), (short)0, rows * 4 * g.F,
-                                                   kBigRsrcWord3);
-            o1 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.hp + (int64_t)row0 * g.F), (short)0, rows * 2 * g.F,
-                                                   kBigRsrcWord3);
-        } else {
-            o0 = __builtin_amdgcn_make_buffer_rsrc((void*)(g.dx + (int64_t)row0 * N), (short)0, rows * N * 4,
-                                                   kBigRsrcWord3);
-        }
+        const GradOut out = grad_out<SWIGLU>(g, row0, rows);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            // 32 rows x 32 fp32 through the wave's region: row r in slot r ^ ((r / 4) % 2), its
-            // 16-byte chunk c at c ^ ((r / 2) % 4), so that a write's two rows fall in different
-            // halves of the banks and so do the 8 rows that 16 lanes read
-            const int hi = elane >> 5, c32 = elane & 31;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int r = 8 * (v >> 2) + 4 * hi + (v & 3);
-                *(float*)(ep + (r ^ ((r >> 2) & 1)) * 128 + ((4 * c32) ^ (16 * ((r >> 1) & 3)))) = acc[i][v];
-            }
-            float raw[16];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const f32x4 v = *(const f32x4*)(ep + (prow ^ ((prow >> 2) & 1)) * 128 +
-                                                ((64 * half + 16 * c) ^ (16 * ((prow >> 1) & 3))));
-#pragma unroll
-                for (int m = 0; m < 4; ++m) raw[4 * c + m] = v[m];
-            }
-            const int wr = 32 * i + prow;
-            if constexpr (SWIGLU) {
-                uint32_t og[8], ou[8], oh[8];
-                float dot = grad_swiglu16(raw, kept[i], p[i], og, ou, oh);
-                grad_swiglu_store(o0, o1, g.F, wr, ib, half, og, ou, oh);
-                dot += __shfl_xor(dot, 1);
-                if (half == 0 && wr < rows && 32 * ib < g.F) g.part[(int64_t)(row0 + wr) * (g.F / 32) + ib] = dot;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const u32x4_t val = {__float_as_uint(raw[4 * c]), __float_as_uint(raw[4 * c + 1]),
-                                         __float_as_uint(raw[4 * c + 2]), __float_as_uint(raw[4 * c + 3])};
-                    const int off = 32 * ib < N ? (wr * N + 32 * ib + 16 * half + 4 * c) * 4 : 0x7ffffff0;
-                    __builtin_amdgcn_raw_buffer_store_b128(val, o0, off, 0, 0);
-                }
-            }
-        }
+        for (int i = 0; i < 2; ++i)
+            if constexpr (SWIGLU)
+                grad_swiglu_block(g, out, acc[i], ep, elane, kept[i], p[i], row0, rows, 32 * i, ib);
+            else
+                grad_dx_block(g, out, acc[i], ep, elane, 32 * i, ib);
         if (!more) {
             BIG_WAIT_VMCNT(0);          // the repeated loads land before the LDS is released
             break;
@@ -963,26 +977,29 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
             const int recs = 32 * blk < M ? 32 * N * (FP32 ? 4 : 2) : 0;
             const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
                 FP32 ? (void*)((float*)out + at) : (void*)((uint16_t*)out + at), (short)0, recs, kBigRsrcWord3);
+            // a lane's 16 bytes: row elane / 8 of 8, chunk elane % 8 of a row's 128 bytes
+            const int c = elane & 7;
             if constexpr (FP32) {
 #pragma unroll
-                for (int hv = 0; hv < 2; ++hv) {
-                    big_half_to_lds(acc[i], hv, ep, elane);
-                    const int c = elane & 15;
-                    const int col = pos.n0 + 64 * wn + 4 * c;
+                for (int jb = 0; jb < 2; ++jb) {
+                    grad_block_to_lds(acc[i][jb], ep, elane);
+                    const int col = pos.n0 + 64 * wn + 32 * jb + 4 * c;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int lr = (elane >> 4) + 4 * k;
-                        const u32x4_t val = *(const u32x4_t*)(ep + lr * 256 + ((16 * c) ^ half_swz(lr)));
-                        const int off = col < N ? ((16 * hv + lr) * N + col) * 4 : 0x7ffffff0;
-                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
+                        const int rr = (elane >> 3) + 8 * k;
+                        const u32x4_t val = *(const u32x4_t*)(ep + grad_at(rr, c));
+                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 4 : 0x7ffffff0, 0, 0);
                     }
                 }
             } else {
-                grad_rows_bf16(acc[i], ep, elane, [&](int, int rr, int c, u32x4_t val) {
-                    const int col = pos.n0 + 64 * wn + 8 * c;
-                    const int off = col < N ? (rr * N + col) * 2 : 0x7ffffff0;
-                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, off, 0, 0);
-                });
+                grad_blocks_to_lds_bf16(acc[i], ep, elane);
+                const int col = pos.n0 + 64 * wn + 8 * c;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int rr = (elane >> 3) + 8 * k;
+                    const u32x4_t val = *(const u32x4_t*)(ep + grad_at(rr, c));
+                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 2 : 0x7ffffff0, 0, 0);
+                }
             }
         }
         if (!more) {

@@ -55,7 +55,7 @@ hipError_t launch_combine(const void* rows, int in_bf16, const int32_t* row_of, 
 hipError_t launch_combine_backward(const void* d_out, int out_bf16, const void* rows, int rows_bf16,
                                    const int32_t* row_of, const float* probs, const int32_t* live, int64_t T_cap,
                                    int k, int H, void* d_rows, float* d_probs, int num_cu, hipStream_t s);
-hipError_t launch_grad_ends(const float* rows, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
+hipError_t launch_grad_ends(const uint16_t* rows, const uint8_t* scales, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
                             const int32_t* live, int64_t T_cap, int k, int H, void* d_x, float* d_probs, int num_cu,
                             hipStream_t s);
 hipError_t launch_cast_rows(const float* in, const int32_t* live, int64_t T_cap, int H, uint16_t* out, int num_cu,
@@ -200,7 +200,8 @@ struct BackwardLayout {
     WsLayout prep;
     size_t dgu;            // bf16 [R][2F]: gradient of gate and up
     size_t hp;             // bf16 [R][F]: SwiGLU rows times their probability
-    size_t dx;             // fp32 [R][H]: gradient of the grouped rows of x
+    size_t dx;             // [R][H] 16-bit codes: gradient of the grouped rows of x
+    size_t dx_scale;       // [R][H / 16]: their scale bytes
     size_t part;           // fp32 [R][F / 32]: partial sums of the probabilities' gradient
     size_t row_tok;        // int32 [R]: token of each grouped row
     size_t d_out;          // bf16 [T_cap][H]: d_out rounded, where it is given in fp32
@@ -215,7 +216,8 @@ static BackwardLayout backward_layout(const moe_ctx* h, int64_t T_cap)
     auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes > 0 ? bytes : 1); return at; };
     B.dgu = take(4 * R * F);
     B.hp = take(2 * R * F);
-    B.dx = take(4 * R * H);
+    B.dx = take(2 * R * H);
+    B.dx_scale = take(R * (H / 16));
     B.part = take(R * F / 8);
     B.row_tok = take(4 * (R + 512));        // (read ahead of the rows, up to 256 entries)
     B.d_out = take(2 * T_cap * H);
@@ -997,7 +999,8 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     g.scales = scales;
     g.dgu = (uint16_t*)(w + B.dgu);
     g.hp = (uint16_t*)(w + B.hp);
-    g.dx = (float*)(w + B.dx);
+    g.dx = (uint16_t*)(w + B.dx);
+    g.dx_scale = (uint8_t*)(w + B.dx_scale);
     g.part = (float*)(w + B.part);
     g.row_tok = (int32_t*)(w + B.row_tok);
     g.d_w1 = d_w1;
@@ -1005,7 +1008,7 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     e = launch_grad_gemms(g, T_cap, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: product launch");
     if (T_cap == 0) return MOE_OK;
-    e = launch_grad_ends(g.dx, (const int32_t*)(w + L.dst), g.part, h->F / 32, expert_ids, live_rows_dev, T_cap, h->k,
+    e = launch_grad_ends(g.dx, g.dx_scale, (const int32_t*)(w + L.dst), g.part, h->F / 32, expert_ids, live_rows_dev, T_cap, h->k,
                          h->H, d_x, d_probs, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: d_x launch");
     return MOE_OK;

@@ -12,6 +12,7 @@
 // Bound by memory: every row is touched once.  A thread takes 16 bytes of neighbouring
 // columns of a token's rows, with all k rows' accesses in flight at once.
 #include "common.h"
+#include "grad_dx.h"
 
 namespace moe {
 
@@ -411,12 +412,18 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(CombineBwdArgs a)
 
 // ---------------------------------------------------------------- experts' backward: ends
 
-// d_x from the fp32 rows of its gradient, by the first `blocks_x` workgroups, and
+// d_x from the rows of its gradient (an fp32 sum in ascending row order), by the first `blocks_x` workgroups, and
 // d_probs[t][j] of the caller's route j from the n_part partial sums of its row, 8 lanes a
 // route (in the same launch: a launch of its own cost 3 us at 64 tokens, and a thread a route
 // 27 us at 16K tokens)
 struct GradEndsArgs {
-    CombineArgs x;
+    const uint16_t* dx;        // [rows][H] codes and [rows][H / 16] scales of x's gradient
+    const uint8_t* dx_scale;
+    const int32_t* dst;        // rows by route, canonical order
+    const int32_t* live;
+    int64_t T_cap;
+    int H;
+    uint16_t* d_x;             // bf16 [T_cap][H]
     const float* part;
     int n_part;
     const int32_t* ids;
@@ -427,11 +434,44 @@ struct GradEndsArgs {
 template <int K>
 __global__ void __launch_bounds__(256) grad_ends_kernel(GradEndsArgs a)
 {
+    const int64_t T = rows_live(a.live, a.T_cap);
     if ((int)blockIdx.x < a.blocks_x) {
-        combine_tokens<K, false, true>(a.x, blockIdx.x, a.blocks_x);
+        const int nc = a.H / 8;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < T * nc; i += (int64_t)a.blocks_x * 256) {
+            const int64_t t = i / nc;
+            const int c = (int)(i - t * nc);
+            int d[K];
+            uint32_t b[K];
+            RowN<true, 8> v[K];
+#pragma unroll
+            for (int j = 0; j < K; ++j) d[j] = a.dst[t * K + j];
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                b[j] = 0;
+                v[j].zero();
+                if (d[j] >= 0) {
+                    v[j].load(a.dx, (int64_t)d[j] * a.H + 8 * c);
+                    b[j] = a.dx_scale[(int64_t)d[j] * (a.H / 16) + (c >> 1)];
+                }
+            }
+            float acc[8] = {};
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                if (d[j] < 0) continue;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    float lo, hi;
+                    dx_unpack(v[j].w[n], b[j], lo, hi);
+                    acc[2 * n] += lo;
+                    acc[2 * n + 1] += hi;
+                }
+            }
+            RowN<true, 8> o;
+            o.set(acc);
+            o.store(a.d_x, t * a.H + 8 * c);
+        }
         return;
     }
-    const int64_t T = rows_live(a.x.live, a.x.T_cap);
     const int sub = threadIdx.x & 7;
     const int64_t first = (int64_t)(blockIdx.x - a.blocks_x) * 32 + (threadIdx.x >> 3);
     for (int64_t r = first; r < T * K; r += (int64_t)(gridDim.x - a.blocks_x) * 32) {
@@ -444,7 +484,7 @@ __global__ void __launch_bounds__(256) grad_ends_kernel(GradEndsArgs a)
             const int o = a.ids[t * K + i];
             rank += (o < id || (o == id && i < j)) ? 1 : 0;
         }
-        const int d = a.x.row_of[t * K + rank];
+        const int d = a.dst[t * K + rank];
         float s = 0.0f;
         if (d >= 0)
             for (int i = sub; i < a.n_part; i += 8) s += a.part[(int64_t)d * a.n_part + i];
@@ -556,12 +596,12 @@ hipError_t launch_combine_backward(const void* d_out, int out_bf16, const void* 
     return hipGetLastError();
 }
 
-hipError_t launch_grad_ends(const float* rows, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
+hipError_t launch_grad_ends(const uint16_t* rows, const uint8_t* scales, const int32_t* dst, const float* part, int n_part, const int32_t* ids,
                             const int32_t* live, int64_t T_cap, int k, int H, void* d_x, float* d_probs, int num_cu,
                             hipStream_t s)
 {
-    const dim3 gx = rows_grid(T_cap * (H / 4), num_cu), gp = rows_grid(T_cap * k * 8, num_cu), b(256);
-    const GradEndsArgs a{{rows, dst, nullptr, live, T_cap, H, d_x}, part, n_part, ids, d_probs, (int)gx.x};
+    const dim3 gx = rows_grid(T_cap * (H / 8), num_cu), gp = rows_grid(T_cap * k * 8, num_cu), b(256);
+    const GradEndsArgs a{rows, scales, dst, live, T_cap, H, (uint16_t*)d_x, part, n_part, ids, d_probs, (int)gx.x};
 #define M(K)                                                                                   \
     case K:                                                                                    \
         hipLaunchKernelGGL(grad_ends_kernel<K>, dim3(gx.x + gp.x), b, 0, s, a);                \

@@ -92,9 +92,11 @@ def backward_ref(d_out, x, ids, probs, T, codes, scales, w1, w2, wide):
         oh = hp.abs() * (B + 2 * SIG)
         dgu, ogu = torch.cat([dg, du], dim=1), torch.cat([og, ou], dim=1)
         row = dgu @ v1
-        # a route's row: its operand's rounding, the sum's, and a rounding to bf16 at most
+        # a route's row: its operand's rounding, the sum's, and that of 16-bit integers whose
+        # scale 16 columns share: half of one, 2^-15 of the largest of the 16
         row_off = (ogu + (2 * F + 4) * S * (dgu.abs() + ogu)) @ v1.abs()
-        row_off = row_off * (1 + B) + row.abs() * B
+        top = (row.abs() + row_off).view(n, H // 16, 16).max(dim=2, keepdim=True).values
+        row_off = row_off + (2.0 ** -15 * top).expand(n, H // 16, 16).reshape(n, H)
         dx.index_add_(0, t, row)
         bx.index_add_(0, t, row_off)
         mag_x.index_add_(0, t, row.abs() + row_off)
