@@ -415,7 +415,11 @@ __device__ __forceinline__ void grad_dx_block(const GradArgs& g, const GradOut& 
 // Stores of a 32 x 32 block that every lane issues (SWIGLU: and one of partial sums)
 constexpr int grad_block_stores(bool swiglu) { return swiglu ? 6 : 3; }
 
-template <bool SWIGLU>
+// WIDE: 64-bit addresses, and a sum that may be an odd multiple of 32.  Otherwise the direct
+// loads go through descriptors, the lane's offset fixed for the tile and the place in the
+// sum a scalar offset, so that a stage's loads cost no vector instruction (16K tokens, the
+// plain product 1250 us with 64-bit addresses, 1090 so).
+template <bool SWIGLU, bool WIDE>
 __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
 {
     __shared__ __attribute__((aligned(1024))) char lds0[kBigStage];
@@ -454,6 +458,8 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
     // so that the 4 rows x 4 chunks that 32 lanes read together lie on distinct banks.
     const char* arow[kBigALoads];
     const char* wbase;
+    __amdgpu_buffer_rsrc_t ar, wr;
+    int aoff[kBigALoads];
     int s32;
     const int wlane = 16 * ((lane & 48) | ((lane & 15) ^ (4 * (lane >> 4))));
     // the routes of a tile's rows: loaded before the K loop of the tile before it
@@ -474,12 +480,33 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
                 grad_leave_token(g, p.row0, p.n0 == 0 ? p.rows : 0, rr, tok, lane);
                 src = tok;
             }
-            arow[i] = (const char*)(A + src * Kc);
+            if constexpr (WIDE) arow[i] = (const char*)(A + src * Kc);
+            else aoff[i] = (int)(SWIGLU ? src : src - p.row0) * 2 * Kc + 16 * ((lane & 7) ^ (rr & 7));
         }
-        wbase = (const char*)(W + (int64_t)p.e * Kc * N) + wlane;
+        const uint16_t* w = W + (int64_t)p.e * Kc * N;
+        if constexpr (WIDE) wbase = (const char*)w + wlane;
+        else {
+            ar = __builtin_amdgcn_make_buffer_rsrc((void*)(SWIGLU ? A : A + (int64_t)p.row0 * Kc), (short)0, 0x7fffffff,
+                                                   kBigRsrcWord3);
+            wr = __builtin_amdgcn_make_buffer_rsrc((void*)w, (short)0, 2 * Kc * N, kBigRsrcWord3);
+        }
         s32 = min(p.n0 / 32 + wid, ks - 1);
     };
     auto issue = [&](char* st, int s) {
+        const int grp = s >> 3;
+        const int w = min(32, nt16 - 32 * grp);
+        if constexpr (!WIDE) {
+#pragma unroll
+            for (int i = 0; i < kBigALoads; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, (lds_void_t*)(st + (4 * wid + i) * 1024), 16, aoff[i], 128 * s,
+                                                         0, 0);
+            const int wo = (grp * 32 * ks + s32 * w + ((4 * s) & 31)) * 1024;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void_t*)(st + kBigWOff + (4 * wid + i) * 1024), 16, wlane,
+                                                         wo + 1024 * i, 0, 0);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kBigALoads; ++i) {
             const int rr = 32 * wid + 8 * i + (lane >> 3);
@@ -488,8 +515,6 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
         }
         // (the last stage of a sum that is an odd multiple of 32 holds zeros against the
         // weights of its first half again: a NaN there is one of the same output column)
-        const int grp = s >> 3;
-        const int w = min(32, nt16 - 32 * grp);
         const char* wp = wbase + ((int64_t)grp * 32 * ks + (int64_t)s32 * w + ((4 * s) & 31)) * 1024;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -601,8 +626,8 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
 // not depend on the tile that computes them).  The weights stream from memory, each byte for
 // at most 64 rows, so what counts is loads in flight: three LDS stages of 64 along the sum
 // (8 KB of rows, 32 KB of weights), two of them in flight, a barrier a stage.  With the
-// 256-row tiles in their place (three quarters and more of every tile empty) 4,096 tokens on
-// 128 unevenly loaded experts took 858 us for both products instead of GRAD_SMALL_4K.
+// 256-row tiles in their place (three quarters and more of every tile empty) both products
+// took 467 us instead of 266 at 1,000 tokens on 64 experts, and 42 instead of 20 at 64 tokens.
 // take_big: this launch also takes the 256-row tiles, as four of 64 rows each.
 constexpr int kGradSmallStage = 40 * 1024;
 constexpr int kGradSmallW = 8 * 1024;           // weight part of a stage
@@ -812,8 +837,10 @@ __device__ __forceinline__ int grad_part(const int32_t* offsets, int E, int per_
     return e * per_e + (int)((target - before) * per_e / own);
 }
 
-// FP32: gradients of the weights in fp32, else bf16
-template <bool FP32>
+// FP32: gradients of the weights in fp32, else bf16.  WIDE: 64-bit addresses; otherwise
+// descriptors of the expert's own rows and of the gathered matrix, and an offset past them
+// for rows past the expert's last (a load out of a descriptor's range brings zeros).
+template <bool FP32, bool WIDE>
 __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
 {
     constexpr int kHalf = kBigStage / 2;            // 32 rows of P, then of Q, 512 bytes each
@@ -857,6 +884,9 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     const int odd = lane >> 5;
     const char* own[2];                    // own rows of the next half to issue, at the lane's column
     const char* gcol[2];                   // gathered matrix at the lane's column
+    __amdgpu_buffer_rsrc_t orsrc, grsrc;   // and as descriptors with offsets
+    int ooff[2], goff[2];
+    int left = 0;                          // rows from the wave's first of the next half on
     uint32_t ostep = 0;                    // bytes of 32 own rows
     int row = 0;                           // the lane's first row of the next half to issue
     struct Tok { int t[4]; };
@@ -878,11 +908,39 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
         for (int i = 0; i < 2; ++i) {
             // the slot's chunk; a column past the matrix reads its last chunk (never stored)
             const int c = 8 * ((lane & 31) ^ (4 * (2 * i + odd)));
-            gcol[i] = (const char*)(gb + min(g0 + c, H - 8));
-            own[i] = (const char*)(ob + min(o0 + c, ow - 8) + ((int64_t)p.row0 + row + 2 * i) * ow);
+            if constexpr (WIDE) {
+                gcol[i] = (const char*)(gb + min(g0 + c, H - 8));
+                own[i] = (const char*)(ob + min(o0 + c, ow - 8) + ((int64_t)p.row0 + row + 2 * i) * ow);
+            } else {
+                goff[i] = 2 * min(g0 + c, H - 8);
+                ooff[i] = 2 * (min(o0 + c, ow - 8) + (row + 2 * i) * ow);
+            }
+        }
+        left = p.cnt - 4 * wid;
+        if constexpr (!WIDE) {
+            orsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(ob + (int64_t)p.row0 * ow), (short)0, p.cnt * ow * 2,
+                                                      kBigRsrcWord3);
+            grsrc = __builtin_amdgcn_make_buffer_rsrc((void*)gb, (short)0, 0x7fffffff, kBigRsrcWord3);
         }
     };
     auto issue_rows = [&](char* st, const Tok& t) {
+        if constexpr (!WIDE) {
+            const uint32_t pitch = 2u * (uint32_t)H;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // (scalar: the offsets of the instruction's two rows)
+                const uint32_t s0 = left > 2 * i ? (uint32_t)t.t[2 * i] * pitch : 0x80000000u;
+                const uint32_t s1 = left > 2 * i + 1 ? (uint32_t)t.t[2 * i + 1] * pitch : 0x80000000u;
+                const int off = (int)(odd ? s1 : s0) + goff[i];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(orsrc, (lds_void_t*)(st + oslot + (2 * wid + i) * 1024), 16,
+                                                         ooff[i], 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(grsrc, (lds_void_t*)(st + gslot + (2 * wid + i) * 1024), 16, off, 0,
+                                                         0, 0);
+                ooff[i] += (int)ostep;
+            }
+            left -= 32;
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool in = row + 2 * i < cnt;

@@ -4,10 +4,10 @@
 
 namespace moe {
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool WIDE>
 __global__ void __launch_bounds__(512, 1) grad_rows_kernel(GradArgs g)
 {
-    grad_rows_tiles<SWIGLU>(g);
+    grad_rows_tiles<SWIGLU, WIDE>(g);
 }
 
 template <bool SWIGLU>
@@ -16,10 +16,10 @@ __global__ void __launch_bounds__(512, 1) grad_small_kernel(GradArgs g, int take
     grad_small_tiles<SWIGLU>(g, take_big != 0);
 }
 
-template <bool FP32>
+template <bool FP32, bool WIDE>
 __global__ void __launch_bounds__(512, 1) grad_weight_kernel(GradArgs g)
 {
-    grad_weight_tiles<FP32>(g);
+    grad_weight_tiles<FP32, WIDE>(g);
 }
 
 hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int num_cu, hipStream_t s)
@@ -27,12 +27,24 @@ hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int nu
     // a multiple of 8 workgroups: the tiles are split over the 8 XCDs
     const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
     const int take_big = T_cap <= 1024;
-    if (!take_big) hipLaunchKernelGGL(grad_rows_kernel<true>, grid, block, 0, s, g);
+    // 32-bit byte offsets: in the gathered rows, in an expert's rows (at most one a token) and in
+    // its weights
+    const int64_t lim = (int64_t)1 << 31;
+    const bool wide = T_cap * 2 * g.H >= lim || T_cap * 4 * g.F >= lim || (int64_t)4 * g.F * g.H >= lim;
+    if (!take_big) {
+        if (wide || g.H % 64) hipLaunchKernelGGL((grad_rows_kernel<true, true>), grid, block, 0, s, g);
+        else hipLaunchKernelGGL((grad_rows_kernel<true, false>), grid, block, 0, s, g);
+    }
     hipLaunchKernelGGL(grad_small_kernel<true>, grid, block, 0, s, g, take_big);
-    if (!take_big) hipLaunchKernelGGL(grad_rows_kernel<false>, grid, block, 0, s, g);
+    if (!take_big) {
+        if (wide) hipLaunchKernelGGL((grad_rows_kernel<false, true>), grid, block, 0, s, g);
+        else hipLaunchKernelGGL((grad_rows_kernel<false, false>), grid, block, 0, s, g);
+    }
     hipLaunchKernelGGL(grad_small_kernel<false>, grid, block, 0, s, g, take_big);
-    if (fp32) hipLaunchKernelGGL(grad_weight_kernel<true>, grid, block, 0, s, g);
-    else hipLaunchKernelGGL(grad_weight_kernel<false>, grid, block, 0, s, g);
+    if (fp32 && wide) hipLaunchKernelGGL((grad_weight_kernel<true, true>), grid, block, 0, s, g);
+    else if (fp32) hipLaunchKernelGGL((grad_weight_kernel<true, false>), grid, block, 0, s, g);
+    else if (wide) hipLaunchKernelGGL((grad_weight_kernel<false, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((grad_weight_kernel<false, false>), grid, block, 0, s, g);
     return hipGetLastError();
 }
 
