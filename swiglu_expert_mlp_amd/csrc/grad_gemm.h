@@ -673,16 +673,22 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
     // as in the 256-row tiles: rows 8 wid + lane / 8, the wave's 32-column weight block
     const char* arow;
     const char* wbase;
-    int s32, look = 0;
+    int s32, look = 0, route[2] = {};
     const int myrow = 8 * wid + (lane >> 3), achunk = (lane & 7) ^ (lane >> 3);
     const int wlane = 16 * ((lane & 48) | ((lane & 15) ^ (4 * (lane >> 4))));
     auto lookup = [&](const TilePos& p) {
-        if constexpr (SWIGLU) look = g.perm_src[p.row0 + min(myrow, p.rows - 1)];
+        if constexpr (SWIGLU) {
+            look = g.perm_src[p.row0 + min(myrow, p.rows - 1)];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) route[i] = g.perm_src[p.row0 + min(32 * i + (lane >> 1), p.rows - 1)];
+        }
     };
     auto sources = [&](const TilePos& p) {
         int64_t src = p.row0 + min(myrow, p.rows - 1);
         if constexpr (SWIGLU) {
             const int tok = look / g.topk;
+            // (the routes have landed with it: awaited here, not among the next loads in flight)
+            asm volatile("" : "+v"(route[0]), "+v"(route[1]));
             grad_leave_token(g, p.row0, p.n0 == 0 ? p.rows : 0, myrow, tok, lane);
             src = tok;
         }
@@ -717,7 +723,9 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
     int tile = advance(xcd_first_tile(), pos);
     if (tile >= total) return;
     constexpr int kStores = 2 * grad_block_stores(SWIGLU);
-    constexpr int kLook = SWIGLU ? 1 : 0;
+    // the epilogue's own loads (kept values and probabilities) and the next tile's lookup, all
+    // before the K loop: after it they were two round trips of every tile
+    constexpr int kLook = SWIGLU ? 11 : 0;
     lookup(pos);
     sources(pos);
     issue(lds0, 0);
@@ -730,6 +738,17 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
         const int next = advance(tile + (int)gridDim.x, npos);
         const bool more = next < total;
         if (!more) npos = pos;
+        const int half = lane & 1, prow = lane >> 1;
+        const int ib = n0 / 32 + wid;
+        GradKept kept[2];
+        float p[2];
+        if constexpr (SWIGLU) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                p[i] = g.prob[route[i]];
+                kept[i] = grad_kept(g, row0 + min(32 * i + prow, rows - 1), min(ib, g.F / 32 - 1), half);
+            }
+        }
         lookup(npos);
         f32x16 acc[2];
 #pragma unroll
@@ -770,21 +789,8 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
             step(Now{}, s, lds1, lds0);
             if (s + 1 < nst) step(Now{}, s + 1, lds2, lds1);
         }
-        // lane = row lane / 2 of 32 and 16 of the wave's 32 columns
         int elane = lane;
         asm volatile("" : "+v"(elane));
-        const int half = elane & 1, prow = elane >> 1;
-        const int ib = n0 / 32 + wid;
-        GradKept kept[2];
-        float p[2];
-        if constexpr (SWIGLU) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int64_t row = row0 + min(32 * i + prow, rows - 1);
-                p[i] = g.prob[g.perm_src[row]];
-                kept[i] = grad_kept(g, row, min(ib, g.F / 32 - 1), half);
-            }
-        }
         __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();               // every wave has read its last stage
         sources(npos);
@@ -1035,7 +1041,9 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
             const int recs = 32 * blk < M ? 32 * N * (FP32 ? 4 : 2) : 0;
             const __amdgpu_buffer_rsrc_t orr = __builtin_amdgcn_make_buffer_rsrc(
                 FP32 ? (void*)((float*)out + at) : (void*)((uint16_t*)out + at), (short)0, recs, kBigRsrcWord3);
-            // a lane's 16 bytes: row elane / 8 of 8, chunk elane % 8 of a row's 128 bytes
+            // a lane's 16 bytes: row elane / 8 of 8, chunk elane % 8 of a row's 128 bytes.  The
+            // gradients are not read here again: non-temporal (16K tokens 1781 -> 1737 us,
+            // 4,096 776 -> 751, 1,000 the same)
             const int c = elane & 7;
             if constexpr (FP32) {
 #pragma unroll
@@ -1046,7 +1054,8 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
                     for (int k = 0; k < 4; ++k) {
                         const int rr = (elane >> 3) + 8 * k;
                         const u32x4_t val = *(const u32x4_t*)(ep + grad_at(rr, c));
-                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 4 : 0x7ffffff0, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 4 : 0x7ffffff0, 0,
+                                                               kNonTemporal);
                     }
                 }
             } else {
@@ -1056,7 +1065,7 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
                 for (int k = 0; k < 4; ++k) {
                     const int rr = (elane >> 3) + 8 * k;
                     const u32x4_t val = *(const u32x4_t*)(ep + grad_at(rr, c));
-                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 2 : 0x7ffffff0, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(val, orr, col < N ? (rr * N + col) * 2 : 0x7ffffff0, 0, kNonTemporal);
                 }
             }
         }
