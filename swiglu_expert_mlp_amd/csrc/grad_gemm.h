@@ -265,9 +265,13 @@ __device__ __forceinline__ void grad_read16(const char* ep, int row, int h, floa
     }
 }
 
+// Two values rounded to bf16 (nearest even) by one instruction (rounded one by one and put
+// together they were four, a sixth of the SwiGLU's backward)
 __device__ __forceinline__ uint32_t grad_pair(float a, float b)
 {
-    return (uint32_t)f32_to_bf16_bits(a) | ((uint32_t)f32_to_bf16_bits(b) << 16);
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 
 __device__ __forceinline__ void grad_blocks_to_lds_bf16(const f32x16 (&acc)[2], char* ep, int lane)
