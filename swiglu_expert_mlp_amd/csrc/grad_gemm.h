@@ -179,57 +179,61 @@ __device__ __forceinline__ void grad_kloop(int nst, char* s0, char* s1, f32x16 (
 
 // grad_kloop with the two stages in halves of 32 along the sum (h0, h1 the first stage's, h2,
 // h3 the second's) that are refilled one by one, so three halves instead of one stage are in
-// flight, for two barriers a stage.  LOADS: direct loads of a half per wave; on entry four
-// halves are in flight.  read(Q, half, frag): sub-step Q = 0, 1 of a half; issue(half): the
-// next half not issued yet (past the last stage: zeros).
+// flight, for two barriers a stage.  LOADS: direct loads of a half per wave.  On entry four
+// halves are in flight, the last of them h3 or h1, followed by AFTER stores.  read(Q, half,
+// frag): sub-step Q = 0, 1 of a half; issue(slot, half): refills that half, with the tile's
+// next one or, past its last, with the next tile's half of that slot.
 template <int READS, int AFTER, int LOADS, typename Read, typename Issue>
 __device__ __forceinline__ void grad_kloop_halves(int nst, char* h0, char* h1, char* h2, char* h3,
                                                   f32x16 (&acc)[4][2], Read read, Issue issue)
 {
-    static_assert(AFTER + 3 * LOADS <= 63, "vmcnt bound");
+    static_assert(AFTER + 2 * LOADS <= 63, "vmcnt bound");
     GradFrag x, y;
     using Q0 = std::integral_constant<int, 0>;
     using Q1 = std::integral_constant<int, 1>;
-    using Now = std::integral_constant<int, 0>;
-    using Aft = std::integral_constant<int, AFTER>;
-    BIG_WAIT_VMCNT(AFTER + 3 * LOADS);
+    BIG_WAIT_VMCNT(AFTER + LOADS);
     __builtin_amdgcn_s_barrier();
     read(Q0{}, h0, x);
-    // the next half landed (the two halves after it, and N stores, may be in flight), every
-    // wave's reads of `cur` are done: `cur` is refilled
-    auto boundary = [&](auto NC, char* cur) {
+    // N: the operations younger than the next half that may be in flight.  It has landed then,
+    // and every wave's reads of `cur` are done: `cur` is refilled
+    auto boundary = [&](auto NC, auto SC, char* cur) {
         __builtin_amdgcn_sched_barrier(0);
-        BIG_WAIT_VMCNT(2 * LOADS + decltype(NC)::value);
+        BIG_WAIT_VMCNT(decltype(NC)::value);
         __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        issue(cur);
+        issue(SC, cur);
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto body = [&](auto NC, char* a, char* b) {
+    auto body = [&](auto NC, auto SC, char* a, char* b) {
         grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, a, n); }, y);
-        boundary(NC, a);
+        boundary(NC, SC, a);
         grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, b, n); }, x);
         grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, b, n); }, y);
     };
-    auto into = [&](auto NC, char* b, char* c) {
-        boundary(NC, b);
+    auto into = [&](auto NC, auto SC, char* b, char* c) {
+        boundary(NC, SC, b);
         grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, c, n); }, x);
     };
-    body(Aft{}, h0, h1);
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+    using S3 = std::integral_constant<int, 3>;
+    using Two = std::integral_constant<int, 2 * LOADS>;
+    body(std::integral_constant<int, AFTER>{}, S0{}, h0, h1);       // the first four have landed
     if (nst > 1) {
-        into(Aft{}, h1, h2);
-        body(Aft{}, h2, h3);
+        into(std::integral_constant<int, AFTER + LOADS>{}, S1{}, h1, h2);
+        body(std::integral_constant<int, AFTER + 2 * LOADS>{}, S2{}, h2, h3);
         int s = 2;
         for (; s + 2 <= nst; s += 2) {
-            into(Now{}, h3, h0);
-            body(Now{}, h0, h1);
-            into(Now{}, h1, h2);
-            body(Now{}, h2, h3);
+            into(Two{}, S3{}, h3, h0);
+            body(Two{}, S0{}, h0, h1);
+            into(Two{}, S1{}, h1, h2);
+            body(Two{}, S2{}, h2, h3);
         }
         if (s < nst) {
-            into(Now{}, h3, h0);
-            body(Now{}, h0, h1);
+            into(Two{}, S3{}, h3, h0);
+            body(Two{}, S0{}, h0, h1);
         }
     }
     grad_mma(acc, y);
@@ -890,97 +894,137 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     // its token, which comes by a scalar load a half ahead from the table that the first
     // product left (with the row and its token worked out anew each stage these were 4.6
     // vector instructions per MFMA).
-    int cnt = 0, oslot = 0, gslot = 0;     // rows; where own and gathered rows lie in a half
+    // The loads run ahead across tiles: a half that the tile has no more use for is refilled
+    // with the next tile's, whose sources are worked out before the tile's K loop.
     const int odd = lane >> 5;
-    const char* own[2];                    // own rows of the next half to issue, at the lane's column
-    const char* gcol[2];                   // gathered matrix at the lane's column
-    __amdgpu_buffer_rsrc_t orsrc, grsrc;   // and as descriptors with offsets
-    int ooff[2], goff[2];
-    int left = 0;                          // rows from the wave's first of the next half on
-    uint32_t ostep = 0;                    // bytes of 32 own rows
-    int row = 0;                           // the lane's first row of the next half to issue
     struct Tok { int t[4]; };
-    const int32_t* toks = nullptr;         // the wave's first token of the next half to issue
-    Tok tok;
+    struct Src {
+        const char *own[2], *gcol[2];          // WIDE: own rows, gathered matrix, at the lane's column
+        const uint16_t *obase, *gbase;         // else what their descriptors hold, and offsets
+        int orecs;
+        int ooff[2], goff[2];
+        uint32_t ostep;                        // bytes of 32 own rows
+        int left;                              // rows from the wave's first of the half on
+        int oslot, gslot;                      // where own and gathered rows lie in a half
+    };
     auto tokens = [&](const int32_t* p) { return Tok{{ld_const(p), ld_const(p + 1), ld_const(p + 2), ld_const(p + 3)}}; };
     auto sources = [&](const TilePos& p) {
+        Src c;
         const int ow = p.w2 ? F : 2 * F;                         // columns of the own matrix
         const int o0 = p.w2 ? p.n0 : p.m0, g0 = p.w2 ? p.m0 : p.n0;
         const uint16_t* ob = p.w2 ? g.hp : g.dgu;
         const uint16_t* gb = p.w2 ? g.d_out : g.x;
-        cnt = p.cnt;
-        oslot = p.w2 ? kHalfQ : 0;
-        gslot = p.w2 ? 0 : kHalfQ;
-        ostep = 64u * (uint32_t)ow;
-        row = 4 * wid + odd;
-        toks = g.row_tok + p.row0 + 4 * wid;
+        c.oslot = p.w2 ? kHalfQ : 0;
+        c.gslot = p.w2 ? 0 : kHalfQ;
+        c.ostep = 64u * (uint32_t)ow;
+        c.left = p.cnt - 4 * wid;
+        const int row = 4 * wid + odd;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             // the slot's chunk; a column past the matrix reads its last chunk (never stored)
-            const int c = 8 * ((lane & 31) ^ (4 * (2 * i + odd)));
+            const int k = 8 * ((lane & 31) ^ (4 * (2 * i + odd)));
             if constexpr (WIDE) {
-                gcol[i] = (const char*)(gb + min(g0 + c, H - 8));
-                own[i] = (const char*)(ob + min(o0 + c, ow - 8) + ((int64_t)p.row0 + row + 2 * i) * ow);
+                c.gcol[i] = (const char*)(gb + min(g0 + k, H - 8));
+                c.own[i] = (const char*)(ob + min(o0 + k, ow - 8) + ((int64_t)p.row0 + row + 2 * i) * ow);
             } else {
-                goff[i] = 2 * min(g0 + c, H - 8);
-                ooff[i] = 2 * (min(o0 + c, ow - 8) + (row + 2 * i) * ow);
+                c.goff[i] = 2 * min(g0 + k, H - 8);
+                c.ooff[i] = 2 * (min(o0 + k, ow - 8) + (row + 2 * i) * ow);
             }
         }
-        left = p.cnt - 4 * wid;
-        if constexpr (!WIDE) {
-            orsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(ob + (int64_t)p.row0 * ow), (short)0, p.cnt * ow * 2,
-                                                      kBigRsrcWord3);
-            grsrc = __builtin_amdgcn_make_buffer_rsrc((void*)gb, (short)0, 0x7fffffff, kBigRsrcWord3);
-        }
+        c.obase = ob + (int64_t)p.row0 * ow;
+        c.gbase = gb;
+        c.orecs = WIDE ? 0 : p.cnt * ow * 2;
+        return c;
     };
-    auto issue_rows = [&](char* st, const Tok& t) {
+    // half `h` of c's rows into st, h counted from where c's offsets stand
+    auto issue_rows = [&](char* st, const Src& c, int h, const Tok& t) {
+        const int left = c.left - 32 * h;
+        const uint32_t pitch = 2u * (uint32_t)H;
+        __amdgpu_buffer_rsrc_t orsrc, grsrc;
         if constexpr (!WIDE) {
-            const uint32_t pitch = 2u * (uint32_t)H;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // (scalar: the offsets of the instruction's two rows)
-                const uint32_t s0 = left > 2 * i ? (uint32_t)t.t[2 * i] * pitch : 0x80000000u;
-                const uint32_t s1 = left > 2 * i + 1 ? (uint32_t)t.t[2 * i + 1] * pitch : 0x80000000u;
-                const int off = (int)(odd ? s1 : s0) + goff[i];
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(orsrc, (lds_void_t*)(st + oslot + (2 * wid + i) * 1024), 16,
-                                                         ooff[i], 0, 0, 0);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(grsrc, (lds_void_t*)(st + gslot + (2 * wid + i) * 1024), 16, off, 0,
-                                                         0, 0);
-                ooff[i] += (int)ostep;
-            }
-            left -= 32;
-            return;
+            orsrc = __builtin_amdgcn_make_buffer_rsrc((void*)c.obase, (short)0, c.orecs, kBigRsrcWord3);
+            grsrc = __builtin_amdgcn_make_buffer_rsrc((void*)c.gbase, (short)0, 0x7fffffff, kBigRsrcWord3);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool in = row + 2 * i < cnt;
-            const uint32_t tk = (uint32_t)(odd ? t.t[2 * i + 1] : t.t[2 * i]);
-            const char* gp = gcol[i] + (uint64_t)tk * (2u * (uint32_t)H);
-            big_load_block(in ? own[i] : (const char*)grad_zeros, st + oslot + (2 * wid + i) * 1024);
-            big_load_block(in ? gp : (const char*)grad_zeros, st + gslot + (2 * wid + i) * 1024);
-            own[i] += ostep;
+            void* const od = st + c.oslot + (2 * wid + i) * 1024;
+            void* const gd = st + c.gslot + (2 * wid + i) * 1024;
+            if constexpr (WIDE) {
+                const bool in = left > 2 * i + odd;
+                const uint32_t tk = (uint32_t)(odd ? t.t[2 * i + 1] : t.t[2 * i]);
+                big_load_block(in ? c.own[i] + (uint64_t)c.ostep * h : (const char*)grad_zeros, od);
+                big_load_block(in ? c.gcol[i] + (uint64_t)tk * pitch : (const char*)grad_zeros, gd);
+            } else {
+                // (scalar: the offsets of the instruction's two rows)
+                const uint32_t s0 = left > 2 * i ? (uint32_t)t.t[2 * i] * pitch : 0x80000000u;
+                const uint32_t s1 = left > 2 * i + 1 ? (uint32_t)t.t[2 * i + 1] * pitch : 0x80000000u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(orsrc, (lds_void_t*)od, 16, c.ooff[i] + (int)c.ostep * h, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(grsrc, (lds_void_t*)gd, 16, (int)(odd ? s1 : s0) + c.goff[i], 0, 0, 0);
+            }
         }
-        row += 32;
     };
-    auto issue = [&](char* st) {
-        issue_rows(st, tok);
-        toks += 32;
-        tok = tokens(toks);                // (the table is 256 entries longer than the rows)
-    };
-    // a tile's first four halves, and the tokens of its fifth; the tokens are loaded before the
-    // K loop of the tile before it
-    Tok ahead[4];
-    auto lookup = [&](const TilePos& p) {
+    // cur stands at the tile's next half to issue (the fifth when its K loop begins), with that
+    // half's tokens; nxt at the next tile's first, with the tokens of its first four
+    Src cur, nxt;
+    const int32_t* toks = nullptr;
+    Tok tok, ahead[4];
+    int to_issue = 0;                      // halves of the tile that are not issued yet
+    auto look_ahead = [&](const TilePos& p) {
+        nxt = sources(p);
 #pragma unroll
         for (int h = 0; h < 4; ++h) ahead[h] = tokens(g.row_tok + p.row0 + 32 * h + 4 * wid);
     };
-    auto start = [&](const TilePos& p) {
-        sources(p);
-        issue_rows(lds0, ahead[0]);
-        issue_rows(lds1, ahead[1]);
-        issue_rows(lds2, ahead[2]);
-        issue_rows(lds3, ahead[3]);
-        toks += 128;
+    auto issue = [&](auto SC, char* st) {
+        // (one set of loads whose sources are chosen: with a set on either side of a branch the
+        // compiler waited for all in flight before later fragment reads)
+        constexpr int j = decltype(SC)::value;
+        const bool own_half = to_issue > 0;
+        auto pick = [&](auto a, auto b) { return own_half ? a : b; };       // (by value)
+        Src c = nxt;
+        Tok t = ahead[j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (WIDE) {
+                c.own[i] = pick(cur.own[i], nxt.own[i] + (uint64_t)nxt.ostep * j);
+                c.gcol[i] = pick(cur.gcol[i], nxt.gcol[i]);
+                cur.own[i] += cur.ostep;
+            } else {
+                c.ooff[i] = pick(cur.ooff[i], nxt.ooff[i] + (int)nxt.ostep * j);
+                c.goff[i] = pick(cur.goff[i], nxt.goff[i]);
+                cur.ooff[i] += (int)cur.ostep;
+            }
+        }
+        c.obase = pick(cur.obase, nxt.obase);
+        c.gbase = pick(cur.gbase, nxt.gbase);
+        c.orecs = pick(cur.orecs, nxt.orecs);
+        c.left = pick(cur.left, nxt.left - 32 * j);
+        c.oslot = pick(cur.oslot, nxt.oslot);
+        c.gslot = pick(cur.gslot, nxt.gslot);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.t[i] = pick(tok.t[i], ahead[j].t[i]);
+        issue_rows(st, c, 0, t);
+        cur.left -= 32;
+        toks += 32;
+        tok = tokens(pick(toks, g.row_tok));      // (the table is 512 entries longer than the rows)
+        --to_issue;
+    };
+    auto stages_of = [&](const TilePos& p) { return (p.cnt + 63) / 64; };
+    // the halves of the next tile that the K loop of `p` has not issued (bit j: slot j), then
+    // the next tile becomes the current one
+    auto turn = [&](int missing, const TilePos& p) {
+        if (missing & 1) issue_rows(lds0, nxt, 0, ahead[0]);
+        if (missing & 2) issue_rows(lds1, nxt, 1, ahead[1]);
+        if (missing & 4) issue_rows(lds2, nxt, 2, ahead[2]);
+        if (missing & 8) issue_rows(lds3, nxt, 3, ahead[3]);
+        cur = nxt;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (WIDE) cur.own[i] += 4 * (uint64_t)cur.ostep;
+            else cur.ooff[i] += 4 * (int)cur.ostep;
+        }
+        cur.left -= 128;
+        to_issue = 2 * stages_of(p) - 4;
+        toks = g.row_tok + p.row0 + 128 + 4 * wid;
         tok = tokens(toks);
     };
     // fragments of sub-step Q of a half: rows 16 Q + 8 (l / 32) + {0, 4} + (l % 16) / 4, the
@@ -1007,8 +1051,8 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
     int tile = grad_part(g.offsets, g.E, per_e, xcd, lane) + (int)(blockIdx.x >> 3);
     if (tile >= end) return;
     TilePos pos = locate(tile), npos = pos;
-    lookup(pos);
-    start(pos);
+    look_ahead(pos);
+    turn(15, pos);
     constexpr int kStores = FP32 ? 32 : 16;
     grad_dummy_stores<kStores>(g.dgu, lane);
     char* const ep = lds_x + wid * kBigEpi;
@@ -1023,14 +1067,16 @@ __device__ __forceinline__ void grad_weight_tiles(const GradArgs& g)
         const int next = tile + (int)(gridDim.x >> 3);
         const bool more = next < end;
         if (more) npos = locate(next);
-        lookup(npos);
-        if (pos.cnt > 0)
-            grad_kloop_halves<12, kStores, 4>((pos.cnt + 63) / 64, lds0, lds1, lds2, lds3, acc, read, issue);
+        look_ahead(npos);
+        const int nst = stages_of(pos);
+        if (nst > 0)
+            grad_kloop_halves<12, kStores, 4>(nst, lds0, lds1, lds2, lds3, acc, read, issue);
         else
             BIG_WAIT_VMCNT(kStores);                // its loads land before the next tile's go out
         __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
-        start(npos);
+        // a K loop of n stages refills 2 n - 1 halves: all but its last, or with one stage the first
+        turn(nst == 0 ? 15 : nst == 1 ? 14 : nst & 1 ? 2 : 8, npos);
 
         int elane = lane;
         asm volatile("" : "+v"(elane));
