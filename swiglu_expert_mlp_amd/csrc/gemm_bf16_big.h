@@ -376,7 +376,9 @@ constexpr int kCkptStores = 16;
 // WPOL, RPOL: the cache policies of the weights' loads and of FC2's row stores.
 // CKPT: FC1 also stores its gate and up values in 8 bits (checkpoint.h): through the wave's
 // LDS region 16 rows at a time, so that a lane holds 16 neighbouring columns of a row (half
-// a block; the block's other half is the next lane's), quantizes them and stores 16 bytes.
+// a block; the block's other half is the next lane's), quantizes them and stores 16 bytes
+// (a forward of 4,096 unevenly routed tokens 718 us with its checkpoint, 710 without; 64
+// tokens, hidden 128, 24.4 and 22.2).
 template <typename Op, bool FC1, bool PROB, int WPOL = FC1 ? 0 : kNonTemporal, int RPOL = 0, bool CKPT = false>
 __device__ __forceinline__ void big_tiles(const GemmArgs& g, int n_mt)
 {

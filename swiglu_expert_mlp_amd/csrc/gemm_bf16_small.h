@@ -248,9 +248,9 @@ __device__ __forceinline__ void small_finalize(const GemmArgs& g, SmallFinLds* f
 // from the header).
 // CKPT: FC1 also stores its gate and up values in 8 bits (ckpt_store_half), through the ring
 // stage after the last one: whoever is past the K loop has passed the last step's barrier,
-// so every wave's reads of that stage are done.  (Quantized in place instead, the 32 lanes of
-// a half wave reducing each row's block and storing a byte each, the 64-row FC1 of 4,096
-// tokens on 128 unevenly loaded experts took 480 us beside the 256-row one, 942 a forward.)
+// so every wave's reads of that stage are done.  (Quantized in place, the 32 lanes of a half
+// wave reducing each row's block and storing a byte each, this launch took 480 us of 4,096
+// tokens on 128 unevenly loaded experts instead of 475.)
 template <typename Op, bool FC1, bool PROB, int FUSE, int WPOL, bool CKPT = false>
 __device__ __forceinline__ void small_tiles(const GemmArgs& g, char* smem, int n_small, int n_big,
                                             int e0, int row00, int need = 0, SmallFinLds* fin_lds = nullptr)

