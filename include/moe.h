@@ -35,9 +35,9 @@
  *     They and `stream` belong to the device current at the call.
  *   - The library never allocates device memory and never synchronizes the
  *     stream, except moe_check (which reads the error word) and
- *     moe_get_indices (which copies to host).  moe_route, moe_forward and
- *     the training calls only enqueue work on `stream`, so they can be captured
- *     in a HIP graph; a bf16 or int8 forward above 1024 tokens may run its
+ *     moe_get_indices (which copies to host).  moe_route, moe_forward, the
+ *     training calls, moe_dispatch and moe_combine_rows only enqueue work on
+ *     `stream`, so they can be captured in a HIP graph; a bf16 or int8 forward above 1024 tokens may run its
  *     64-row GEMM launches on a side stream of the library (one per GPU,
  *     default priority, created by the first bf16 or int8 weight load there
  *     and kept until the process ends), forked from `stream` and joined back
@@ -182,7 +182,8 @@ moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_sc
  * same call reads, so a fresh allocation (or one left by another handle) can
  * be passed as is.  Its bytes are the library's until the work enqueued on it
  * has finished; moe_get_indices, moe_get_rows and moe_check read the state of
- * the last moe_route / moe_forward that used it. */
+ * the last moe_route / moe_forward that used it (the first two refuse one that
+ * moe_backward, moe_dispatch or moe_balance used since). */
 size_t moe_workspace_bytes(moe_handle h, int64_t T_cap);
 
 /* Router (Megatron-Core `_route`): for each live token, softmax over the E
@@ -429,8 +430,10 @@ size_t moe_backward_workspace_bytes(moe_handle h, int64_t T_cap);
  * s = 1 / (1 + exp(-g)) and h = g s u:
  *   raw      = W2_e^T d_out[t]                     (fp32)
  *   d_gate   = p raw u s (1 + g (1 - s)),  d_up = p raw g s      (rounded to bf16)
- *   d_x[t]   = sum over j of W1_e^T [d_gate; d_up]  (each route's rounded to bf16,
- *              the sum over ascending experts fp32)
+ *   d_x[t]   = sum over j of W1_e^T [d_gate; d_up]  (each route's is kept in 16 bits
+ *              with a power of two per 16 columns, within 2^-15 of the largest of
+ *              the 16, or in bf16 where one is not finite; the sum over ascending
+ *              experts is fp32)
  *   d_w1[e]  = sum over rows of [d_gate; d_up] x[t]^T
  *   d_w2[e]  = sum over rows of d_out[t] (p h)^T    (p h rounded to bf16)
  *   d_probs[t][j] = sum over the FFN of raw h       (fp32)

@@ -68,7 +68,9 @@ hipError_t launch_quant_x(const uint16_t* x, int64_t T_cap, const int32_t* live,
 #include "grad_args.h"
 
 namespace moe {
-hipError_t launch_grad_gemms(const GradArgs& g, int64_t T_cap, bool fp32, int num_cu, hipStream_t s);
+bool grad_takes_big(int64_t T_cap);
+hipError_t launch_grad_rows(const GradArgs& g, int64_t T_cap, int num_cu, hipStream_t s, hipStream_t small);
+hipError_t launch_grad_weights(const GradArgs& g, int64_t T_cap, bool fp32, int num_cu, hipStream_t s);
 hipError_t launch_gemm_bf16(bool fc1, const GemmArgs& g, int num_cu, hipStream_t s, hipEvent_t t0,
                             hipEvent_t t1, hipStream_t s_small = nullptr);
 hipError_t launch_gemm_bf16_fused(const GemmArgs& g1, const GemmArgs& g2, int num_cu, hipStream_t s,
@@ -1005,7 +1007,28 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     g.row_tok = (int32_t*)(w + B.row_tok);
     g.d_w1 = d_w1;
     g.d_w2 = d_w2;
-    e = launch_grad_gemms(g, T_cap, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
+    // the 64-row tiles' products beside the 256-row ones, as the forward's stages and under its rule
+    const SideStream* ss = (h->device >= 0 && h->device < kMaxScratchDevices) ? &g_side[h->device] : nullptr;
+    std::unique_lock<std::mutex> lock(g_side_mu, std::defer_lock);
+    bool forked = !grad_takes_big(T_cap) && ss && ss->s && T_cap * h->k < (int64_t)4 * kBigMin * h->E;
+    if (forked) {
+        lock.lock();
+        forked = side_stream_free(*ss, stream);
+    }
+    if (forked) {
+        e = hipEventRecord(ss->fork, stream);
+        if (e == hipSuccess) e = hipStreamWaitEvent(ss->s, ss->fork, 0);
+        if (e != hipSuccess) return hip_fail(e, "moe_backward: fork");
+    }
+    const hipError_t rows_e = launch_grad_rows(g, T_cap, h->num_cu, stream, forked ? ss->s : stream);
+    if (forked) {
+        e = hipEventRecord(ss->join, ss->s);
+        if (e == hipSuccess) e = hipStreamWaitEvent(stream, ss->join, 0);
+        if (e != hipSuccess) return hip_fail(e, "moe_backward: join");
+    }
+    if (lock.owns_lock()) lock.unlock();
+    if (rows_e != hipSuccess) return hip_fail(rows_e, "moe_backward: product launch");
+    e = launch_grad_weights(g, T_cap, d_w_type == MOE_TYPE_FP32, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: product launch");
     if (T_cap == 0) return MOE_OK;
     e = launch_grad_ends(g.dx, g.dx_scale, (const int32_t*)(w + L.dst), g.part, h->F / 32, expert_ids, live_rows_dev, T_cap, h->k,
@@ -1129,6 +1152,8 @@ moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t*
     hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "moe_get_indices: header copy");
+    if (hdr.mark == kErrMark && hdr.tag == 0)
+        return fail(MOE_ERR_INVALID_ARG, "moe_get_indices: the workspace was last used by a call that is no forward");
     const int64_t R = (int64_t)hdr.T * h->k;
     if (counts) e = hipMemcpy(counts, w + L.counts, 4 * h->E, hipMemcpyDeviceToHost);
     if (e == hipSuccess && offsets)
@@ -1156,6 +1181,8 @@ moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_
     hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "moe_get_rows: header copy");
+    if (hdr.mark == kErrMark && hdr.tag == 0)
+        return fail(MOE_ERR_INVALID_ARG, "moe_get_rows: the workspace was last used by a call that is no forward");
     const size_t n = (size_t)hdr.n_rows;
     const size_t T = (size_t)hdr.T;
     const size_t R = T * h->k;

@@ -325,6 +325,33 @@ def test_combine_rows_outside_and_infinities():
     assert d_p[1, 0] == 0 and d_p[1, 1] == 0 and d_p[1, 2].isinf() and (d_rows[[3, 5]] == 0).all()
 
 
+def test_a_workspace_of_another_call_holds_no_forward():
+    """Indices and rows are read from a forward's workspace only, and so is the gradient of the
+    combine's probabilities; a forward on the same memory makes them readable again."""
+    T, E, H, F, k = 40, 8, 64, 96, 2
+    for T in (40, 300):                                  # dispatch in one launch and in three
+        c = _make(T, T, E, H, F, k, 0, seed=31)
+        m = _moe(c, k)
+        ws = _garbage(max(m.new_workspace(T).numel(), m.new_backward_workspace(T).numel()))
+        out, codes, scales = m.forward_checkpoint(c["x"], c["ids"], c["probs"], c["live"], ws=ws)
+        want = m.get_indices(ws, T)
+        d = m.probs_backward(c["d_out"], c["ids"], ws)
+        for other in (lambda: m.dispatch(c["x"], c["ids"], c["live"], ws=ws),
+                      lambda: m.backward(c["d_out"], c["x"], c["ids"], c["probs"], c["live"], codes, scales, ws=ws)):
+            other()
+            assert m.check(ws) == 0
+            with pytest.raises(ValueError):
+                m.get_indices(ws, T)
+            with pytest.raises(ValueError):
+                m.get_rows(ws, T, want["n_rows"], T)
+            m.probs_backward(c["d_out"], c["ids"], ws)
+            assert m.check(ws) == 32                     # no rows: not written
+            m.forward(c["x"], c["ids"], c["probs"], c["live"], ws=ws)
+            got = m.get_indices(ws, T)
+            assert all((got[n] == want[n]).all() if hasattr(got[n], "all") else got[n] == want[n] for n in want)
+            assert torch.equal(m.probs_backward(c["d_out"], c["ids"], ws), d)
+
+
 def test_whole_step_together():
     """A training step with experts of the library and one with the caller's own experts
     between dispatch and combine agree with fp64 autograd of the layer."""
@@ -460,3 +487,37 @@ def test_offsets_past_32_bits(H, F):
     assert torch.equal(grads[0][pick], sg[0]) and torch.equal(grads[3][pick], sg[3])
     for v in grads:
         assert v.isfinite().all()
+
+
+@pytest.mark.parametrize("H,F", [(2080, 64), (64, 2080)])
+def test_weights_gradients_past_32_bits(H, F):
+    """The gradients of the weights over rows past 4 GiB are the sums of those over pieces of
+    the tokens, which are smaller than 2 GiB."""
+    T, E, k, piece = 530000, 8, 2, 53000
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    from swiglu_expert_mlp_amd import MoE
+    g = torch.Generator(device="cuda").manual_seed(4)
+    m = MoE(E, H, F, k)
+    m.load_weights((torch.randn((E, 2 * F, H), generator=g, device="cuda") * 0.05).bfloat16(),
+                   (torch.randn((E, H, F), generator=g, device="cuda") * 0.05).bfloat16())
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, piece):
+        x[i:i + piece] = torch.randn((piece, H), generator=g, device="cuda").bfloat16()
+    ids = torch.rand((T, E), generator=g, device="cuda").topk(k, dim=1).indices.to(torch.int32)
+    probs = torch.rand((T, k), generator=g, device="cuda")
+    live = lambda n: torch.tensor([n], dtype=torch.int32, device="cuda")     # noqa: E731
+    _, codes, scales = m.forward_checkpoint(x, ids, probs, live(T), combine="bf16")
+    got = m.backward(x, x, ids, probs, live(T), codes, scales, grad_dtype="fp32")[1:3]
+    del codes, scales
+    n = live(piece)
+    want = [torch.zeros(v.shape, dtype=torch.float64, device="cuda") for v in got]
+    for i in range(0, T, piece):
+        xs, it, pt = x[i:i + piece], ids[i:i + piece], probs[i:i + piece]
+        _, sc, ss = m.forward_checkpoint(xs, it, pt, n, combine="bf16")
+        for w, v in zip(want, m.backward(xs, xs, it, pt, n, sc, ss, grad_dtype="fp32")[1:3]):
+            w += v
+    for v, w in zip(got, want):
+        # fp32 sums of about T k / E terms of random sign, of the same products: well inside
+        # their linear bound
+        assert float((v.double() - w).norm() / w.norm()) <= 2 * T * k / E * S
