@@ -6,12 +6,13 @@
 //   rows, SWIGLU   raw[r][f] = sum_h d_out[t][h] W2_e[h][f], then per element, from the
 //                  8-bit gate g and up u:  s = 1 / (1 + exp(-g)),  h = g s u,
 //                    dgu[r] = p raw (u s (1 + g (1 - s)),  g s),   hp[r] = p h,
-//                    part[r][f / 64] = sum over 64 columns of raw h
+//                    part[r][f / 32] = sum over 32 columns of raw h
 //   rows, plain    dx[r][h] = sum_n dgu[r][n] W1_e[n][h]
 //   weights        dW1_e[n][h] = sum_r dgu[r][n] x[t][h]
 //                  dW2_e[h][f] = sum_r d_out[t][h] hp[r][f]
-// dgu, hp and dx are rounded to bf16 (the operand type of the next product, and half
-// the bytes of fp32 rows); every sum is fp32.
+// dgu and hp are rounded to bf16, the operand type of the next product; dx is kept in
+// 16-bit integers with a scale per 16 columns (grad_dx.h: half the bytes of fp32 rows, 1/128
+// of bf16's error at the block's largest); every sum is fp32.
 //
 // Every product but the rows' first operand runs over an index that is not contiguous in
 // memory: the rows products over the rows of the kernel weights, which hold 8
