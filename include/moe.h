@@ -37,13 +37,13 @@
  *     stream, except moe_check (which reads the error word) and
  *     moe_get_indices (which copies to host).  moe_route, moe_forward, the
  *     training calls, moe_dispatch and moe_combine_rows only enqueue work on
- *     `stream`, so they can be captured in a HIP graph; a bf16 or int8 forward above 1024 tokens may run its
- *     64-row GEMM launches on a side stream of the library (one per GPU,
- *     default priority, created by the first bf16 or int8 weight load there
- *     and kept until the process ends), forked from `stream` and joined back
- *     to it with events, so the work still completes in `stream` order and is
- *     captured with it.  While a capture holds the side stream, forwards outside
- *     it run on their own stream alone.
+ *     `stream`, so they can be captured in a HIP graph; a bf16 or int8 forward
+ *     or a backward above 1024 tokens may run its 64-row GEMM launches on a side
+ *     stream of the library (one per GPU, default priority, created by the first
+ *     bf16 or int8 weight load there and kept until the process ends), forked
+ *     from `stream` and joined back to it with events, so the work still
+ *     completes in `stream` order and is captured with it.  While a capture holds
+ *     the side stream, such calls outside it run on their own stream alone.
  *   - The live token count is read from device memory (live_rows_dev, int32,
  *     in TOKENS).  It is clamped to [0, T_cap]; a value outside sets an error
  *     bit (see moe_check).  Token rows >= live are never read and rows >= live

@@ -101,22 +101,36 @@ __device__ __forceinline__ void grad_mma(f32x16 (&acc)[4][2], const GradFrag& f)
 }
 
 // One sub-step of 16 along the sum: the MFMAs of `cur` with the READS fragment reads of
-// the next sub-step spread between them; nothing crosses its ends
-template <int READS, typename Read>
+// the next sub-step spread between them, and DMA direct loads (4 or 8) issued just before,
+// with ALU scalar and vector instructions of their addresses a MFMA, so that no wave stands at
+// its loads with its matrix unit idle (16K tokens: rows after the SwiGLU 1077 -> 1063 us, before
+// it 784 -> 777, weights 1705 -> 1669); nothing else crosses its ends
+template <int READS, int DMA = 0, int ALU = 0, typename Read>
 __device__ __forceinline__ void grad_phase(f32x16 (&acc)[4][2], const GradFrag& cur, Read read, GradFrag& nxt)
 {
     read(nxt);
     grad_mma(acc, cur);
     constexpr int two = READS > 8 ? READS - 8 : 0;       // MFMAs followed by two reads
+    auto extra = [&](int k) {
+        if constexpr (DMA > 0) {
+            if constexpr (ALU > 0) {
+                __builtin_amdgcn_sched_group_barrier(0x004, ALU, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, ALU, 0);
+            }
+            if (k % (8 / DMA) == 8 / DMA - 1) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        }
+    };
 #pragma unroll
     for (int k = 0; k < two; ++k) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        extra(k);
     }
 #pragma unroll
     for (int k = two; k < 8; ++k) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        extra(k);
     }
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -157,8 +171,7 @@ __device__ __forceinline__ void grad_kloop(int nst, char* s0, char* s1, f32x16 (
         __builtin_amdgcn_sched_barrier(0);
     };
     auto into = [&](const char* nxt) {
-        __builtin_amdgcn_sched_barrier(0);
-        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, nxt, n); }, x);
+        grad_phase<READS, 8>(acc, y, [&](GradFrag& n) { read(Q0{}, nxt, n); }, x);
     };
     using Now = std::integral_constant<int, 0>;
     body(s0);
@@ -213,17 +226,16 @@ __device__ __forceinline__ void grad_kloop_halves(int nst, char* h0, char* h1, c
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         issue(SC, cur);
-        __builtin_amdgcn_sched_barrier(0);
     };
     auto body = [&](auto NC, auto SC, char* a, char* b) {
         grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, a, n); }, y);
         boundary(NC, SC, a);
-        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, b, n); }, x);
+        grad_phase<READS, 4, 6>(acc, y, [&](GradFrag& n) { read(Q0{}, b, n); }, x);
         grad_phase<READS>(acc, x, [&](GradFrag& n) { read(Q1{}, b, n); }, y);
     };
     auto into = [&](auto NC, auto SC, char* b, char* c) {
         boundary(NC, SC, b);
-        grad_phase<READS>(acc, y, [&](GradFrag& n) { read(Q0{}, c, n); }, x);
+        grad_phase<READS, 4, 6>(acc, y, [&](GradFrag& n) { read(Q0{}, c, n); }, x);
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
