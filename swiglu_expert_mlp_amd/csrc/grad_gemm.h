@@ -27,9 +27,9 @@
 // next tile's first two stages issued before the epilogue, which has LDS of its own.
 //
 // Measured (16,384 tokens, top-8 of 128 experts, hidden 2048, FFN 1024; the library's dense
-// bf16 product of 8192^3 runs at 1.21 PF/s): the product before the SwiGLU 754 us (0.73
+// bf16 product of 8192^3 runs at 1.21 PF/s): the product before the SwiGLU 767 us (0.72
 // PF/s; its epilogue, 23 vector instructions an element, is a fifth of it), the one after it
-// 1058 (1.04), the weights' 1604 (1.03).  What bounds them: the matrix units are busy 57 % of
+// 1071 (1.03), the weights' 1567 (1.05).  What bounds them: the matrix units are busy 60 % of
 // the cycles at 1.8 to 1.9 GHz, the clock that the power limit leaves; with the loads taken
 // out of a copy the two large ones take 870 and 1360 us, with the MFMAs out 890 and 1270.
 // Not bound by LDS: with the bank conflicts of the row operand's reads removed (40 % of the
