@@ -452,7 +452,8 @@ size_t moe_backward_workspace_bytes(moe_handle h, int64_t T_cap);
  * ws reports the ids and the live count as a forward's.
  * Errors: MOE_ERR_INVALID_ARG (another precision or type, NULL or misaligned
  * pointer, an output or the workspace in the memory of another argument, T_cap
- * outside [0, 2^26], ws_bytes too small), MOE_ERR_NOT_LOADED, MOE_ERR_HIP. */
+ * outside [0, 2^26], ws_bytes too small), MOE_ERR_UNSUPPORTED (H or F above
+ * 2^20), MOE_ERR_NOT_LOADED, MOE_ERR_HIP. */
 moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const void* x,
                         const int32_t* expert_ids, const float* probs, int64_t T_cap,
                         const int32_t* live_rows_dev, const int8_t* codes, const uint8_t* scales,

@@ -958,6 +958,9 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     moe_status st = check_tokens(what, h, T_cap);
     if (st != MOE_OK) return st;
     if (h->precision != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "%s: the handle's precision is not bf16", what);
+    // 32-bit byte offsets of the rows of a tile
+    if (h->H > 1 << 20 || h->F > 1 << 20)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d, F=%d above %d", what, h->H, h->F, 1 << 20);
     if (!h->kbuf) return fail(MOE_ERR_NOT_LOADED, "%s: no weights loaded (moe_load_weights)", what);
     if ((st = check_type(what, d_out_type)) != MOE_OK || (st = check_type(what, d_w_type)) != MOE_OK) return st;
     if ((st = check_ptrs(what, {d_out, x, expert_ids, probs, live_rows_dev, codes, scales, d_x, d_w1, d_w2, d_probs, ws})) !=

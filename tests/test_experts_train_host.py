@@ -113,6 +113,10 @@ def test_backward_refusals(L):
         fc = L.moe_forward_checkpoint(h, a[0], a[1], a[2], 64, a[3], 0, a[4], a[5], a[6], a[7], BIG, None)
         _refused(L, fc, "bf16")
         L.moe_destroy(h)
+    for H, F in ((32, (1 << 20) + 32), ((1 << 20) + 32, 32)):
+        h = _create(L, 1, H, F, 1)
+        assert call(h) == -2 and b"above" in L.moe_last_error()
+        L.moe_destroy(h)
     h = _create(L)
     assert call(h) == -3 and b"load" in L.moe_last_error()
 
