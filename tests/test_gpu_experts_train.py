@@ -444,6 +444,73 @@ def test_captured_replayed_and_on_streams():
     assert same(r3, a)
 
 
+def test_both_tile_designs_on_one_stream_and_beside_each_other():
+    """Enough rows per expert that the 64-row tiles stay on the call's stream: the bits of the
+    same tokens at a capacity whose mean puts them beside the 256-row ones, and the bounds."""
+    T, E, H, F, k = 1300, 4, 96, 160, 2
+    c = _make(T, T, E, H, F, k, 0, seed=41)
+    ids = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(T, 1)
+    ids[::13, 0], ids[5::17, 1] = 2, 3                       # experts 2 and 3 keep at most 128 rows
+    m = _moe(c, k)
+    _, codes, scales = m.forward_checkpoint(c["x"], ids, c["probs"], c["live"])
+    ref = backward_ref(c["d_out"], c["x"], ids, c["probs"], T, codes, scales, c["w1"], c["w2"], False)
+    assert T * k >= 4 * 128 * E
+    got = m.backward(c["d_out"], c["x"], ids, c["probs"], c["live"], codes, scales)
+    for name, v in zip(("d_x", "d_w1", "d_w2", "d_probs"), got):
+        _within(v, *ref[name], name)
+    # the same experts among twice as many: the mean is under the threshold
+    wide = dict(c, w1=torch.cat([c["w1"], c["w1"]]), w2=torch.cat([c["w2"], c["w2"]]))
+    assert T * k < 4 * 128 * 2 * E
+    m2 = _moe(wide, k)
+    again = m2.backward(c["d_out"], c["x"], ids, c["probs"], c["live"], codes, scales)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[3], got[3])
+    assert torch.equal(again[1][:E], got[1]) and torch.equal(again[2][:E], got[2]) and (again[1][E:] == 0).all()
+
+
+def test_eager_backward_beside_a_capture():
+    """A captured backward leaves the side stream in the capture until it ends: an eager one on
+    another stream meanwhile stays out of the graph; replays beside eager calls, the same bits."""
+    shape = (1400, 1500, 16, 96, 192, 2, 1)
+    T, cap, E, H, F, k, _ = shape
+    a, b = _make(*shape, seed=51), _make(*shape, seed=52)
+    m = _moe(a, k)
+    kept = {id(c): m.forward_checkpoint(c["x"], c["ids"], c["probs"], c["live"])[1:] for c in (a, b)}
+    bf = torch.bfloat16
+
+    def buffers():
+        e = lambda s, t: torch.full(s, NAN, dtype=t, device="cuda")      # noqa: E731
+        return dict(d_x=e((cap, H), bf), d_w1=e((E, 2 * F, H), bf), d_w2=e((E, H, F), bf), d_probs=e((cap, k), torch.float32),
+                    ws=_garbage(m.new_backward_workspace(cap).numel()))
+
+    def back(c, o, stream=None):
+        return m.backward(c["d_out"], c["x"], c["ids"], c["probs"], c["live"], *kept[id(c)], stream=stream, **o)
+
+    cut = lambda g: (g[0][:T].clone(), g[1].clone(), g[2].clone(), g[3][:T].clone())     # noqa: E731
+    want = {id(c): cut(back(c, buffers())) for c in (a, b)}
+    names = ("d_x", "d_w1", "d_w2", "d_probs")
+    same = lambda o, c: all(torch.equal(x, y) for x, y in zip(cut([o[n] for n in names]), want[id(c)]))   # noqa: E731
+    outs = [buffers() for _ in range(4)]
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        back(a, outs[0])
+        back(b, outs[1], other)                              # not captured
+        back(b, outs[2])
+        back(a, outs[3], other)                              # not captured
+    torch.cuda.synchronize()
+    assert same(outs[1], b) and same(outs[3], a)
+    for n in range(3):
+        for o in (outs[0], outs[2], outs[1]):
+            for name in names:
+                o[name].fill_(NAN)
+        torch.cuda.synchronize()
+        graph.replay()
+        back(b, outs[1], other)                              # beside the replay
+        torch.cuda.synchronize()
+        assert same(outs[0], a) and same(outs[2], b) and same(outs[1], b), n
+
+
 @pytest.mark.parametrize("H,F", [(2080, 64), (64, 2080)])
 def test_offsets_past_32_bits(H, F):
     """Buffers past 4 GiB (rows of H columns, then those of F): tokens at both ends and in the
