@@ -12,7 +12,9 @@ or no GPU is present, the calls raise.
     ids, probs = moe.route(logits, live, ws=ws)
     out = moe.forward(x, ids, probs, live, ws=ws)   # fp32 [T_cap, H]
 
-``live`` is an int32 device tensor holding the number of live tokens.
+``live`` is an int32 device tensor holding the number of live tokens.  A training step runs
+``forward_checkpoint`` and ``backward`` instead of ``forward`` (bf16); ``dispatch`` and ``combine``,
+with their gradients, serve experts of the caller's own.
 """
 from __future__ import annotations
 
