@@ -183,7 +183,7 @@ moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_sc
  * be passed as is.  Its bytes are the library's until the work enqueued on it
  * has finished; moe_get_indices, moe_get_rows and moe_check read the state of
  * the last moe_route / moe_forward that used it (the first two refuse one that
- * moe_backward, moe_dispatch or moe_balance used since). */
+ * moe_backward or moe_dispatch used since). */
 size_t moe_workspace_bytes(moe_handle h, int64_t T_cap);
 
 /* Router (Megatron-Core `_route`): for each live token, softmax over the E

@@ -980,7 +980,7 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
     char* w = (char*)ws;
     const WsLayout& L = B.prep;
     hipError_t e = launch_prep(expert_ids, probs, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
-                               MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr);
+                               MOE_COMBINE_FP32, nullptr, kOtherTag, 0, nullptr);
     if (e != hipSuccess) return hip_fail(e, "moe_backward: prep launch");
     const uint16_t* g_out = (const uint16_t*)d_out;
     if (d_out_type == MOE_TYPE_FP32) {
@@ -1072,7 +1072,7 @@ moe_status moe_dispatch(moe_handle h, const void* x, int type, const int32_t* ex
     if (!dispatch_in_one(T_cap)) {
         // (the rows of the routes come from the ranks and bases: no scatter)
         e = launch_prep(expert_ids, nullptr, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H,
-                        MOE_COMBINE_FP32, nullptr, 0 /* no forward's rows */, 0, nullptr, false);
+                        MOE_COMBINE_FP32, nullptr, kOtherTag, 0, nullptr, false);
         if (e != hipSuccess) return hip_fail(e, "moe_dispatch: prep launch");
     }
     e = launch_dispatch(x, type == MOE_TYPE_BF16, expert_ids, w, L, live_rows_dev, T_cap, h->E, h->k, h->H, rows,
@@ -1158,8 +1158,8 @@ moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t*
     hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "moe_get_indices: header copy");
-    if (hdr.mark == kErrMark && hdr.tag == 0)
-        return fail(MOE_ERR_INVALID_ARG, "moe_get_indices: the workspace was last used by a call that is no forward");
+    if (hdr.mark == kErrMark && hdr.tag == kOtherTag)
+        return fail(MOE_ERR_INVALID_ARG, "moe_get_indices: moe_backward or moe_dispatch used the workspace since its forward");
     const int64_t R = (int64_t)hdr.T * h->k;
     if (counts) e = hipMemcpy(counts, w + L.counts, 4 * h->E, hipMemcpyDeviceToHost);
     if (e == hipSuccess && offsets)
@@ -1187,8 +1187,8 @@ moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_
     hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
     if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return hip_fail(e, "moe_get_rows: header copy");
-    if (hdr.mark == kErrMark && hdr.tag == 0)
-        return fail(MOE_ERR_INVALID_ARG, "moe_get_rows: the workspace was last used by a call that is no forward");
+    if (hdr.mark == kErrMark && hdr.tag == kOtherTag)
+        return fail(MOE_ERR_INVALID_ARG, "moe_get_rows: moe_backward or moe_dispatch used the workspace since its forward");
     const size_t n = (size_t)hdr.n_rows;
     const size_t T = (size_t)hdr.T;
     const size_t R = T * h->k;

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(256) dispatch_small_kernel(DispatchArgs a)
         a.hdr->mark = kErrMark;
         a.hdr->T = T;
         a.hdr->n_rows = total;
-        a.hdr->tag = 0;                                  // holds no forward's rows
+        a.hdr->tag = kOtherTag;                          // holds no forward's rows
     }
     __syncthreads();
     // tokens blockIdx.x, blockIdx.x + gridDim.x, ..
