@@ -181,9 +181,10 @@ moe_status moe_load_quantized(moe_handle h, const int8_t* w1, const float* w1_sc
  * required initial contents: every launch writes what a later launch of the
  * same call reads, so a fresh allocation (or one left by another handle) can
  * be passed as is.  Its bytes are the library's until the work enqueued on it
- * has finished; moe_get_indices, moe_get_rows and moe_check read the state of
- * the last moe_route / moe_forward that used it (the first two refuse one that
- * moe_backward or moe_dispatch used since). */
+ * has finished; moe_check reads the bits of the last moe_route / moe_forward
+ * that used it, moe_get_indices and moe_get_rows the state of the last forward
+ * (any other workspace, one that moe_balance, moe_backward or moe_dispatch
+ * wrote over since among them, is refused). */
 size_t moe_workspace_bytes(moe_handle h, int64_t T_cap);
 
 /* Router (Megatron-Core `_route`): for each live token, softmax over the E
@@ -520,7 +521,11 @@ moe_status moe_combine_backward(moe_handle h, const void* d_out, int out_type, c
  * (= t*topk + j of the route at each grouped row, experts ascending, tokens
  * ascending within an expert); dst: int32 [T*topk] (grouped row of each
  * route, -1 if dropped); n_rows_out / T_out: the row and live-token counts.
- * perm_src and dst must hold T_cap*topk entries.  Any output may be NULL. */
+ * perm_src and dst must hold T_cap*topk entries.  Any output may be NULL.
+ * Errors: MOE_ERR_INVALID_ARG for a NULL handle or workspace, a T_cap outside
+ * [0, 2^26], or a workspace that a forward of this handle's shape and
+ * precision with this T_cap was not the last to write; MOE_ERR_HIP if a copy
+ * fails. */
 moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t* counts,
                            int32_t* offsets, int32_t* perm_src, int32_t* dst,
                            int32_t* n_rows_out, int32_t* T_out, hipStream_t stream);
@@ -536,8 +541,8 @@ moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t*
  * activations, E4M3 codes uint8 [T][H] and E8M0 scale bytes uint8 [T][H/32],
  * or int8 codes [T][H] and fp32 scales [T] (T = the live tokens of the last
  * forward).  Any output may be NULL.  For tests and
- * debugging.  Errors: MOE_ERR_INVALID_ARG for a NULL handle or workspace, or
- * x_codes / x_scales with bf16; MOE_ERR_HIP if a copy fails. */
+ * debugging.  Errors: as moe_get_indices; MOE_ERR_INVALID_ARG also for
+ * x_codes / x_scales with bf16. */
 moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_rows,
                         void* fc1_out_rows, int32_t* sorted_ids, float* sorted_probs,
                         void* x_codes, void* x_scales, hipStream_t stream);

@@ -212,7 +212,8 @@ struct WsHeader {
 
 // Identifies a workspace layout: a workspace whose header holds this tag was last
 // used by a forward of this shape and capacity, so its regions are where the
-// caller's layout says.  kOtherTag instead: moe_backward or moe_dispatch used it since.
+// caller's layout says.  kOtherTag instead: moe_backward or moe_dispatch used it since; 0: a
+// balance loss of several workgroups did.
 constexpr uint64_t kOtherTag = 1;
 inline uint64_t forward_tag(int E, int H, int F, int k, int precision, int64_t T_cap)
 {

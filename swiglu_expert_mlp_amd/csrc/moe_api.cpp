@@ -1147,6 +1147,22 @@ moe_status moe_forward_noalloc(moe_handle h, const void* x, const int32_t* exper
                           kScratchBytes, stream);
 }
 
+// The header of a workspace that is read back, refused unless a forward of the handle's shape,
+// precision and capacity was the last to write it: only then its regions are where layout_of
+// says and its counts size the copies
+static moe_status read_header(const char* what, moe_handle h, const char* ws, int64_t T_cap, WsHeader& hdr,
+                              hipStream_t stream)
+{
+    hipError_t e = hipMemcpyAsync(&hdr, ws, sizeof(hdr), hipMemcpyDeviceToHost, stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(stream);
+    if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s: header copy: %s", what, hipGetErrorString(e));
+    if (hdr.mark != kErrMark || hdr.tag != forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "%s: the workspace was not last written by a forward of this shape, precision and T_cap=%lld", what,
+                    (long long)T_cap);
+    return MOE_OK;
+}
+
 moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t* counts,
                            int32_t* offsets, int32_t* perm_src, int32_t* dst,
                            int32_t* n_rows_out, int32_t* T_out, hipStream_t stream)
@@ -1155,11 +1171,9 @@ moe_status moe_get_indices(moe_handle h, const void* ws, int64_t T_cap, int32_t*
     const WsLayout L = layout_of(h, T_cap);
     const char* w = (const char*)ws;
     WsHeader hdr;
-    hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
-    if (e == hipSuccess) e = hipStreamSynchronize(stream);
-    if (e != hipSuccess) return hip_fail(e, "moe_get_indices: header copy");
-    if (hdr.mark == kErrMark && hdr.tag == kOtherTag)
-        return fail(MOE_ERR_INVALID_ARG, "moe_get_indices: moe_backward or moe_dispatch used the workspace since its forward");
+    const moe_status st = read_header("moe_get_indices", h, w + L.hdr, T_cap, hdr, stream);
+    if (st != MOE_OK) return st;
+    hipError_t e = hipSuccess;
     const int64_t R = (int64_t)hdr.T * h->k;
     if (counts) e = hipMemcpy(counts, w + L.counts, 4 * h->E, hipMemcpyDeviceToHost);
     if (e == hipSuccess && offsets)
@@ -1184,11 +1198,9 @@ moe_status moe_get_rows(moe_handle h, const void* ws, int64_t T_cap, float* fc2_
     const WsLayout L = layout_of(h, T_cap);
     const char* w = (const char*)ws;
     WsHeader hdr;
-    hipError_t e = hipMemcpyAsync(&hdr, w + L.hdr, sizeof(hdr), hipMemcpyDeviceToHost, stream);
-    if (e == hipSuccess) e = hipStreamSynchronize(stream);
-    if (e != hipSuccess) return hip_fail(e, "moe_get_rows: header copy");
-    if (hdr.mark == kErrMark && hdr.tag == kOtherTag)
-        return fail(MOE_ERR_INVALID_ARG, "moe_get_rows: moe_backward or moe_dispatch used the workspace since its forward");
+    const moe_status st = read_header("moe_get_rows", h, w + L.hdr, T_cap, hdr, stream);
+    if (st != MOE_OK) return st;
+    hipError_t e = hipSuccess;
     const size_t n = (size_t)hdr.n_rows;
     const size_t T = (size_t)hdr.T;
     const size_t R = T * h->k;
