@@ -46,8 +46,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// 16 bytes of zeros, the source of loads that lie past the end of a sum
-__device__ const uint32_t grad_zeros[4] __attribute__((aligned(16))) = {};
+// Zeros, the source of loads that lie past the end of a sum (1 KB: a block of weights)
+__device__ const uint32_t grad_zeros[256] __attribute__((aligned(16))) = {};
 
 // 8 elements along the sum for one column of an MFMA operand: two transposing reads,
 // the second `step` bytes after the first
@@ -518,7 +518,7 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
                 aoff[i] = rr < p.rows ? rr * 2 * Kc + 16 * ((lane & 7) ^ (rr & 7)) : (int)0x80000000;
         }
         const uint16_t* w = W + (int64_t)p.e * Kc * N;
-        if constexpr (WIDE) wbase = (const char*)w + wlane;
+        if constexpr (WIDE) wbase = (const char*)w;
         else {
             ar = __builtin_amdgcn_make_buffer_rsrc((void*)(SWIGLU ? A : A + (int64_t)p.row0 * Kc), (short)0, 0x7fffffff,
                                                    kBigRsrcWord3);
@@ -547,14 +547,13 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
             const int c = 8 * s + ((lane & 7) ^ (rr & 7));
             big_load_block(c < Kc / 8 ? arow[i] + 16 * c : (const char*)grad_zeros, st + (4 * wid + i) * 1024);
         }
-        // (the last stage of a sum that is an odd multiple of 32 holds zeros against the
-        // weights of its first half again: a NaN there is one of the same output column)
+        // (the last stage of a sum that is an odd multiple of 32 holds zeros on both sides: zeros
+        // against weights would make an infinite weight's sums NaN)
         const char* wp = wbase + ((int64_t)grp * 32 * ks + (int64_t)s32 * w + ((4 * s) & 31)) * 1024;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 4 * s + i < nt16 ? i : i - 2;
-            big_load_block(wp + n * 1024, st + kBigWOff + (4 * wid + i) * 1024);
-        }
+        for (int i = 0; i < 4; ++i)
+            big_load_block((4 * s + i < nt16 ? wp + i * 1024 : (const char*)grad_zeros) + wlane,
+                           st + kBigWOff + (4 * wid + i) * 1024);
     };
     // fragments of sub-step Q: A row l % 32, chunk 2 Q + l / 32 at its slot; B one 1 KB
     // block (16 of the sum x 32 columns), rows 8 (l / 32) + {0, 4} + (l % 16) / 4
@@ -730,7 +729,7 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
             src = tok;
         }
         arow = (const char*)(A + src * Kc);
-        wbase = (const char*)(W + (int64_t)p.e * Kc * N) + wlane;
+        wbase = (const char*)(W + (int64_t)p.e * Kc * N);
         s32 = min(p.n0 / 32 + wid, ks - 1);
     };
     auto issue = [&](char* st, int s) {
@@ -740,10 +739,9 @@ __device__ __forceinline__ void grad_small_tiles(const GradArgs& g, bool take_bi
         const int w = min(32, nt16 - 32 * grp);
         const char* wp = wbase + ((int64_t)grp * 32 * ks + (int64_t)s32 * w + ((4 * s) & 31)) * 1024;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 4 * s + i < nt16 ? i : i - 2;
-            big_load_block(wp + n * 1024, st + kGradSmallW + (4 * wid + i) * 1024);
-        }
+        for (int i = 0; i < 4; ++i)             // (past the sum's end zeros, as in the 256-row tiles)
+            big_load_block((4 * s + i < nt16 ? wp + i * 1024 : (const char*)grad_zeros) + wlane,
+                           st + kGradSmallW + (4 * wid + i) * 1024);
     };
     int a_off[4], b_off[2];
     {
