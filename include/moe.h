@@ -32,6 +32,7 @@
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers of the caller, 16-byte aligned,
  *     row-major, dense.  bf16 data is passed as its 16-bit patterns.
+ *     With T_cap 0 a tensor of T_cap tokens has no elements and may be NULL.
  *     They and `stream` belong to the device current at the call.
  *   - The library never allocates device memory and never synchronizes the
  *     stream, except moe_check (which reads the error word) and

@@ -130,6 +130,9 @@ static moe_status hip_fail(hipError_t e, const char* what)
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Whether a tensor of T_cap tokens is missing (one without tokens may have no address)
+static bool missing(const void* p, int64_t T_cap) { return !p && T_cap > 0; }
+
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 static bool overlap(const void* a, size_t na, const void* b, size_t nb)
@@ -439,7 +442,7 @@ moe_status moe_route(moe_handle h, const float* logits, int64_t T_cap,
     if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_route: NULL handle");
     if (T_cap < 0 || T_cap > (int64_t)1 << 26)
         return fail(MOE_ERR_INVALID_ARG, "moe_route: T_cap=%lld out of range", (long long)T_cap);
-    if (!logits || !live_rows_dev || !ids || !probs || !ws)
+    if (missing(logits, T_cap) || !live_rows_dev || missing(ids, T_cap) || missing(probs, T_cap) || !ws)
         return fail(MOE_ERR_INVALID_ARG, "moe_route: NULL pointer");
     if (ws_bytes < sizeof(WsHeader))
         return fail(MOE_ERR_INVALID_ARG, "moe_route: workspace too small");
@@ -447,7 +450,6 @@ moe_status moe_route(moe_handle h, const float* logits, int64_t T_cap,
         return fail(MOE_ERR_INVALID_ARG, "moe_route: pointers must be 16-byte aligned");
     moe_status st = ensure_device(h);
     if (st != MOE_OK) return st;
-    if (T_cap == 0) return MOE_OK;
     hipError_t e = launch_route(logits, T_cap, live_rows_dev, h->E, h->k, ids, probs,
                                 (WsHeader*)ws, h->num_cu, stream);
     if (e != hipSuccess) return hip_fail(e, "moe_route: launch");
@@ -467,7 +469,7 @@ moe_status moe_balance(moe_handle h, const float* logits, const int32_t* expert_
     if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_balance: NULL handle");
     if (T_cap < 0 || T_cap > (int64_t)1 << 26)
         return fail(MOE_ERR_INVALID_ARG, "moe_balance: T_cap=%lld out of range", (long long)T_cap);
-    if (!logits || !expert_ids || !live_rows_dev || !losses || !counts || !prob_sums || !ws)
+    if (missing(logits, T_cap) || missing(expert_ids, T_cap) || !live_rows_dev || !losses || !counts || !prob_sums || !ws)
         return fail(MOE_ERR_INVALID_ARG, "moe_balance: NULL pointer");
     if (!aligned16(logits) || !aligned16(expert_ids) || !aligned16(token_mask) || !aligned16(losses) ||
         !aligned16(counts) || !aligned16(prob_sums) || !aligned16(ws))
@@ -492,13 +494,13 @@ moe_status moe_route_backward(moe_handle h, const float* logits, const int32_t* 
     if (!h) return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL handle");
     if (T_cap < 0 || T_cap > (int64_t)1 << 26)
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: T_cap=%lld out of range", (long long)T_cap);
-    if (!logits || !live_rows_dev || !d_logits)
+    if (missing(logits, T_cap) || !live_rows_dev || missing(d_logits, T_cap))
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: NULL pointer");
-    if (!probs != !d_probs || (d_probs && !expert_ids))
+    if (T_cap > 0 && (!probs != !d_probs || (d_probs && !expert_ids)))
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_probs needs expert_ids and probs, and probs d_probs");
     if (!counts != !d_losses)
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: d_losses needs counts, and counts d_losses");
-    if (!d_probs && !d_losses)
+    if (T_cap > 0 && !d_probs && !d_losses)
         return fail(MOE_ERR_INVALID_ARG, "moe_route_backward: neither d_probs nor d_losses");
     for (const void* p : {(const void*)logits, (const void*)expert_ids, (const void*)probs, (const void*)d_probs,
                           (const void*)token_mask, (const void*)counts, (const void*)d_losses, (const void*)d_logits})
@@ -528,7 +530,7 @@ moe_status moe_probs_backward(moe_handle h, const void* d_out, int combine, cons
         return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: T_cap=%lld out of range", (long long)T_cap);
     if (combine != MOE_COMBINE_FP32 && combine != MOE_COMBINE_BF16)
         return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: combine %d (fp32 and bf16 only)", combine);
-    if (!d_out || !expert_ids || !d_probs || !ws)
+    if (missing(d_out, T_cap) || missing(expert_ids, T_cap) || missing(d_probs, T_cap) || !ws)
         return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: NULL pointer");
     if (!aligned16(d_out) || !aligned16(expert_ids) || !aligned16(d_probs) || !aligned16(ws))
         return fail(MOE_ERR_INVALID_ARG, "moe_probs_backward: pointers must be 16-byte aligned");
@@ -579,8 +581,8 @@ static moe_status forward_impl(moe_handle h, const void* x, const int32_t* exper
         return fail(MOE_ERR_INVALID_ARG, "moe_forward: %s is implemented for bf16 only",
                     fused_fin ? "MOE_FUSED_FINALIZE" : "MOE_FUSED_FFN");
     // row mode does not use the probabilities (every route has probability 1)
-    if (!x || !expert_ids || (!probs && combine != MOE_COMBINE_ROWS) || !live_rows_dev || !out ||
-        !ws)
+    if (missing(x, T_cap) || missing(expert_ids, T_cap) || (missing(probs, T_cap) && combine != MOE_COMBINE_ROWS) ||
+        !live_rows_dev || missing(out, T_cap) || !ws)
         return fail(MOE_ERR_INVALID_ARG, "moe_forward: NULL pointer");
     if (!aligned16(x) || !aligned16(expert_ids) || (probs && !aligned16(probs)) ||
         !aligned16(out) || !aligned16(ws))
@@ -591,17 +593,22 @@ static moe_status forward_impl(moe_handle h, const void* x, const int32_t* exper
                     L.total, (long long)T_cap);
     moe_status st = ensure_device(h);
     if (st != MOE_OK) return st;
-    if (T_cap == 0) return MOE_OK;
     char* w = (char*)ws;
     WsHeader* hdr = (WsHeader*)(w + L.hdr);
-    hipError_t e = mark(h, 0, stream);
-    if (e != hipSuccess) return hip_fail(e, "moe_forward: stage event");
+    const uint64_t tag = forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap);
+    hipError_t e = hipSuccess;
+    if (T_cap == 0) {                       // the header alone
+        e = launch_prep(expert_ids, probs, 0, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream, h->H, combine, nullptr,
+                        tag, fc1_topk ? 1 : 0, nullptr);
+        return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_forward: prep launch");
+    }
+    if ((e = mark(h, 0, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
     // int8: x is quantized by extra workgroups of the permutation's launches
     const QuantRows quant_x{(const uint16_t*)x, live_rows_dev, T_cap, h->H, int8_pitch(h->H),
                             (uint8_t*)(w + L.xq), (float*)(w + L.xs)};
     e = launch_prep(expert_ids, probs, T_cap, live_rows_dev, h->E, h->k, h->num_cu, w, L, stream,
                     h->H, combine, fused_fin ? out : nullptr,
-                    forward_tag(h->E, h->H, h->F, h->k, h->precision, T_cap), fc1_topk ? 1 : 0,
+                    tag, fc1_topk ? 1 : 0,
                     h->precision == MOE_INT8 ? &quant_x : nullptr);
     if (e != hipSuccess) return hip_fail(e, "moe_forward: prep launch");
     if ((e = mark(h, 1, stream)) != hipSuccess) return hip_fail(e, "moe_forward: stage event");
@@ -878,13 +885,18 @@ moe_status moe_forward_ex(moe_handle h, const void* x, const int32_t* expert_ids
                         stream);
 }
 
-// Pointers of a call: none may be null or unaligned
-static moe_status check_ptrs(const char* what, std::initializer_list<const void*> ptrs)
+// Pointers of a call, first those of T_cap tokens: none may be null (without tokens: of the
+// others) or unaligned
+static moe_status check_ptrs(const char* what, int64_t T_cap, std::initializer_list<const void*> of_tokens,
+                             std::initializer_list<const void*> others)
 {
-    for (const void* p : ptrs)
+    for (const void* p : of_tokens)
+        if (missing(p, T_cap)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    for (const void* p : others)
         if (!p) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
-    for (const void* p : ptrs)
-        if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+    for (auto list : {of_tokens, others})
+        for (const void* p : list)
+            if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
     return MOE_OK;
 }
 
@@ -932,7 +944,7 @@ moe_status moe_forward_checkpoint(moe_handle h, const void* x, const int32_t* ex
     if (combine != MOE_COMBINE_FP32 && combine != MOE_COMBINE_BF16 && combine != MOE_COMBINE_ROWS)
         return fail(MOE_ERR_INVALID_ARG, "moe_forward_checkpoint: combine %d (no options are taken)", combine);
     moe_status st = check_tokens("moe_forward_checkpoint", h, T_cap);
-    if (st != MOE_OK || (st = check_ptrs("moe_forward_checkpoint", {codes, scales})) != MOE_OK) return st;
+    if (st != MOE_OK || (st = check_ptrs("moe_forward_checkpoint", T_cap, {codes, scales}, {})) != MOE_OK) return st;
     const size_t T = T_cap, R = T * h->k, H = h->H;
     const size_t out_bytes = combine == MOE_COMBINE_ROWS ? 4 * R * H : combine == MOE_COMBINE_BF16 ? 2 * T * H : 4 * T * H;
     st = check_overlap("moe_forward_checkpoint", {{codes, R * 2 * h->F}, {scales, R * (h->F / 16)}},
@@ -963,8 +975,8 @@ moe_status moe_backward(moe_handle h, const void* d_out, int d_out_type, const v
         return fail(MOE_ERR_UNSUPPORTED, "%s: H=%d, F=%d above %d", what, h->H, h->F, 1 << 20);
     if (!h->kbuf) return fail(MOE_ERR_NOT_LOADED, "%s: no weights loaded (moe_load_weights)", what);
     if ((st = check_type(what, d_out_type)) != MOE_OK || (st = check_type(what, d_w_type)) != MOE_OK) return st;
-    if ((st = check_ptrs(what, {d_out, x, expert_ids, probs, live_rows_dev, codes, scales, d_x, d_w1, d_w2, d_probs, ws})) !=
-        MOE_OK)
+    if ((st = check_ptrs(what, T_cap, {d_out, x, expert_ids, probs, codes, scales, d_x, d_probs},
+                         {live_rows_dev, d_w1, d_w2, ws})) != MOE_OK)
         return st;
     const BackwardLayout B = backward_layout(h, T_cap);
     if (ws_bytes < B.total)
@@ -1057,7 +1069,7 @@ moe_status moe_dispatch(moe_handle h, const void* x, int type, const int32_t* ex
     const char* what = "moe_dispatch";
     moe_status st = check_tokens(what, h, T_cap);
     if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK ||
-        (st = check_ptrs(what, {x, expert_ids, live_rows_dev, rows, row_of, offsets, ws})) != MOE_OK)
+        (st = check_ptrs(what, T_cap, {x, expert_ids, rows, row_of}, {live_rows_dev, offsets, ws})) != MOE_OK)
         return st;
     WsLayout L;
     const size_t need = prep_layout(h, T_cap, L);
@@ -1087,7 +1099,7 @@ moe_status moe_combine_rows(moe_handle h, const void* rows, int type, const int3
     const char* what = "moe_combine_rows";
     moe_status st = check_tokens(what, h, T_cap);
     if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK || (st = check_type(what, out_type)) != MOE_OK ||
-        (st = check_ptrs(what, {rows, row_of, live_rows_dev, out})) != MOE_OK)
+        (st = check_ptrs(what, T_cap, {rows, row_of, out}, {live_rows_dev})) != MOE_OK)
         return st;
     if (!aligned16(probs)) return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
     const size_t T = T_cap, R = T * h->k, H = h->H;
@@ -1108,9 +1120,9 @@ moe_status moe_combine_backward(moe_handle h, const void* d_out, int out_type, c
     const char* what = "moe_combine_backward";
     moe_status st = check_tokens(what, h, T_cap);
     if (st != MOE_OK || (st = check_type(what, type)) != MOE_OK || (st = check_type(what, out_type)) != MOE_OK ||
-        (st = check_ptrs(what, {d_out, row_of, probs, live_rows_dev, d_rows})) != MOE_OK)
+        (st = check_ptrs(what, T_cap, {d_out, row_of, probs, d_rows}, {live_rows_dev})) != MOE_OK)
         return st;
-    if (!rows != !d_probs) return fail(MOE_ERR_INVALID_ARG, "%s: d_probs needs rows, and rows d_probs", what);
+    if (T_cap > 0 && !rows != !d_probs) return fail(MOE_ERR_INVALID_ARG, "%s: d_probs needs rows, and rows d_probs", what);
     if (!aligned16(rows) || !aligned16(d_probs))
         return fail(MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
     const size_t T = T_cap, R = T * h->k, H = h->H;
