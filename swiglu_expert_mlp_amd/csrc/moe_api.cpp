@@ -144,7 +144,7 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb)
 // returns their end
 static size_t prep_layout(const moe_ctx* h, int64_t T_cap, WsLayout& L)
 {
-    const int64_t E = h->E, H = h->H, k = h->k;
+    const int64_t E = h->E, k = h->k;
     const int64_t R = T_cap * k;
     L = WsLayout{};
     L.nchunks = (T_cap + kChunkTok - 1) / kChunkTok;
@@ -165,8 +165,6 @@ static size_t prep_layout(const moe_ctx* h, int64_t T_cap, WsLayout& L)
     L.dst = take(4 * R);
     L.tiles = take(8 * L.max_tiles);
     L.tiles_big = take(8 * L.max_tiles_big);
-    L.ready = take(4 * (L.max_tiles + 4 * L.max_tiles_big));
-    L.fin_cnt = take(4 * T_cap * ((H + kFinCols - 1) / kFinCols));
     return o;
 }
 
@@ -177,6 +175,8 @@ static WsLayout layout_of(const moe_ctx* h, int64_t T_cap)
     const int64_t R = T_cap * h->k;
     size_t o = prep_layout(h, T_cap, L);
     auto take = [&](size_t bytes) { size_t at = o; o += up256(bytes > 0 ? bytes : 1); return at; };
+    L.ready = take(4 * (L.max_tiles + 4 * L.max_tiles_big));
+    L.fin_cnt = take(4 * T_cap * ((H + kFinCols - 1) / kFinCols));
     if (h->precision == MOE_BF16) {
         L.hbuf = take(2 * R * F);
         L.hscale = 0;
