@@ -517,8 +517,10 @@ class MoE:
                  ws=None, stream=None, grad_dtype="bf16"):
         """Gradients of the experts (moe_backward): d_x bf16 [T_cap, H], d_w1 [E, 2F, H] (gate rows
         first) and d_w2 [E, H, F] (bf16, or fp32 with grad_dtype="fp32" or tensors of that
-        type), d_probs fp32 [T_cap, topk].  d_out [T_cap, H] fp32 or bf16; the other inputs as
-        given to, and kept by, forward_checkpoint."""
+        type), d_probs fp32 [T_cap, topk].  d_out [T_cap, H] fp32 (rounded to bf16 first) or bf16;
+        the other inputs as given to, and kept by, forward_checkpoint.  At the 8-bit kept values,
+        so about 1 % off the layer's own gradients; probs_backward on the forward's workspace is
+        the more exact d_probs."""
         torch = _torch()
         if grad_dtype not in ("bf16", "fp32"):
             raise ValueError("grad_dtype must be bf16 or fp32")

@@ -1,9 +1,12 @@
 // The rows of x's gradient between the product that makes them and the sum over a token's
 // routes: 16-bit integers, 16 neighbouring columns sharing a scale 2^(byte - 127), the
 // smallest power of two (at least 2^-126) whose 32767-fold reaches their largest magnitude.
-// A value is off by at most half a scale, 2^-15 of that magnitude, so d_x carries the
-// roundings of its operand and its own to bf16 alone (bf16 rows would add a third; fp32 rows
-// are twice the bytes: at 16K tokens, top-8, hidden 2048, the sum took 212 us instead of 117).
+// A value is off by at most half a scale: less than 1/32767 of that magnitude, or 2^-127 where
+// the scale is at its floor (a largest magnitude below 32767 2^-126).  So d_x carries the
+// roundings of its operand and its own to bf16 alone, but for values less than 1/128 of the
+// loudest of their 16, which keep fewer bits than bf16 rows would leave them.  (bf16 rows would
+// add a third rounding to every value; fp32 rows are twice the bytes: at 16K tokens, top-8,
+// hidden 2048, the sum took 212 us instead of 117.)
 // Where one of the 16 is an infinity or a NaN the byte is 255 and the values are bf16 patterns.
 #pragma once
 

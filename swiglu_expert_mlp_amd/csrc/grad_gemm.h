@@ -27,9 +27,10 @@
 // next tile's first two stages issued before the epilogue, which has LDS of its own.
 //
 // Measured (16,384 tokens, top-8 of 128 experts, hidden 2048, FFN 1024; the library's dense
-// bf16 product of 8192^3 runs at 1.21 PF/s): the product before the SwiGLU 767 us (0.72
+// bf16 product of 8192^3 runs at 1.21 PF/s): the product before the SwiGLU 769 us (0.72
 // PF/s; its epilogue, 23 vector instructions an element, is a fifth of it), the one after it
-// 1071 (1.03), the weights' 1567 (1.05).  What bounds them: the matrix units are busy 60 % of
+// 1064 (1.03), the weights' 1571 (1.05; a fp32 result, twice the bytes stored, takes the call from
+// 3515 to 3784, 4,096 skewed tokens from 1351 to 1602, 1,000 tokens on 64 experts 435 to 519).  What bounds them: the matrix units are busy 60 % of
 // the cycles at 1.8 to 1.9 GHz, the clock that the power limit leaves; with the loads taken
 // out of a copy the two large ones take 870 and 1360 us, with the MFMAs out 890 and 1270.
 // Not bound by LDS: with the bank conflicts of the row operand's reads removed (40 % of the
@@ -448,7 +449,10 @@ constexpr int grad_block_stores(bool swiglu) { return swiglu ? 6 : 3; }
 // WIDE: 64-bit addresses, and a sum that may be an odd multiple of 32.  Otherwise the direct
 // loads go through descriptors, the lane's offset fixed for the tile and the place in the
 // sum a scalar offset, so that a stage's loads cost no vector instruction (16K tokens, the
-// plain product 1250 us with 64-bit addresses, 1090 so).
+// plain product 1250 us with 64-bit addresses, 1090 so).  A hidden size that is an odd multiple
+// of 32 takes the product before the SwiGLU here with 64-bit addresses (its kept values wait
+// behind the next tile's loads): 8,192 tokens, top-6 of 64 experts, FFN 1024, 367 us at hidden
+// 2080 against 332 at 2112.
 template <bool SWIGLU, bool WIDE>
 __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
 {
@@ -659,9 +663,10 @@ __device__ __forceinline__ void grad_rows_tiles(const GradArgs& g)
 // not depend on the tile that computes them).  The weights stream from memory, each byte for
 // at most 64 rows: three LDS stages of 64 along the sum (8 KB of rows, 32 KB of weights), two
 // of them in flight, a barrier a stage.  Measured at 1,000 tokens, top-6 of 64 experts, hidden
-// 2048, FFN 1024: 85 us before the SwiGLU, 142 after it, bound by the 1.3 GB that the latter
-// brings through the L2s (125 with the MFMAs taken out of a copy, 118 with all weights in the
-// L2s; no change with four stages or with fragments read a stage ahead).  With the
+// 2048, FFN 1024: 88 us before the SwiGLU, 138 after it, bound by the 1.43 GB that the latter
+// brings through the L2s at 10.3 TB/s, 2 of 34 stages a tile its last one again (125 with the
+// MFMAs taken out of a copy, 118 with all weights in the L2s; no change with four stages or with
+// fragments read a stage ahead).  With the
 // 256-row tiles in their place (three quarters and more of every tile empty) both products
 // took 467 us instead of 266 at 1,000 tokens on 64 experts, and 42 instead of 20 at 64 tokens.
 // take_big: this launch also takes the 256-row tiles, as four of 64 rows each.

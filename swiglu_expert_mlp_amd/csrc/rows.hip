@@ -12,8 +12,14 @@
 // Bound by memory: every row is touched once.  A thread takes 16 bytes of neighbouring
 // columns of a token's rows, with all k rows' accesses in flight at once.  Measured at 16,384
 // tokens, top-8, hidden 2048 (a large device copy runs at 5.1 TB/s, read and written): the
-// copy of dispatch 115 us (5.2 TB/s), sums of fp32 rows 206 (5.9), both gradients of bf16
-// rows 230 (5.0), x's and the probabilities' gradients of the experts 113 (5.8).
+// copy of dispatch 118 us (5.1 TB/s), sums of fp32 rows 202 to 228 a launch and 207 to 212 a
+// call (5.8), both gradients of bf16 rows 230 (5.0), x's and the probabilities' gradients of the
+// experts 115 (5.7).
+// The sums take columns of tokens as they come, so every hidden size runs at that rate (131,072
+// tokens of hidden 64, bf16: 31 us).  dispatch above 256 tokens and the gradients of combine give
+// a wave up to 64 columns of one token, so below 1 KB a row the launch is bound by its waves, not
+// by bytes: hidden 64 in bf16, 131,072 tokens, 139 us (1.2 TB/s) and 154 (1.9), hidden 128 160 and
+// 169, hidden 256 198 (3.1) and 219 (5.3); hidden 544, 49,152 tokens, 144 (3.4) and 195 (4.7).
 #include "common.h"
 #include "grad_dx.h"
 
