@@ -4,6 +4,7 @@ import torch
 
 from experts_train_ref import backward_ref
 from test_gpu_experts_train import _make, _moe, _within
+from test_gpu_experts_train import test_forward_checkpoint as check_forward_checkpoint
 
 pytestmark = pytest.mark.gpu
 NAMES = ("d_x", "d_w1", "d_w2", "d_probs")
@@ -167,3 +168,27 @@ def test_weights_gradients_past_32_bits_by_expert(H, F):
         assert o.max() <= tol, o
     for o in off(pieces(piece - 32)):                     # an oracle without the last 32 tokens is told apart
         assert o.min() > tol, o
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T", [70, 1100], ids=["64-row tiles", "256-row tiles"])
+def test_an_expert_whose_weights_pass_32_bits(T, wide):
+    """An expert's W1 of more than 2 GiB: the kept values and every gradient within the bounds of
+    fp64, where a 32-bit offset into the weights would have wrapped."""
+    E, H, F, k = 2, 32768, 16416, 1
+    assert 4 * F * H >= 1 << 31
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    check_forward_checkpoint((T, T, E, H, F, k, 0))
+    torch.cuda.empty_cache()
+    c = _make(T, T, E, H, F, k, 0, seed=68, std=0.01)
+    m = _moe(c, k)
+    args = (c["x"], c["ids"], c["probs"], c["live"])
+    _, codes, scales = m.forward_checkpoint(*args)
+    got = m.backward(c["d_out"], *args, codes, scales, grad_dtype="fp32" if wide else "bf16")
+    ref = backward_ref(c["d_out"], c["x"], c["ids"], c["probs"], T, codes, scales, c["w1"], c["w2"], wide)
+    for name, v in zip(NAMES, got):
+        value, bound = ref.pop(name)
+        for e in range(E) if value.dim() == 3 else (slice(None),):
+            _within(v[e], value[e], bound[e], name)
+        del value, bound
